@@ -425,6 +425,139 @@ spc_status spc_gather_by_voxel_id(spc_dtype dtype, const void* seg_features, int
                                   hipStream_t stream);
 
 /*
+ * ----------------------------------------------------------------------------
+ * Row operators: what a residual block puts next to the convolutions, on the
+ * same features [n, C] (channels last, C a positive multiple of 16).
+ *
+ * Samples.  seg_ptr, device int32 [n_seg + 1], ascending: sample s owns the
+ * rows [seg_ptr[s], seg_ptr[s+1]), of any length, 0 and 1 included (the rows
+ * of a strided map come out sorted by sample; searchsorted of their batch
+ * column gives seg_ptr).  Rows in no sample are neither read nor written.
+ * NULL with n_seg = 1 is one sample of all n rows.  The offsets are read on
+ * the device, each clamped to [0, n]; offsets that fall give rows of no
+ * defined value, never an access outside the arrays.
+ * Values are read and written in the call's dtype and computed in fp32, with
+ * one rounding to nearest even at the end.  Every result is run-to-run
+ * identical.  Every call is asynchronous, issues kernels only (no memset or
+ * copy, so it can be captured into a graph) and allocates nothing.
+ */
+
+#define SPC_ACT_NONE 0
+#define SPC_ACT_RELU 1   /* max(z, 0), derivative 0 at 0; NaN passes through */
+#define SPC_ACT_SILU 2   /* z * sigmoid(z)                                    */
+
+/*
+ * Dropout from a counter-based generator; no mask is stored.  Element i of a
+ * tensor (its position in memory order) takes half-word i % 8 (low half of
+ * each word first) of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011) with
+ * key = seed and counter words (lo, hi of offset + i / 8, layer, 0), and is
+ * dropped iff that 16-bit number is below thr = round(65536 p).  Kept elements
+ * are scaled by 65536 / (65536 - thr); dropped ones are 0 whatever they held.
+ * rng is read on the device, so a captured step draws new masks on every
+ * replay once its caller advances {seed, offset} there; the backward has to see
+ * the values that its forward saw.  Calls of one step take distinct `layer`s.
+ */
+typedef struct spc_dropout {
+    const uint64_t* rng;   /* device, {seed, offset}, 16-byte aligned */
+    uint32_t layer;
+    float p;               /* in [0, 1]; 1 drops everything            */
+} spc_dropout;
+
+/*
+ * out[i] = residual[i] + (kept(i) ? x[i] * scale : 0), numel elements of any
+ * count; residual NULL for none.  out may be x or residual.
+ */
+spc_status spc_dropout_fwd(spc_dtype dtype, const void* x, int64_t numel, const void* residual,
+                           const spc_dropout* drop, void* out, hipStream_t stream);
+
+/* din[i] = kept(i) ? dout[i] * scale : 0, the mask drawn again (the residual's
+ * gradient is dout itself).  din may be dout. */
+spc_status spc_dropout_bwd(spc_dtype dtype, const void* dout, int64_t numel, const spc_dropout* drop, void* din,
+                           hipStream_t stream);
+
+/* Host only.  Workspace bytes of spc_group_norm_fwd and spc_group_norm_bwd. */
+spc_status spc_group_norm_workspace(int64_t n, int32_t C, int32_t groups, int64_t n_seg, size_t* bytes);
+
+/*
+ * Group norm, activation and dropout in one call: per sample and group of
+ * C / groups channels, mean and variance (of the population) over the sample's
+ * rows and the group's channels, then
+ *   z = gamma[c] * (x - mean) * rstd + beta[c],  rstd = (var + eps)^-1/2
+ *   y = dropout(act(z))
+ * groups divides C.  gamma, beta fp32 [C] (NULL: 1 and 0); act one of
+ * SPC_ACT_*; drop NULL for none.  x, y [n, C]; y may be x.
+ * stats fp32 [n_seg, groups, 2] receives mean and rstd for the backward (an
+ * empty sample: mean 0, variance 0).  Sums are fp32 over at most 2048 rows,
+ * of differences from a row of the data, and double above that.
+ * ws: spc_group_norm_workspace bytes, scratch.
+ */
+spc_status spc_group_norm_fwd(spc_dtype dtype, const void* x, int64_t n, int32_t C, int32_t groups,
+                              const int32_t* seg_ptr, int64_t n_seg, const float* gamma, const float* beta, float eps,
+                              int32_t act, const spc_dropout* drop, void* y, float* stats, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/*
+ * Backward of spc_group_norm_fwd from its x and stats (with the same gamma,
+ * beta, act and drop): with dz = act'(z) * dropout'(dout),
+ *   dx = rstd * (gamma dz - mean_g(gamma dz) - xhat mean_g(gamma dz xhat)),
+ *   dgamma = sum dz xhat,  dbeta = sum dz  over the rows of all samples.
+ * dx [n, C] (may be dout, not x); dgamma, dbeta fp32 [C], overwritten, each
+ * NULL ok.
+ */
+spc_status spc_group_norm_bwd(spc_dtype dtype, const void* dout, const void* x, int64_t n, int32_t C, int32_t groups,
+                              const int32_t* seg_ptr, int64_t n_seg, const float* gamma, const float* beta,
+                              const float* stats, int32_t act, const spc_dropout* drop, void* dx, float* dgamma,
+                              float* dbeta, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Host only.  Workspace bytes of the recurrence calls below, and the bytes of
+ * the carry that the forward leaves for the backward. */
+spc_status spc_linear_recurrence_workspace(spc_dtype dtype, int64_t n, int32_t C, int64_t n_seg, size_t* ws,
+                                           size_t* carry);
+
+/*
+ * Gated linear recurrence along the rows of each sample, per channel:
+ *   a_t = sigmoid(gate_t),  h_t = a_t h_{t-1} + (1 - a_t) x_t,  out_t = h_t
+ * with the state in fp32.  Step t of sample s is row order[seg_ptr[s] + t]
+ * (order NULL: row seg_ptr[s] + t); reverse != 0 walks the sample from its end.
+ * order int32 [n], no row twice: a serialisation of the voxels (a space-filling
+ * curve); entries outside [0, n) are steps that leave the state as it is.
+ * gate, x: rows of C elements, ld elements apart (one product may give both
+ * side by side); ld >= C, a multiple of 16 bytes.  out [n, C] dense.
+ * h0 fp32 [n_seg, C] the states before the first rows (NULL: 0); h_last fp32
+ * [n_seg, C] (NULL ok) the ones after the last, h0 for an empty sample.
+ * carry (NULL ok): states that spc_linear_recurrence_bwd starts from,
+ * spc_linear_recurrence_workspace's bytes, of no documented layout.
+ * A NaN or infinity stays within its channel and sample.
+ */
+spc_status spc_linear_recurrence_fwd(spc_dtype dtype, const void* gate, const void* x, int64_t ld, int64_t n, int32_t C,
+                                     const int32_t* seg_ptr, int64_t n_seg, const int32_t* order, int32_t reverse,
+                                     const float* h0, void* out, float* h_last, float* carry, void* ws, size_t ws_bytes,
+                                     hipStream_t stream);
+
+/*
+ * Backward: dout [n, C], dh_last fp32 [n_seg, C] (NULL: 0), carry from the
+ * forward of the same arguments.  With D_t = dout_t + a_{t+1} D_{t+1}, D_last +=
+ * dh_last:
+ *   dx_t = (1 - a_t) D_t,  dgate_t = a_t (1 - a_t) (h_{t-1} - x_t) D_t,
+ *   dh0 = a_0 D_0  (fp32 [n_seg, C], NULL ok; dh_last for an empty sample).
+ * dgate, dx: rows ldg elements apart (as ld).  The states are computed again
+ * in fp32 from carry, gate and x; the rounded outputs are not read.
+ */
+spc_status spc_linear_recurrence_bwd(spc_dtype dtype, const void* dout, const void* gate, const void* x, int64_t ld,
+                                     int64_t n, int32_t C, const int32_t* seg_ptr, int64_t n_seg, const int32_t* order,
+                                     int32_t reverse, const float* h0, const float* carry, const float* dh_last,
+                                     void* dgate, void* dx, int64_t ldg, float* dh0, void* ws, size_t ws_bytes,
+                                     hipStream_t stream);
+
+/*
+ * One step of n running sequences: new_state = a * state + (1 - a) * x and
+ * out = new_state rounded.  state, new_state fp32 [n, C], which may be one
+ * buffer; gate, x rows ld elements apart; out [n, C] dense.
+ */
+spc_status spc_linear_recurrence_step(spc_dtype dtype, const void* gate, const void* x, int64_t ld, int64_t n, int32_t C,
+                                      const float* state, float* new_state, void* out, hipStream_t stream);
+
+/*
  * Measurement support (not part of the convolution): the dense MFMA rate of
  * this part, against which the convolutions' roofline fractions are read.
  * Launches `blocks` workgroups of 4 waves; each wave runs independent

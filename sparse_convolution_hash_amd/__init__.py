@@ -6,6 +6,7 @@ behind the C ABI of ``include/spc.h``); this package only binds it.
 
 from .binding import (  # noqa: F401
     EXPORTS,
+    Dropout,
     SpcError,
     build_kmap,
     calibrate_mfma,
@@ -15,8 +16,15 @@ from .binding import (  # noqa: F401
     conv_fwd_dev_rows,
     conv_fwd_fused,
     conv_fwd_wt,
+    dropout_bwd,
+    dropout_fwd,
     gather_by_voxel_id,
+    group_norm_bwd,
+    group_norm_fwd,
     lib,
+    linear_recurrence_bwd,
+    linear_recurrence_fwd,
+    linear_recurrence_step,
     make_geom,
     out_shape,
     strided_out_bound,

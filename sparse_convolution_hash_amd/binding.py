@@ -30,7 +30,10 @@ EXPORTS = ("spc_out_shape", "spc_kmap_workspace", "spc_build_kmap", "spc_build_k
            "spc_conv_fwd_wt", "spc_conv_fwd_dev_rows", "spc_conv_bwd_input",
            "spc_conv_bwd_filter_workspace",
            "spc_conv_bwd_filter", "spc_conv_bwd_filter_noalloc", "spc_sparse_maxpool_fwd", "spc_sparse_maxpool_bwd",
-           "spc_point_to_voxel_workspace", "spc_point_to_voxel", "spc_gather_by_voxel_id", "spc_calibrate_mfma",
+           "spc_point_to_voxel_workspace", "spc_point_to_voxel", "spc_gather_by_voxel_id", "spc_dropout_fwd",
+           "spc_dropout_bwd", "spc_group_norm_workspace", "spc_group_norm_fwd", "spc_group_norm_bwd",
+           "spc_linear_recurrence_workspace", "spc_linear_recurrence_fwd", "spc_linear_recurrence_bwd",
+           "spc_linear_recurrence_step", "spc_calibrate_mfma",
            "spc_last_error", "spc_version")
 
 
@@ -44,6 +47,10 @@ class Geom(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("shape", ctypes.c_int32 * 3), ("ksize", ctypes.c_int32 * 3),
                 ("stride", ctypes.c_int32 * 3), ("pad", ctypes.c_int32 * 3), ("dil", ctypes.c_int32 * 3),
                 ("subm", ctypes.c_int32), ("table", ctypes.c_int32)]
+
+
+class _DropArg(ctypes.Structure):
+    _fields_ = [("rng", ctypes.c_void_p), ("layer", ctypes.c_uint32), ("p", ctypes.c_float)]
 
 
 TABLES = {"hash": 0, "grid": 1}   # SPC_TABLE_HASH, SPC_TABLE_GRID
@@ -77,7 +84,7 @@ def lib() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m sparse_convolution_hash_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
-    GP = ctypes.POINTER(Geom)
+    GP, DP = ctypes.POINTER(Geom), ctypes.POINTER(_DropArg)
     sig = {
         "spc_out_shape": [GP, ctypes.POINTER(_I32)],
         "spc_kmap_workspace": [GP, _I64, ctypes.POINTER(_SZ)],
@@ -102,6 +109,17 @@ def lib() -> ctypes.CDLL:
         "spc_point_to_voxel": [_P, _I64, _I32, _P, _P, _I64, _I32, _I32, _P, _P, _P, _P,
                                ctypes.POINTER(ctypes.c_int64), _P, _SZ, _P],
         "spc_gather_by_voxel_id": [_I32, _P, _I64, _I32, _P, _I64, _P, _P],
+        "spc_dropout_fwd": [_I32, _P, _I64, _P, DP, _P, _P],
+        "spc_dropout_bwd": [_I32, _P, _I64, DP, _P, _P],
+        "spc_group_norm_workspace": [_I64, _I32, _I32, _I64, ctypes.POINTER(_SZ)],
+        "spc_group_norm_fwd": [_I32, _P, _I64, _I32, _I32, _P, _I64, _P, _P, ctypes.c_float, _I32, DP, _P, _P, _P, _SZ,
+                               _P],
+        "spc_group_norm_bwd": [_I32, _P, _P, _I64, _I32, _I32, _P, _I64, _P, _P, _P, _I32, DP, _P, _P, _P, _P, _SZ, _P],
+        "spc_linear_recurrence_workspace": [_I32, _I64, _I32, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
+        "spc_linear_recurrence_fwd": [_I32, _P, _P, _I64, _I64, _I32, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P],
+        "spc_linear_recurrence_bwd": [_I32, _P, _P, _P, _I64, _I64, _I32, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _I64,
+                                      _P, _P, _SZ, _P],
+        "spc_linear_recurrence_step": [_I32, _P, _P, _I64, _I64, _I32, _P, _P, _P, _P],
         "spc_calibrate_mfma": [_I32, _I32, _I32, _P, ctypes.POINTER(ctypes.c_double), _P],
     }
     for name, args in sig.items():
@@ -652,6 +670,289 @@ def gather_by_voxel_id(seg_features: torch.Tensor, pc_voxel_id: torch.Tensor,
     st = lib().spc_gather_by_voxel_id(_DTYPES[seg_features.dtype], _ptr(seg_features), seg_features.shape[0], C,
                                       _ptr(pc_voxel_id), pc_voxel_id.shape[0], _ptr(out), _stream(dev))
     _check(st, "spc_gather_by_voxel_id")
+    return out
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2}   # SPC_ACT_*
+
+
+class Dropout:
+    """Dropout of one call (spc_dropout): ``rng`` int64 [2] on the GPU holds
+    {seed, offset}, ``p`` the probability, ``layer`` tells the calls of one
+    step apart.  The mask is a function of these alone and is drawn again by
+    the backward; advance ``rng`` on the device between steps."""
+
+    def __init__(self, rng: torch.Tensor, p: float, layer: int = 0):
+        _need(rng, "rng", torch.int64)
+        if tuple(rng.shape) != (2,):
+            raise ValueError(f"rng must be [2] {{seed, offset}}, got {tuple(rng.shape)}")
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p={p} is outside [0, 1]")
+        if not 0 <= layer < 1 << 32:
+            raise ValueError(f"layer={layer} is not a 32-bit number")
+        self.rng, self.p, self.layer = rng, float(p), int(layer)
+        self._arg = _DropArg(rng.data_ptr(), self.layer, self.p)
+
+
+def _drop_arg(dropout, dev):
+    if dropout is None:
+        return None
+    if not isinstance(dropout, Dropout):
+        raise TypeError("dropout must be a Dropout")
+    if dropout.rng.device != dev:
+        raise ValueError(f"rng is on {dropout.rng.device}, expected {dev}")
+    return ctypes.byref(dropout._arg)
+
+
+def _need_like(t, name, dtype, dev, shape):
+    _need(t, name, dtype, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+
+
+def _rows_checks(x, name="input"):
+    _need(x, name)
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [N, C]")
+
+
+def _n_seg(seg_ptr, dev) -> int:
+    if seg_ptr is None:
+        return 1
+    _need(seg_ptr, "seg_ptr", torch.int32, dev)
+    if seg_ptr.dim() != 1 or seg_ptr.numel() < 2:
+        raise ValueError("seg_ptr must be [n_seg + 1]")
+    return seg_ptr.numel() - 1
+
+
+def dropout_fwd(x: torch.Tensor, dropout: Dropout, residual: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + dropout(x), any shape (spc_dropout_fwd); ``out`` may be x or
+    residual."""
+    _need(x, "input")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    dev = x.device
+    if dropout is None:
+        raise TypeError("dropout must be a Dropout")
+    if residual is not None:
+        _need_like(residual, "residual", x.dtype, dev, x.shape)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need_like(out, "out", x.dtype, dev, x.shape)
+    st = lib().spc_dropout_fwd(_DTYPES[x.dtype], _ptr(x), x.numel(), _ptr(residual), _drop_arg(dropout, dev), _ptr(out),
+                               _stream(dev))
+    _check(st, "spc_dropout_fwd")
+    return out
+
+
+def dropout_bwd(dout: torch.Tensor, dropout: Dropout, din: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of dropout_fwd's x (spc_dropout_bwd): the same mask, drawn
+    again.  ``din`` may be dout."""
+    _need(dout, "dout")
+    if dout.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dout.dtype}")
+    dev = dout.device
+    if dropout is None:
+        raise TypeError("dropout must be a Dropout")
+    if din is None:
+        din = torch.empty_like(dout)
+    else:
+        _need_like(din, "din", dout.dtype, dev, dout.shape)
+    st = lib().spc_dropout_bwd(_DTYPES[dout.dtype], _ptr(dout), dout.numel(), _drop_arg(dropout, dev), _ptr(din),
+                               _stream(dev))
+    _check(st, "spc_dropout_bwd")
+    return din
+
+
+@functools.lru_cache(maxsize=256)
+def group_norm_workspace(n: int, C: int, groups: int, n_seg: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().spc_group_norm_workspace(n, C, groups, n_seg, ctypes.byref(b)), "spc_group_norm_workspace")
+    return b.value
+
+
+def _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace):
+    _rows_checks(x)
+    dev, (n, C) = x.device, x.shape
+    n_seg = _n_seg(seg_ptr, dev)
+    for t, nm in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _need_like(t, nm, torch.float32, dev, (C,))
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, got {act!r}")
+    need = group_norm_workspace(n, C, int(groups), n_seg)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    return dev, n, C, n_seg, workspace
+
+
+def group_norm_fwd(x: torch.Tensor, groups: int, seg_ptr: Optional[torch.Tensor] = None,
+                   gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   act: str = "none", dropout: Optional[Dropout] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """dropout(act(group norm of x [N, C])) over the samples of seg_ptr int32
+    [S + 1] (None: one sample) (spc_group_norm_fwd).  gamma, beta fp32 [C].
+    Returns ``(y, stats fp32 [S, groups, 2])``, stats for group_norm_bwd;
+    ``out`` may be x."""
+    dev, n, C, n_seg, workspace = _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need_like(out, "out", x.dtype, dev, x.shape)
+    stats = torch.empty((n_seg, groups, 2), dtype=torch.float32, device=dev)
+    st = lib().spc_group_norm_fwd(_DTYPES[x.dtype], _ptr(x), n, C, int(groups), _ptr(seg_ptr), n_seg, _ptr(gamma),
+                                  _ptr(beta), eps, ACTIVATIONS[act], _drop_arg(dropout, dev), _ptr(out), _ptr(stats),
+                                  _ptr(workspace), workspace.numel(), _stream(dev))
+    _check(st, "spc_group_norm_fwd")
+    return out, stats
+
+
+def group_norm_bwd(dout: torch.Tensor, x: torch.Tensor, groups: int, seg_ptr: Optional[torch.Tensor],
+                   gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], stats: torch.Tensor,
+                   act: str = "none", dropout: Optional[Dropout] = None, want_affine: bool = True,
+                   dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of group_norm_fwd (spc_group_norm_bwd) from its x and stats:
+    ``(dx, dgamma, dbeta)``, the last two fp32 [C] or None; ``dx`` may be dout."""
+    dev, n, C, n_seg, workspace = _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace)
+    _need_like(dout, "dout", x.dtype, dev, x.shape)
+    _need_like(stats, "stats", torch.float32, dev, (n_seg, groups, 2))
+    if dx is None:
+        dx = torch.empty_like(x)
+    else:
+        _need_like(dx, "dx", x.dtype, dev, x.shape)
+    dgamma = dbeta = None
+    if want_affine:
+        dgamma = torch.empty(C, dtype=torch.float32, device=dev)
+        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
+    st = lib().spc_group_norm_bwd(_DTYPES[x.dtype], _ptr(dout), _ptr(x), n, C, int(groups), _ptr(seg_ptr), n_seg,
+                                  _ptr(gamma), _ptr(beta), _ptr(stats), ACTIVATIONS[act], _drop_arg(dropout, dev),
+                                  _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(),
+                                  _stream(dev))
+    _check(st, "spc_group_norm_bwd")
+    return dx, dgamma, dbeta
+
+
+@functools.lru_cache(maxsize=256)
+def linear_recurrence_workspace(dtype: torch.dtype, n: int, C: int, n_seg: int) -> tuple:
+    """(workspace bytes, carry bytes) of the recurrence calls."""
+    w, c = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().spc_linear_recurrence_workspace(_DTYPES[dtype], n, C, n_seg, ctypes.byref(w), ctypes.byref(c)),
+           "spc_linear_recurrence_workspace")
+    return w.value, c.value
+
+
+def _gate_x(gate, x, names=("gate", "x")):
+    """Checks a pair of [N, C] row views (which may be column slices of one
+    tensor) and returns their common row stride."""
+    for t, nm in ((gate, names[0]), (x, names[1])):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{nm} must be a CUDA (HIP) tensor")
+        if t.dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        if t.dim() != 2:
+            raise ValueError(f"{nm} must be [N, C]")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{nm}'s channels must be contiguous")
+    if gate.dtype != x.dtype or gate.shape != x.shape or gate.device != x.device:
+        raise ValueError(f"{names[0]} and {names[1]} must agree in dtype, shape and device")
+    if x.shape[0] <= 1:
+        return x.shape[1]
+    if gate.stride(0) != x.stride(0):
+        raise ValueError(f"{names[0]} and {names[1]} must have one row stride")
+    return x.stride(0)
+
+
+def _lr_checks(gate, x, seg_ptr, h0, order, workspace):
+    ld = _gate_x(gate, x)
+    dev, (n, C) = x.device, x.shape
+    n_seg = _n_seg(seg_ptr, dev)
+    if h0 is not None:
+        _need_like(h0, "h0", torch.float32, dev, (n_seg, C))
+    if order is not None:
+        _need_like(order, "order", torch.int32, dev, (n,))
+    ws, carry = linear_recurrence_workspace(x.dtype, n, C, n_seg)
+    if workspace is None or workspace.numel() < ws:
+        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+    return dev, n, C, n_seg, ld, workspace, carry
+
+
+def linear_recurrence_fwd(gate: torch.Tensor, x: torch.Tensor, seg_ptr: Optional[torch.Tensor] = None,
+                          h0: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None,
+                          reverse: bool = False, want_carry: bool = False, out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None):
+    """h_t = sigmoid(gate_t) h_{t-1} + sigmoid(-gate_t) x_t along the rows of
+    each sample (spc_linear_recurrence_fwd): gate, x [N, C], or column slices
+    of one wider tensor; h0 fp32 [S, C].  Returns ``(out [N, C], h_last fp32
+    [S, C], carry or None)``; carry is for linear_recurrence_bwd."""
+    dev, n, C, n_seg, ld, workspace, carry_bytes = _lr_checks(gate, x, seg_ptr, h0, order, workspace)
+    if out is None:
+        out = torch.empty((n, C), dtype=x.dtype, device=dev)
+    else:
+        _need_like(out, "out", x.dtype, dev, (n, C))
+    h_last = torch.empty((n_seg, C), dtype=torch.float32, device=dev)
+    carry = torch.empty(max(carry_bytes // 4, 4), dtype=torch.float32, device=dev) if want_carry else None
+    st = lib().spc_linear_recurrence_fwd(_DTYPES[x.dtype], _ptr(gate), _ptr(x), ld, n, C, _ptr(seg_ptr), n_seg,
+                                         _ptr(order), 1 if reverse else 0, _ptr(h0), _ptr(out), _ptr(h_last),
+                                         _ptr(carry), _ptr(workspace), workspace.numel(), _stream(dev))
+    _check(st, "spc_linear_recurrence_fwd")
+    return out, h_last, carry
+
+
+def linear_recurrence_bwd(dout: torch.Tensor, gate: torch.Tensor, x: torch.Tensor, seg_ptr: Optional[torch.Tensor],
+                          carry: torch.Tensor, h0: Optional[torch.Tensor] = None,
+                          dh_last: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None,
+                          reverse: bool = False, want_dh0: bool = False, dgate: Optional[torch.Tensor] = None,
+                          dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of linear_recurrence_fwd (spc_linear_recurrence_bwd) from its
+    arguments and carry: ``(dgate [N, C], dx [N, C], dh0 fp32 [S, C] or None)``.
+    ``dgate`` and ``dx`` may be given as column slices of one tensor."""
+    dev, n, C, n_seg, ld, workspace, carry_bytes = _lr_checks(gate, x, seg_ptr, h0, order, workspace)
+    _need_like(dout, "dout", x.dtype, dev, (n, C))
+    _need_like(carry, "carry", torch.float32, dev, (max(carry_bytes // 4, 4),))
+    if dh_last is not None:
+        _need_like(dh_last, "dh_last", torch.float32, dev, (n_seg, C))
+    if (dgate is None) != (dx is None):
+        raise ValueError("dgate and dx: give both or neither")
+    if dgate is None:
+        dgate = torch.empty((n, C), dtype=x.dtype, device=dev)
+        dx = torch.empty((n, C), dtype=x.dtype, device=dev)
+        ldg = C
+    else:
+        ldg = _gate_x(dgate, dx, ("dgate", "dx"))
+        if dx.dtype != x.dtype or dx.shape != x.shape or dx.device != dev:
+            raise ValueError("dgate and dx must agree with x in dtype, shape and device")
+    dh0 = torch.empty((n_seg, C), dtype=torch.float32, device=dev) if want_dh0 else None
+    st = lib().spc_linear_recurrence_bwd(_DTYPES[x.dtype], _ptr(dout), _ptr(gate), _ptr(x), ld, n, C, _ptr(seg_ptr),
+                                         n_seg, _ptr(order), 1 if reverse else 0, _ptr(h0), _ptr(carry), _ptr(dh_last),
+                                         _ptr(dgate), _ptr(dx), ldg, _ptr(dh0), _ptr(workspace), workspace.numel(),
+                                         _stream(dev))
+    _check(st, "spc_linear_recurrence_bwd")
+    return dgate, dx, dh0
+
+
+def linear_recurrence_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor,
+                           new_state: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One step of N running sequences (spc_linear_recurrence_step): state
+    fp32 [N, C] is replaced in place, or left and the new one written to
+    ``new_state``; returns the new state in gate's dtype."""
+    ld = _gate_x(gate, x)
+    dev, (n, C) = x.device, x.shape
+    _need_like(state, "state", torch.float32, dev, (n, C))
+    if new_state is None:
+        new_state = state
+    else:
+        _need_like(new_state, "new_state", torch.float32, dev, (n, C))
+    if out is None:
+        out = torch.empty((n, C), dtype=x.dtype, device=dev)
+    else:
+        _need_like(out, "out", x.dtype, dev, (n, C))
+    st = lib().spc_linear_recurrence_step(_DTYPES[x.dtype], _ptr(gate), _ptr(x), ld, n, C, _ptr(state), _ptr(new_state),
+                                          _ptr(out), _stream(dev))
+    _check(st, "spc_linear_recurrence_step")
     return out
 
 
