@@ -11,45 +11,40 @@
 // whatever the lengths.  Backward, with E_t = a_t D_t, the map is
 // E -> a_t (dh_t + E), over the rows in the opposite order.
 //
-// One pass over the data.  A thread holds a chunk of T rows x 4 channels in
-// registers and folds them to one map per channel; the chunks of a workgroup
-// (its tile) are folded in LDS; tiles are joined across workgroups by
-// look-back over published maps, in a tree of radix 16: word i of level l is
-// the map of tiles [i 16^l, (i + 1) 16^l), and a tile folds at most 15 words a
-// level.  The tree is fixed by the tile numbers, so the result does not depend
-// on timing.  A word is one 64-bit atomic (A, B) and is its own flag: all ones
-// (a NaN that is never published as A) until written.
-// Waits end: tiles are numbered by a ticket taken when a workgroup starts, a
-// tile waits only for lower tickets, and those have started.
+// A thread walks a strip of L rows x 4 channels.  Launches: the strips' maps,
+// folded within each workgroup's tile of strips (k_lr_reduce_*); the tiles'
+// maps to the states they start from (k_lr_tiles); the walk again from its
+// start state, with the outputs (k_lr_apply_*).  Up to FEW tiles the walk folds
+// the tiles before its own itself, and a single tile takes one launch.  The
+// order of all folds is fixed by the sizes, so results do not depend on timing.
 #include "rows.h"
 
 namespace spc {
 namespace {
 
-constexpr int NT = 256;     // threads per workgroup
-constexpr int QPR = 16;     // most lanes (of 4 channels) per row: slabs of up to 64 channels
-constexpr int RADIX = 16;   // tiles per group of the look-back tree
+constexpr int NT = 256;      // threads per workgroup
+constexpr int QPR = 16;      // most lanes (of 4 channels) per row: slabs of up to 64 channels
+constexpr int T = 8;         // rows loaded at a time
+constexpr int LMAX = 32;     // most rows of a strip
+constexpr int RMAX = NT / 4 * LMAX;   // most rows of a tile
+constexpr int FEW = 16;
 
-// Rows per chunk: 16-bit types hold twice the rows in the same registers.
-template <typename TT>
-struct ChunkRows {
-    static constexpr int T = TT::E == 8 ? 16 : 8;
-};
-inline int chunk_rows(spc_dtype t) { return t == SPC_F32 ? 8 : 16; }
-
-// How [n, C] is cut: slabs of CW channels, CPR lanes to a row, NCH chunks to a tile.
+// How [n, C] is cut: slabs of CW channels, CPR lanes to a row, NCH strips of L rows to a tile.
 struct Cut {
-    int32_t nslab, CPR, CW, NCH, rows;
+    int32_t nslab, CPR, CW, NCH, L, rows;
     int32_t tiles;
 };
 
-inline Cut cut_of(spc_dtype dtype, int64_t n, int32_t C) {
+inline Cut cut_of(int64_t n, int32_t C) {
     Cut k;
     k.nslab = int32_t(ceil_div(C / 4, QPR));
     k.CPR = int32_t(ceil_div(C / 4, k.nslab));
     k.CW = 4 * k.CPR;
     k.NCH = NT / k.CPR;
-    k.rows = k.NCH * chunk_rows(dtype);
+    // the longest strips that still leave 6 waves to each SIMD
+    k.L = T;
+    while (k.L < LMAX && n * (C / 4) / (2 * k.L) >= 6 * 1024 * WAVE) k.L *= 2;
+    k.rows = k.NCH * k.L;
     k.tiles = int32_t(ceil_div(n, k.rows));
     return k;
 }
@@ -61,11 +56,15 @@ struct LrArgs {
     int64_t ldg;
     const int32_t* order;   // row of each position, NULL: the identity
     Cut k;
-    uint32_t* ticket;       // NULL with one tile
-    uint64_t* words;
+    float2* strip;          // [tile * NCH + strip][C]: map of the strips before it in its tile
+    float2* tile;           // [tile][C]: its map
+    float* start;           // [tile][C]: the state it starts from (more than FEW tiles)
 };
 
 // ---------------------------------------------------------------- elements
+
+// The compiler takes v for a new value from here on.
+__device__ __forceinline__ void hide(float& v) { asm volatile("" : "+v"(v)); }
 
 // Four channels as stored.
 template <typename TT>
@@ -124,6 +123,18 @@ __device__ __forceinline__ void gates(float g, float& a, float& na) {
     a = g >= 0.f ? big : small;
     na = g >= 0.f ? small : big;
 }
+// Both from the smaller one with the gate's sign, which is what a chunk keeps
+// of its gates: half the registers of the two, and no second exp and rcp.
+__device__ __forceinline__ float keep(float g) {
+    float big;
+    return __builtin_copysignf(gate_small(g, big), g);
+}
+__device__ __forceinline__ void gates_of(float kept, float& a, float& na) {
+    const float small = fabsf(kept), big = 1.f - small;
+    const bool neg = __float_as_int(kept) < 0;
+    a = neg ? small : big;
+    na = neg ? big : small;
+}
 
 // -------------------------------------------------------------------- maps
 
@@ -139,117 +150,61 @@ __device__ __forceinline__ Map after(const Map& s, const Map& f) {
 }
 __device__ __forceinline__ float apply(const Map& m, float h) { return is_reset(m.A) ? m.B : fmaf(m.A, h, m.B); }
 
-constexpr uint64_t EMPTY = ~uint64_t(0);
-__device__ __forceinline__ void publish(uint64_t* p, Map m) {
-    if (m.A != m.A) m.A = __uint_as_float(0x7fc00000u);
-    __hip_atomic_store(p, uint64_t(__float_as_uint(m.A)) | uint64_t(__float_as_uint(m.B)) << 32, __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ bool there(uint64_t w) { return uint32_t(w) != 0xffffffffu; }
-
-// A wait that has lasted this many polls (a good part of a second) can only mean a workspace
-// that another call is using at the same time: the missing maps become NaN
-// and the kernel ends.
-constexpr int MAX_POLLS = 1 << 18;
-
-// The map of all tiles before tile t, whose own map is own, for the channel of
-// this lane; called by one wave (lanes from CW on take part in its votes only).
-__device__ __forceinline__ Map look_back(const LrArgs& p, int t, int slab, int c, bool on, Map own) {
-    const Cut& k = p.k;
-    const int64_t stride = int64_t(k.nslab) * k.CW;
-    uint64_t* w = p.words + int64_t(slab) * k.CW + c;
-    Map before{1.f, 0.f}, all = own;
-    if (on) publish(w + t * stride, own);
-    bool full = true;
-    for (int i = t, count = k.tiles;;) {
-        const int m = i % RADIX;
-        if (!__all(!on || is_reset(before.A))) {
-            const uint64_t* q = w + (i - m) * stride;
-            uint64_t v[RADIX - 1];
-            for (int polls = 0;; ++polls) {
-                bool ready = true;
-#pragma unroll
-                for (int j = 0; j < RADIX - 1; ++j) v[j] = j < m && on ? peek(q + j * stride) : 0;
-#pragma unroll
-                for (int j = 0; j < RADIX - 1; ++j) ready = ready && there(v[j]);
-                if (__all(ready) || polls == MAX_POLLS) break;
-                __builtin_amdgcn_s_sleep(1);
-            }
-            Map f{1.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < RADIX - 1; ++j)
-                if (j < m) f = after(Map{__uint_as_float(uint32_t(v[j])), __uint_as_float(uint32_t(v[j] >> 32))}, f);
-            before = after(before, f);
-            all = after(all, f);
-        }
-        w += count * stride;
-        full = full && m == RADIX - 1;
-        i /= RADIX;
-        count /= RADIX;
-        if (full && on && i < count) publish(w + i * stride, all);
-        if (i == 0 || (!full && __all(!on || is_reset(before.A)))) return before;
-    }
-}
-
-// Words of the look-back tree.
-inline int64_t tree_words(const Cut& k) {
-    int64_t w = 0;
-    for (int64_t c = k.tiles; c > 0; c /= RADIX) w += c;
-    return w * k.nslab * k.CW;
-}
-
 // ------------------------------------------------------------------- tiles
 
 // What a workgroup shares.
 struct Shared {
-    float2 map[NT * 4];       // [chunk][channel]: a chunk's map
-    float2 part[NT];          // [part][channel]: the map of a part's chunks
-    float in[NT * 4];         // [chunk][channel]: the state a chunk starts from
-    int32_t sample[NT * 4];   // of a marked row (NT / 4 chunks at most, of 16 rows)
-    uint32_t first[NT / 8], last[NT / 8];   // marks: a sample's first and last row
-    int32_t tile;
+    float2 map[NT * 4];       // [strip][channel]
+    float2 part[NT];          // [part][channel]: the map of a part's strips
+    int32_t sample[RMAX];     // of a marked row
+    uint32_t first[RMAX / 32], last[RMAX / 32];   // marks: a sample's first and last row
 };
 
-// Takes the next tile; returns tile and slab (slabs of one tile are neighbours).
-__device__ __forceinline__ void take(const LrArgs& p, Shared& sh, int& tile, int& slab) {
-    int id = blockIdx.x;
-    if (p.ticket) {
-        if (threadIdx.x == 0) sh.tile = int(atomicAdd(p.ticket, 1u));
-        __syncthreads();
-        id = sh.tile;
+// The samples around a tile, read once: lane i of every wave holds the offset
+// of sample s0 + i.  With up to 63 samples that is all of them and takes one
+// load, whose latency the tile's own loads hide.
+struct Window {
+    int s0, off, lo, hi;   // positions [lo, hi) of the walk lie in samples
+};
+
+// Positions of a tile, in the walk [f0, f1) and among the samples [qa, qb).
+struct Span {
+    int p0, f0, f1, qa, qb;
+    __device__ __forceinline__ Span(const LrArgs& p, int tile) {
+        const int n = p.segs.n;
+        f0 = p0 = tile * p.k.rows;
+        f1 = p.k.rows < n - p0 ? p0 + p.k.rows : n;
+        qa = p.reverse ? n - f1 : f0;
+        qb = p.reverse ? n - f0 : f1;
     }
-    tile = id / p.k.nslab;
-    slab = id - tile * p.k.nslab;
+};
+
+__device__ __forceinline__ Window open_window(const LrArgs& p, const Span& r) {
+    const Segs& g = p.segs;
+    Window w;
+    w.s0 = g.n_seg < WAVE ? 0 : g.find(r.qa);
+    const int s = w.s0 + int(threadIdx.x) % WAVE;
+    w.off = g.at(s < g.n_seg ? s : g.n_seg);
+    const int a = g.at(0), b = g.at(g.n_seg);
+    w.lo = p.reverse ? g.n - b : a;
+    w.hi = p.reverse ? g.n - a : b;
+    return w;
 }
 
-// Marks the first and last rows of the samples that lie in positions
-// [p0, p0 + rows) of the walk, and leaves the rows' own numbers in rowno
-// (ORDERED: -1 where there is none).
-template <bool ORDERED>
-__device__ __forceinline__ void mark(const LrArgs& p, Shared& sh, int32_t* rowno, int p0) {
+// Marks the first and last rows of the samples that lie in the tile; returns
+// false, and leaves the marks alone, if there are none.
+__device__ __forceinline__ bool mark(const LrArgs& p, Shared& sh, const Span& r, const Window& w) {
     const int n = p.segs.n, rows = p.k.rows;
-    if (threadIdx.x < NT / 8) sh.first[threadIdx.x] = sh.last[threadIdx.x] = 0;
-    const int f0 = p0 > 0 ? p0 : 0, f1 = p0 + rows < n ? p0 + rows : n;      // within the walk
-    const int qa = p.reverse ? n - f1 : f0, qb = p.reverse ? n - f0 : f1;    // as positions of the samples
-    if constexpr (ORDERED) {
-        const int lo = p.segs.at(0), hi = p.segs.at(p.segs.n_seg);
-        for (int i = threadIdx.x; i < rows; i += NT) {
-            const int f = p0 + i, q = p.reverse ? n - 1 - f : f;
-            int r = -1;
-            if (q >= qa && q < qb && q >= lo && q < hi) r = p.order[q];
-            rowno[i] = unsigned(r) < unsigned(n) ? r : -1;
-        }
-    }
-    const int s0 = p.segs.find(qa);
+    // a sample's first or last row is in the tile only if an offset is in [qa, qb]
+    const bool past = __any(w.off >= r.qb || w.s0 + int(threadIdx.x) % WAVE >= p.segs.n_seg);
+    if (past && !__any(w.off >= r.qa && w.off <= r.qb)) return false;
+    for (int i = threadIdx.x; i * 32 < rows; i += NT) sh.first[i] = sh.last[i] = 0;
     __syncthreads();
-    for (int s = s0 + int(threadIdx.x); s < p.segs.n_seg; s += NT) {
+    for (int s = w.s0 + int(threadIdx.x); s < p.segs.n_seg; s += NT) {
         const int a = p.segs.at(s), b = p.segs.at(s + 1);
-        if (a >= qb) break;
+        if (a >= r.qb) break;
         if (a >= b) continue;
-        const int i0 = (p.reverse ? n - b : a) - p0, i1 = (p.reverse ? n - 1 - a : b - 1) - p0;
+        const int i0 = (p.reverse ? n - b : a) - r.p0, i1 = (p.reverse ? n - 1 - a : b - 1) - r.p0;
         if (unsigned(i0) < unsigned(rows)) {
             sh.sample[i0] = s;
             atomicOr(&sh.first[i0 / 32], 1u << (i0 % 32));
@@ -260,343 +215,397 @@ __device__ __forceinline__ void mark(const LrArgs& p, Shared& sh, int32_t* rowno
         }
     }
     __syncthreads();
+    return true;
 }
 
-// The state that each chunk starts from, given the chunks' maps in sh.map in
-// the order of the walk.  All threads call it.
-__device__ __forceinline__ void join(const LrArgs& p, Shared& sh, int tile, int slab) {
+// A thread's strip.
+struct Strip {
+    int ch;      // number within the tile, in the order of the scan
+    int i0;      // its first row within the tile
+    int pos;     // position in the walk of its first row
+    int c;       // first channel
+    int at;      // of its channels in [strip][channel]
+    bool on;     // has rows and channels
+    __device__ __forceinline__ Strip(const LrArgs& p, const Span& r, int slab, bool back) {
+        const int CPR = p.k.CPR;
+        ch = int(threadIdx.x) / CPR;
+        const int quad = int(threadIdx.x) - ch * CPR;
+        c = (slab * CPR + quad) * 4;
+        at = ch * p.k.CW + quad * 4;
+        i0 = (back ? p.k.NCH - 1 - ch : ch) * p.k.L;
+        pos = r.p0 + i0;
+        on = ch < p.k.NCH && c < p.C && pos < p.segs.n;
+    }
+};
+
+// T rows of a strip: their numbers (-1 where there is none) and marks.
+template <bool ORDERED>
+struct Rows {
+    int r[T];
+    uint32_t first, last;
+    bool simple;     // no marks and all rows, for the whole wave
+    __device__ __forceinline__ void numbers(const LrArgs& p, const Window& w, int pos) {
+        const int n = p.segs.n;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int f = pos + t, q = p.reverse ? n - 1 - f : f;
+            r[t] = f >= w.lo && f < w.hi ? (ORDERED ? p.order[q] : q) : -1;
+        }
+        if constexpr (ORDERED)
+#pragma unroll
+            for (int t = 0; t < T; ++t) r[t] = unsigned(r[t]) < unsigned(n) ? r[t] : -1;
+    }
+    __device__ __forceinline__ void marks(const Shared& sh, bool marked, int i) {
+        first = marked ? sh.first[i / 32] >> (i % 32) & ((1u << T) - 1) : 0;
+        last = marked ? sh.last[i / 32] >> (i % 32) & ((1u << T) - 1) : 0;
+        bool all = !(first | last);
+#pragma unroll
+        for (int t = 0; t < T; ++t) all = all && r[t] >= 0;
+        simple = __all(all);
+    }
+    // A row to load for step t: its own, or any if it has none.
+    __device__ __forceinline__ int64_t any(int t) const { return r[t] < 0 ? 0 : r[t]; }
+};
+
+__device__ __forceinline__ f32x4_t ld4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
+__device__ __forceinline__ void st4(float* p, const f32x4_t& v) { *reinterpret_cast<f32x4_t*>(p) = v; }
+
+// A marked row's sample's state in an optional array [n_seg, C].
+__device__ __forceinline__ f32x4_t state_of(const float* a, const LrArgs& p, const Shared& sh, int i, int c) {
+    return a ? ld4(a + int64_t(sh.sample[i]) * p.C + c) : f32x4_t{0, 0, 0, 0};
+}
+
+// T rows of gate and x, or (BACK) of gate and dout.
+template <typename TT, bool ORDERED>
+struct Pair {
+    Rows<ORDERED> rows;
+    Raw4<TT> g[T], x[T];
+    __device__ __forceinline__ void load(const LrArgs& p, const Window& w, const void* gate, const void* v, int64_t ldv, int pos, int c) {
+        using S = typename TT::storage;
+        rows.numbers(p, w, pos);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            g[t] = ldr<TT>(static_cast<const S*>(gate) + rows.any(t) * p.ld + c);
+            x[t] = ldr<TT>(static_cast<const S*>(v) + rows.any(t) * ldv + c);
+        }
+    }
+};
+
+// The map of a strip.  from: h0, or dh_last.
+template <typename TT, bool ORDERED, bool BACK>
+__device__ __forceinline__ void reduce(const void* gate, const void* v, const float* from, const LrArgs& p, const Shared& sh,
+                                       const Window& w, bool marked, const Strip& k, f32x4_t& A, f32x4_t& B) {
+    A = 1.f, B = 0.f;
+    if (!k.on) return;
+    for (int o = 0; o < p.k.L; o += T) {
+        const int i = BACK ? p.k.L - T - o : o;
+        Pair<TT, ORDERED> b;
+        b.load(p, w, gate, v, BACK ? p.C : p.ld, k.pos + i, k.c);
+        b.rows.marks(sh, marked, k.i0 + i);
+        const auto step = [&](int t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a, na;
+                gates(elem<TT>(b.g[t], j), a, na);
+                A[j] *= a;
+                B[j] = BACK ? a * (elem<TT>(b.x[t], j) + B[j]) : fmaf(a, B[j], na * elem<TT>(b.x[t], j));
+            }
+        };
+        if (b.rows.simple) {
+#pragma unroll
+            for (int t = 0; t < T; ++t) step(BACK ? T - 1 - t : t);
+        } else {
+#pragma unroll
+            for (int u = 0; u < T; ++u) {
+                const int t = BACK ? T - 1 - u : u;
+                if ((BACK ? b.rows.last : b.rows.first) >> t & 1) A = -0.f, B = state_of(from, p, sh, k.i0 + i + t, k.c);
+                if (b.rows.r[t] >= 0) step(t);
+            }
+        }
+    }
+}
+
+// Joins the strips' maps of a workgroup in the order of the scan: the map of
+// those before each strip goes to out(strip, channel, map), that of all of
+// them to all(channel, map).
+template <typename F, typename G>
+__device__ __forceinline__ void join(const LrArgs& p, Shared& sh, const Strip& k, const f32x4_t& A, const f32x4_t& B, F out, G all) {
     const int CW = p.k.CW, NCH = p.k.NCH, parts = NT / CW;
-    const int per = (NCH + parts - 1) / parts;   // 4 or 5 chunks
+    const int per = (NCH + parts - 1) / parts;   // 4 or 5 strips
     const int part = int(threadIdx.x) / CW, c = int(threadIdx.x) - part * CW;
     const int k0 = part * per, k1 = part < parts ? (k0 + per < NCH ? k0 + per : NCH) : 0;
+    if (k.ch < NCH) {   // a strip without rows: the identity
+        f32x4_t* q = reinterpret_cast<f32x4_t*>(&sh.map[k.at]);
+        q[0] = f32x4_t{A[0], B[0], A[1], B[1]};
+        q[1] = f32x4_t{A[2], B[2], A[3], B[3]};
+    }
     __syncthreads();
     Map m{1.f, 0.f};
-    for (int k = k0; k < k1; ++k) {
-        const float2 v = sh.map[k * CW + c];
+    for (int i = k0; i < k1; ++i) {
+        const float2 v = sh.map[i * CW + c];
         m = after(Map{v.x, v.y}, m);
     }
     if (part < parts) sh.part[part * CW + c] = float2{m.A, m.B};
     __syncthreads();
-    if (threadIdx.x < WAVE) {
-        const bool on = int(threadIdx.x) < CW;
-        float h = 0.f;
-        if (p.ticket) {
-            Map own{1.f, 0.f};
-            if (on)
-                for (int i = 0; i < parts; ++i) {
-                    const float2 v = sh.part[i * CW + threadIdx.x];
-                    own = after(Map{v.x, v.y}, own);
-                }
-            h = apply(look_back(p, tile, slab, on ? int(threadIdx.x) : 0, on, own), 0.f);
-        }
-        if (on)
-            for (int i = 0; i < parts; ++i) {
-                const float2 v = sh.part[i * CW + threadIdx.x];
-                sh.part[i * CW + threadIdx.x].x = h;
-                h = apply(Map{v.x, v.y}, h);
-            }
-    }
-    __syncthreads();
     if (part < parts) {
-        float h = sh.part[part * CW + c].x;
-        for (int k = k0; k < k1; ++k) {
-            const float2 v = sh.map[k * CW + c];
-            sh.in[k * CW + c] = h;
-            h = apply(Map{v.x, v.y}, h);
+        m = Map{1.f, 0.f};
+        for (int i = 0; i < part; ++i) {
+            const float2 v = sh.part[i * CW + c];
+            m = after(Map{v.x, v.y}, m);
         }
+        for (int i = k0; i < k1; ++i) {
+            const float2 v = sh.map[i * CW + c];
+            out(i, c, m);
+            m = after(Map{v.x, v.y}, m);
+        }
+        if (part == parts - 1) all(c, m);
     }
-    __syncthreads();
 }
 
-// States of the samples without rows.
-__device__ __forceinline__ void pass_empty(const LrArgs& p, const float* from, float* to, int64_t first, int64_t step) {
-    if (!to) return;
-    for (int64_t s = first; s < p.segs.n_seg; s += step)
-        if (p.segs.at(int(s)) >= p.segs.at(int(s) + 1))
-            for (int c = 0; c < p.C; c += 4) {
-                const int64_t i = s * p.C + c;
-                *reinterpret_cast<f32x4_t*>(to + i) = from ? *reinterpret_cast<const f32x4_t*>(from + i) : f32x4_t{0, 0, 0, 0};
-            }
-}
-
-// Before a scan of several tiles: its words and ticket, and the samples without rows.
-__global__ __launch_bounds__(NT) void k_lr_clear(LrArgs p, int64_t words, const float* from, float* to) {
-    const int64_t i = int64_t(blockIdx.x) * NT + threadIdx.x, step = int64_t(gridDim.x) * NT;
-    if (p.ticket) {
-        if (i == 0) *p.ticket = 0;
-        for (int64_t j = i; 2 * j < words; j += step) st16(p.words + 2 * j, u32x4{~0u, ~0u, ~0u, ~0u});
-    }
-    pass_empty(p, from, to, i, step);
-}
-
-// A thread's chunk.
 template <typename TT, bool ORDERED, bool BACK>
-struct Chunk {
-    static constexpr int T = ChunkRows<TT>::T;
-    const LrArgs& p;
-    const int32_t* rowno;
-    int ch;          // number within the tile, in the order of the scan
-    int i0;          // its first row within the tile
-    int pos;         // position in the walk of its first row
-    int lo, hi;      // positions [lo, hi) lie in samples
-    int c;           // first channel
-    bool on;
-    uint32_t first, last;   // marks
-    bool plain;      // the wave's chunks have no marks and all their rows
+__global__ __launch_bounds__(NT, TT::E == 8 ? 5 : 4) void k_lr_reduce(const void* __restrict__ gate, const void* __restrict__ v, LrArgs p,
+                                                  const float* __restrict__ from) {
+    __shared__ Shared sh;
+    const int tile = int(blockIdx.x) / p.k.nslab, slab = int(blockIdx.x) - tile * p.k.nslab;
+    const Span span(p, tile);
+    const Strip k(p, span, slab, BACK);
+    const Window w = open_window(p, span);
+    const bool marked = mark(p, sh, span, w);
+    f32x4_t A, B;
+    reduce<TT, ORDERED, BACK>(gate, v, from, p, sh, w, marked, k, A, B);
+    const int c0 = slab * p.k.CW;
+    join(p, sh, k, A, B,
+         [&](int i, int c, const Map& m) {
+             if (c0 + c < p.C) p.strip[int64_t(tile * p.k.NCH + i) * p.C + c0 + c] = float2{m.A, m.B};
+         },
+         [&](int c, const Map& m) {
+             if (c0 + c < p.C) p.tile[int64_t(tile) * p.C + c0 + c] = float2{m.A, m.B};
+         });
+}
 
-    __device__ __forceinline__ Chunk(const LrArgs& a, Shared& sh, const int32_t* rn, int tile, int slab) : p(a), rowno(rn) {
-        const int CPR = p.k.CPR, n = p.segs.n;
-        ch = int(threadIdx.x) / CPR;
-        const int quad = int(threadIdx.x) - ch * CPR;
-        c = (slab * CPR + quad) * 4;
-        on = ch < p.k.NCH && c < p.C;
-        i0 = (BACK ? p.k.NCH - 1 - ch : ch) * T;
-        if (!on) i0 = 0;
-        pos = base(p, tile) + i0;
-        const int a0 = p.segs.at(0), b0 = p.segs.at(p.segs.n_seg);
-        lo = p.reverse ? n - b0 : a0;
-        hi = p.reverse ? n - a0 : b0;
-        const uint32_t mask = (1u << T) - 1;
-        first = on ? sh.first[i0 / 32] >> (i0 % 32) & mask : 0;
-        last = on ? sh.last[i0 / 32] >> (i0 % 32) & mask : 0;
-        bool whole = pos >= lo && pos + T <= hi;
-        if constexpr (ORDERED)
+// The states that the tiles start from.  A workgroup takes 4 channels; part i
+// of 256 folds TP tiles, the parts are joined in their wave by shuffles and
+// across the 16 waves in LDS.  More tiles than that go round again.
+constexpr int TN = 1024, TP = 8, TR = TN / 4 * TP;
+__global__ __launch_bounds__(TN) void k_lr_tiles(LrArgs p, bool back) {
+    __shared__ float2 wave[TN / WAVE][4];
+    const int c = int(threadIdx.x) % 4, part = int(threadIdx.x) / 4, lane = int(threadIdx.x) % WAVE;
+    const int ch = int(blockIdx.x) * 4 + c, tiles = p.k.tiles;
+    float h = 0.f;   // before this round's tiles
+    for (int base = 0; base < tiles; base += TR) {
+        const int count = tiles - base < TR ? tiles - base : TR, per = (count + TN / 4 - 1) / (TN / 4);
+        const int i0 = base + part * per;
+        Map v[TP], m{1.f, 0.f};
 #pragma unroll
-            for (int t = 0; t < T; ++t) whole = whole && rowno[i0 + t] >= 0;
-        plain = __all(!on || (whole && !(first | last)));
+        for (int j = 0; j < TP; ++j) {
+            const int i = i0 + j;
+            v[j] = Map{1.f, 0.f};
+            if (j < per && i < tiles) {
+                const float2 q = p.tile[int64_t(back ? tiles - 1 - i : i) * p.C + ch];
+                v[j] = Map{q.x, q.y};
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TP; ++j) m = after(v[j], m);
+        for (int o = 4; o < WAVE; o <<= 1) {
+            const Map f{__shfl_up(m.A, o), __shfl_up(m.B, o)};
+            if (lane >= o) m = after(m, f);
+        }
+        if (lane >= WAVE - 4) wave[threadIdx.x / WAVE][c] = float2{m.A, m.B};
+        Map before{__shfl_up(m.A, 4), __shfl_up(m.B, 4)};
+        if (lane < 4) before = Map{1.f, 0.f};
+        __syncthreads();
+        float g = h;
+        for (int i = 0; i < TN / WAVE; ++i) {
+            if (i == int(threadIdx.x) / WAVE) h = g;
+            g = apply(Map{wave[i][c].x, wave[i][c].y}, g);
+        }
+        h = apply(before, h);
+#pragma unroll
+        for (int j = 0; j < TP; ++j) {
+            const int i = i0 + j;
+            if (j < per && i < tiles) p.start[int64_t(back ? tiles - 1 - i : i) * p.C + ch] = h;
+            h = apply(v[j], h);
+        }
+        h = g;
+        __syncthreads();
     }
+}
 
-    // Position of a tile's first row: the backward's tiles are numbered from
-    // the end, and cut at the same chunks as the forward's.
-    static __device__ __forceinline__ int base(const LrArgs& p, int tile) {
-        if (!BACK) return tile * p.k.rows;
-        const int chunks = (p.segs.n + T - 1) / T;
-        return (chunks - (tile + 1) * p.k.NCH) * T;
+// The state that strip k of a tile starts from, after k_lr_reduce.
+template <bool BACK>
+__device__ __forceinline__ f32x4_t start_of(const LrArgs& p, int tile, const Strip& k) {
+    f32x4_t h = 0.f;
+    const auto through = [&](const float2* q) {
+        const f32x4_t u = ld4(&q->x), v = ld4(&q[2].x);
+        h = f32x4_t{apply(Map{u[0], u[1]}, h[0]), apply(Map{u[2], u[3]}, h[1]), apply(Map{v[0], v[1]}, h[2]), apply(Map{v[2], v[3]}, h[3])};
+    };
+    if (p.k.tiles > FEW) {
+        h = ld4(p.start + int64_t(tile) * p.C + k.c);
+    } else {
+#pragma unroll 2
+        for (int i = BACK ? p.k.tiles - 1 : 0; i != tile; i += BACK ? -1 : 1) through(p.tile + int64_t(i) * p.C + k.c);
     }
+    through(p.strip + int64_t(tile * p.k.NCH + k.ch) * p.C + k.c);
+    return h;
+}
 
-    __device__ __forceinline__ int row(int t) const {
-        if constexpr (ORDERED) return rowno[i0 + t];
-        const int f = pos + t;
-        return f >= lo && f < hi ? (p.reverse ? p.segs.n - 1 - f : f) : -1;
+// The samples without rows pass their state on.
+__device__ __forceinline__ void pass_empty(const LrArgs& p, const float* from, float* to) {
+    if (!to) return;
+    for (int64_t s = int64_t(blockIdx.x) * NT + threadIdx.x; s < p.segs.n_seg; s += int64_t(gridDim.x) * NT)
+        if (p.segs.at(int(s)) >= p.segs.at(int(s) + 1))
+            for (int c = 0; c < p.C; c += 4) st4(to + s * p.C + c, from ? ld4(from + s * p.C + c) : f32x4_t{0, 0, 0, 0});
+}
+__global__ __launch_bounds__(NT) void k_lr_empty(LrArgs p, const float* from, float* to) { pass_empty(p, from, to); }
+
+// ONE: a single tile, whose strips are reduced and joined here.
+template <typename TT, bool ORDERED, bool ONE>
+__global__ __launch_bounds__(NT, TT::E == 8 ? 5 : 4) void k_lr_fwd(const void* __restrict__ gate, const void* __restrict__ x, LrArgs p,
+                                               const float* __restrict__ h0, void* __restrict__ out_,
+                                               float* __restrict__ h_last, float* __restrict__ carry) {
+    typename TT::storage* out = static_cast<typename TT::storage*>(out_);
+    __shared__ Shared sh;
+    __shared__ float in[ONE ? NT * 4 : 4];
+    const int tile = int(blockIdx.x) / p.k.nslab, slab = int(blockIdx.x) - tile * p.k.nslab;
+    const Span span(p, tile);
+    const Strip k(p, span, slab, false);
+    const Window w = open_window(p, span);
+    const bool marked = mark(p, sh, span, w);
+    f32x4_t h = 0.f;
+    if constexpr (ONE) {
+        f32x4_t A, B;
+        reduce<TT, ORDERED, false>(gate, x, h0, p, sh, w, marked, k, A, B);
+        join(p, sh, k, A, B, [&](int i, int c, const Map& m) { in[i * p.k.CW + c] = apply(m, 0.f); }, [](int, const Map&) {});
+        __syncthreads();
+        if (k.on) h = ld4(&in[k.at]);
+    } else if (k.on) {
+        h = start_of<false>(p, tile, k);
     }
-    // The row of a plain chunk.
-    __device__ __forceinline__ int64_t prow(int t) const {
-        if constexpr (ORDERED) return rowno[i0 + t];
-        return p.reverse ? p.segs.n - 1 - pos - t : pos + t;
+    if (k.on)
+        for (int i = 0; i < p.k.L; i += T) {
+            Pair<TT, ORDERED> b;
+            b.load(p, w, gate, x, p.ld, k.pos + i, k.c);
+            b.rows.marks(sh, marked, k.i0 + i);
+            if (carry && k.pos + i < p.segs.n) st4(carry + int64_t((k.pos + i) / T) * p.C + k.c, h);
+            const auto step = [&](int t) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float a, na;
+                    gates(elem<TT>(b.g[t], j), a, na);
+                    h[j] = fmaf(a, h[j], na * elem<TT>(b.x[t], j));
+                }
+                str<TT>(out + int64_t(b.rows.r[t]) * p.C + k.c, h);
+            };
+            if (b.rows.simple) {
+#pragma unroll
+                for (int t = 0; t < T; ++t) step(t);
+            } else {
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    if (b.rows.first >> t & 1) h = state_of(h0, p, sh, k.i0 + i + t, k.c);
+                    if (b.rows.r[t] >= 0) step(t);
+                    if ((b.rows.last >> t & 1) && h_last) st4(h_last + int64_t(sh.sample[k.i0 + i + t]) * p.C + k.c, h);
+                }
+            }
+        }
+    pass_empty(p, h0, h_last);
+}
+
+// T rows of the backward's walk, and the state ahead of them.
+template <typename TT, bool ORDERED>
+struct Triple {
+    Rows<ORDERED> rows;
+    Raw4<TT> g[T], v[T], d[T];
+    f32x4_t h;
+    __device__ __forceinline__ void load(const LrArgs& p, const Window& w, const void* gate, const void* x, const void* dout, const float* carry, int pos,
+                                         int c) {
+        using S = typename TT::storage;
+        rows.numbers(p, w, pos);
+        h = ld4(carry + int64_t(pos / T) * p.C + c);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            g[t] = ldr<TT>(static_cast<const S*>(gate) + rows.any(t) * p.ld + c);
+            v[t] = ldr<TT>(static_cast<const S*>(x) + rows.any(t) * p.ld + c);
+            d[t] = ldr<TT>(static_cast<const S*>(dout) + rows.any(t) * p.C + c);
+        }
     }
 };
 
-template <typename TT, bool ORDERED>
-__global__ __launch_bounds__(NT, 2) void k_lr_fwd(const void* __restrict__ gate_, const void* __restrict__ x_, LrArgs p,
-                                                  const float* __restrict__ h0, void* __restrict__ out_,
-                                                  float* __restrict__ h_last, float* __restrict__ carry) {
-    constexpr int T = ChunkRows<TT>::T;
+template <typename TT, bool ORDERED, bool ONE>
+__global__ __launch_bounds__(NT, TT::E == 8 ? 3 : 2) void k_lr_bwd(const void* __restrict__ dout, const void* __restrict__ gate,
+                                               const void* __restrict__ x, LrArgs p, const float* __restrict__ h0,
+                                               const float* __restrict__ carry, const float* __restrict__ dh_last,
+                                               void* __restrict__ dgate_, void* __restrict__ dx_, float* __restrict__ dh0) {
     using S = typename TT::storage;
-    const S *gate = static_cast<const S*>(gate_), *x = static_cast<const S*>(x_);
-    S* out = static_cast<S*>(out_);
-    __shared__ Shared sh;
-    __shared__ int32_t rowno[ORDERED ? NT * 4 : 1];
-    int tile, slab;
-    take(p, sh, tile, slab);
-    if (tile >= p.k.tiles) return;
-    mark<ORDERED>(p, sh, rowno, Chunk<TT, ORDERED, false>::base(p, tile));
-    const Chunk<TT, ORDERED, false> k(p, sh, rowno, tile, slab);
-
-    f32x4_t a[T], b[T];
-    f32x4_t A = 1.f, B = 0.f;
-    if (k.plain) {
-        if (k.on) {
-            Raw4<TT> g[T], v[T];
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const int64_t o = k.prow(t) * p.ld + k.c;
-                g[t] = ldr<TT>(gate + o);
-                v[t] = ldr<TT>(x + o);
-            }
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float aj, na;
-                    gates(elem<TT>(g[t], j), aj, na);
-                    a[t][j] = aj;
-                    b[t][j] = na * elem<TT>(v[t], j);
-                    A[j] *= a[t][j];
-                    B[j] = fmaf(a[t][j], B[j], b[t][j]);
-                }
-        }
-    } else if (k.on) {
-        Raw4<TT> g[T], v[T];
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const int r = k.row(t);
-            const int64_t o = (r < 0 ? 0 : r) * p.ld + k.c;
-            g[t] = ldr<TT>(gate + o);
-            v[t] = ldr<TT>(x + o);
-        }
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const bool ok = k.row(t) >= 0, start = k.first >> t & 1;
-            f32x4_t h = 0.f;
-            if (start && h0) h = *reinterpret_cast<const f32x4_t*>(h0 + int64_t(sh.sample[k.i0 + t]) * p.C + k.c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float aj, na;
-                gates(elem<TT>(g[t], j), aj, na);
-                a[t][j] = aj;
-                b[t][j] = na * elem<TT>(v[t], j);
-                if (!ok) a[t][j] = 1.f, b[t][j] = 0.f;
-                if (start) b[t][j] = fmaf(a[t][j], h[j], b[t][j]), a[t][j] = -0.f;
-                const Map m = after(Map{a[t][j], b[t][j]}, Map{A[j], B[j]});
-                A[j] = m.A, B[j] = m.B;
-            }
-        }
-    }
-    const int at = k.ch * p.k.CW + k.c - slab * p.k.CW;
-    if (k.ch < p.k.NCH) {
-        f32x4_t* q = reinterpret_cast<f32x4_t*>(&sh.map[at]);
-        q[0] = f32x4_t{A[0], B[0], A[1], B[1]};
-        q[1] = f32x4_t{A[2], B[2], A[3], B[3]};
-    }
-    join(p, sh, tile, slab);
-    if (!k.on) return;
-    f32x4_t h = *reinterpret_cast<const f32x4_t*>(&sh.in[at]);
-    if (carry && k.pos < p.segs.n)
-        *reinterpret_cast<f32x4_t*>(carry + int64_t(tile * p.k.NCH + k.ch) * p.C + k.c) = h;
-    if (k.plain) {
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = fmaf(a[t][j], h[j], b[t][j]);
-            str<TT>(out + k.prow(t) * p.C + k.c, h);
-        }
-    } else {
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = apply(Map{a[t][j], b[t][j]}, h[j]);
-            const int r = k.row(t);
-            if (r >= 0) str<TT>(out + int64_t(r) * p.C + k.c, h);
-            if ((k.last >> t & 1) && h_last)
-                *reinterpret_cast<f32x4_t*>(h_last + int64_t(sh.sample[k.i0 + t]) * p.C + k.c) = h;
-        }
-    }
-}
-
-template <typename TT, bool ORDERED>
-__global__ __launch_bounds__(NT, 2) void k_lr_bwd(const void* __restrict__ dout_, const void* __restrict__ gate_,
-                                                  const void* __restrict__ x_, LrArgs p, const float* __restrict__ h0,
-                                                  const float* __restrict__ carry, const float* __restrict__ dh_last,
-                                                  void* __restrict__ dgate_, void* __restrict__ dx_, float* __restrict__ dh0) {
-    constexpr int T = ChunkRows<TT>::T;
-    using S = typename TT::storage;
-    const S *gate = static_cast<const S*>(gate_), *x = static_cast<const S*>(x_), *dout = static_cast<const S*>(dout_);
     S *dgate = static_cast<S*>(dgate_), *dx = static_cast<S*>(dx_);
     __shared__ Shared sh;
-    __shared__ int32_t rowno[ORDERED ? NT * 4 : 1];
-    int tile, slab;
-    take(p, sh, tile, slab);
-    if (tile >= p.k.tiles) return;
-    mark<ORDERED>(p, sh, rowno, Chunk<TT, ORDERED, true>::base(p, tile));
-    const Chunk<TT, ORDERED, true> k(p, sh, rowno, tile, slab);
-    const bool on = k.on && k.pos >= 0;      // the last tile reaches past the walk's start
-
-    // Kept of every element: sm, the smaller of a and 1 - a, with the gate's
-    // sign; u = h_{t-1} - x_t; and dout as it is.
-    f32x4_t sm[T], u[T];
-    Raw4<TT> d[T];
-    f32x4_t A = 1.f, B = 0.f;
-    const auto a_of = [](float s, float& na) {
-        const float m = fabsf(s);
-        const bool pos = !(__float_as_int(s) < 0);
-        na = pos ? m : 1.f - m;
-        return pos ? 1.f - m : m;
-    };
-    if (on) {
-        Raw4<TT> g[T], v[T];
-        f32x4_t h = *reinterpret_cast<const f32x4_t*>(carry + int64_t(k.pos / T) * p.C + k.c);
+    __shared__ float in[ONE ? NT * 4 : 4];
+    const int tile = int(blockIdx.x) / p.k.nslab, slab = int(blockIdx.x) - tile * p.k.nslab;
+    const Span span(p, tile);
+    const Strip k(p, span, slab, true);
+    const Window w = open_window(p, span);
+    const bool marked = mark(p, sh, span, w);
+    f32x4_t E = 0.f;
+    if constexpr (ONE) {
+        f32x4_t A, B;
+        reduce<TT, ORDERED, true>(gate, dout, dh_last, p, sh, w, marked, k, A, B);
+        join(p, sh, k, A, B, [&](int i, int c, const Map& m) { in[i * p.k.CW + c] = apply(m, 0.f); }, [](int, const Map&) {});
+        __syncthreads();
+        if (k.on) E = ld4(&in[k.at]);
+    } else if (k.on) {
+        E = start_of<true>(p, tile, k);
+    }
+    if (k.on)
+        for (int i = p.k.L - T; i >= 0; i -= T) {
+            if (k.pos + i >= p.segs.n) continue;
+            Triple<TT, ORDERED> b;
+            b.load(p, w, gate, x, dout, carry, k.pos + i, k.c);
+            b.rows.marks(sh, marked, k.i0 + i);
+            const auto& rows = b.rows;
+            f32x4_t h = b.h;
+            f32x4_t a[T], u[T];   // the gates as kept, and h_{t-1} - x_t
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const int64_t r = k.plain ? k.prow(t) : (k.row(t) < 0 ? 0 : k.row(t));
-            g[t] = ldr<TT>(gate + r * p.ld + k.c);
-            v[t] = ldr<TT>(x + r * p.ld + k.c);
-            d[t] = ldr<TT>(dout + r * p.C + k.c);
-        }
+            for (int t = 0; t < T; ++t) {
+                if (!rows.simple && (rows.first >> t & 1)) h = state_of(h0, p, sh, k.i0 + i + t, k.c);
+                const bool ok = rows.simple || rows.r[t] >= 0;
+                float kept[4];
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            bool ok = true;
-            if (!k.plain) {
-                ok = k.row(t) >= 0;
-                if (k.first >> t & 1)
-                    h = h0 ? *reinterpret_cast<const f32x4_t*>(h0 + int64_t(sh.sample[k.i0 + t]) * p.C + k.c) : f32x4_t{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float gj = elem<TT>(g[t], j), xj = elem<TT>(v[t], j);
-                float big;
-                const float small = gate_small(gj, big);
-                sm[t][j] = __builtin_copysignf(small, gj);
-                u[t][j] = h[j] - xj;
-                const float a = gj >= 0.f ? big : small, na = gj >= 0.f ? small : big;
-                const float next = fmaf(a, h[j], na * xj);
-                h[j] = ok ? next : h[j];
-            }
-        }
-#pragma unroll
-        for (int t = T - 1; t >= 0; --t) {
-            if (!k.plain) {
-                if (k.last >> t & 1) {
-                    A = -0.f;
-                    B = dh_last ? *reinterpret_cast<const f32x4_t*>(dh_last + int64_t(sh.sample[k.i0 + t]) * p.C + k.c)
-                                : f32x4_t{0, 0, 0, 0};
+                for (int j = 0; j < 4; ++j) {
+                    const float xj = elem<TT>(b.v[t], j);
+                    float aj, na;
+                    kept[j] = keep(elem<TT>(b.g[t], j));
+                    gates_of(kept[j], aj, na);
+                    u[t][j] = h[j] - xj;
+                    const float next = fmaf(aj, h[j], na * xj);
+                    h[j] = ok ? next : h[j];
                 }
-                if (k.row(t) < 0) continue;
+                // the compiler would otherwise keep both gates of all elements, in twice the registers
+#pragma unroll
+                for (int j = 0; j < 4; ++j) hide(kept[j]);
+                a[t] = f32x4_t{kept[0], kept[1], kept[2], kept[3]};
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float na;
-                const float a = a_of(sm[t][j], na);
-                A[j] *= a;
-                B[j] = a * (elem<TT>(d[t], j) + B[j]);
+            for (int t = T - 1; t >= 0; --t) {
+                if (!rows.simple && (rows.last >> t & 1)) E = state_of(dh_last, p, sh, k.i0 + i + t, k.c);
+                if (rows.simple || rows.r[t] >= 0) {
+                    f32x4_t gx, gg;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float aj, na;
+                        gates_of(a[t][j], aj, na);
+                        const float D = elem<TT>(b.d[t], j) + E[j];
+                        gx[j] = na * D;
+                        E[j] = aj * D;
+                        gg[j] = na * u[t][j] * E[j];
+                    }
+                    str<TT>(dx + int64_t(rows.r[t]) * p.ldg + k.c, gx);
+                    str<TT>(dgate + int64_t(rows.r[t]) * p.ldg + k.c, gg);
+                }
+                if (!rows.simple && (rows.first >> t & 1) && dh0) st4(dh0 + int64_t(sh.sample[k.i0 + i + t]) * p.C + k.c, E);
             }
         }
-    }
-    const int at = k.ch * p.k.CW + k.c - slab * p.k.CW;
-    if (k.ch < p.k.NCH) {
-        f32x4_t* q = reinterpret_cast<f32x4_t*>(&sh.map[at]);
-        q[0] = f32x4_t{A[0], B[0], A[1], B[1]};
-        q[1] = f32x4_t{A[2], B[2], A[3], B[3]};
-    }
-    join(p, sh, tile, slab);
-    if (!on) return;
-    f32x4_t E = *reinterpret_cast<const f32x4_t*>(&sh.in[at]);
-#pragma unroll
-    for (int t = T - 1; t >= 0; --t) {
-        int64_t r = 0;
-        if (k.plain) {
-            r = k.prow(t);
-        } else {
-            r = k.row(t);
-            if (k.last >> t & 1)
-                E = dh_last ? *reinterpret_cast<const f32x4_t*>(dh_last + int64_t(sh.sample[k.i0 + t]) * p.C + k.c)
-                            : f32x4_t{0, 0, 0, 0};
-        }
-        if (k.plain || r >= 0) {
-            f32x4_t gx, gg;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float na;
-                const float a = a_of(sm[t][j], na), D = elem<TT>(d[t], j) + E[j];
-                gx[j] = na * D;
-                E[j] = a * D;
-                gg[j] = na * u[t][j] * E[j];
-            }
-            str<TT>(dx + r * p.ldg + k.c, gx);
-            str<TT>(dgate + r * p.ldg + k.c, gg);
-        }
-        if (!k.plain && (k.first >> t & 1) && dh0)
-            *reinterpret_cast<f32x4_t*>(dh0 + int64_t(sh.sample[k.i0 + t]) * p.C + k.c) = E;
-    }
+    pass_empty(p, dh_last, dh0);
 }
 
 // One row of each of n running sequences: state is read, replaced and rounded to out.
@@ -636,11 +645,11 @@ spc_status check_stride(spc_dtype dtype, int64_t ld, int32_t C, const char* name
 }
 
 // The states that the chunks start from.
-size_t carry_bytes(spc_dtype dtype, int64_t n, int32_t C) { return size_t(ceil_div(n, chunk_rows(dtype))) * C * 4; }
-// The ticket and the look-back tree; a scan of one tile needs neither.
-size_t ws_need(spc_dtype dtype, int64_t n, int32_t C) {
-    const Cut k = cut_of(dtype, n, C);
-    return 256 + (k.tiles > 1 ? size_t(tree_words(k)) * 8 : 0);
+size_t carry_bytes(int64_t n, int32_t C) { return size_t(ceil_div(n, T)) * C * 4; }
+// The strips', the tiles' maps and the states that the tiles start from.
+size_t ws_need(int64_t n, int32_t C) {
+    const Cut k = cut_of(n, C);
+    return k.tiles > 1 ? size_t(k.tiles) * C * (8 * size_t(k.NCH) + 8 + 4) : 16;
 }
 
 spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int64_t ld, const int32_t* seg_ptr, int64_t n_seg,
@@ -652,25 +661,66 @@ spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int64_t ld, const i
     if (!ws) return fail(SPC_ERR_ARG, "ws is NULL");
     for (const void* q : {(const void*)seg_ptr, (const void*)order, (const void*)ws})
         if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
-    if (ws_bytes < ws_need(dtype, n, C))
-        return fail(SPC_ERR_WORKSPACE, "ws_bytes=%zu, need %zu", ws_bytes, ws_need(dtype, n, C));
+    if (ws_bytes < ws_need(n, C))
+        return fail(SPC_ERR_WORKSPACE, "ws_bytes=%zu, need %zu", ws_bytes, ws_need(n, C));
     p.segs = Segs{seg_ptr, int32_t(n_seg), int32_t(n)};
     p.C = C, p.reverse = reverse != 0, p.ld = ld, p.ldg = C, p.order = order;
-    p.k = cut_of(dtype, n, C);
+    p.k = cut_of(n, C);
     if (int64_t(p.k.tiles) * p.k.nslab >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
-    const bool many = p.k.tiles > 1;
-    p.ticket = many ? static_cast<uint32_t*>(ws) : nullptr;
-    p.words = many ? reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + 256) : nullptr;
+    p.strip = static_cast<float2*>(ws);
+    p.tile = p.strip + int64_t(p.k.tiles) * p.k.NCH * C;
+    p.start = reinterpret_cast<float*>(p.tile + int64_t(p.k.tiles) * C);
     return SPC_OK;
 }
 
-// The launch before a scan; a single tile of a single sample with rows needs none.
-spc_status clear(const LrArgs& p, const float* from, float* to, hipStream_t stream) {
-    const int64_t words = p.ticket ? tree_words(p.k) : 0;
-    if (!p.ticket && !(to && (p.segs.ptr || p.segs.n == 0))) return SPC_OK;
-    const int64_t work = ceil_div(words / 2 > p.segs.n_seg ? words / 2 : p.segs.n_seg, NT);
-    hipLaunchKernelGGL(k_lr_clear, dim3(unsigned(work < 4096 ? work : 4096)), dim3(NT), 0, stream, p, words, from, to);
-    SPC_LAUNCHED("k_lr_clear");
+// The launches of a scan: ahead of the walk, which is apply(one tile).
+template <typename TT, bool ORDERED, bool BACK>
+spc_status launch_reduce(const void* gate, const void* v, const LrArgs& p, const float* from, hipStream_t stream) {
+    hipLaunchKernelGGL((k_lr_reduce<TT, ORDERED, BACK>), dim3(unsigned(p.k.tiles) * unsigned(p.k.nslab)), dim3(NT), 0, stream, gate, v,
+                       p, from);
+    SPC_LAUNCHED("k_lr_reduce");
+    if (p.k.tiles > FEW) {
+        hipLaunchKernelGGL(k_lr_tiles, dim3(unsigned(p.C / 4)), dim3(TN), 0, stream, p, BACK);
+        SPC_LAUNCHED("k_lr_tiles");
+    }
+    return SPC_OK;
+}
+
+spc_status launch_empty(const LrArgs& p, const float* from, float* to, hipStream_t stream) {
+    if (!to) return SPC_OK;
+    const int64_t blocks = ceil_div(p.segs.n_seg, NT);
+    hipLaunchKernelGGL(k_lr_empty, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(NT), 0, stream, p, from, to);
+    SPC_LAUNCHED("k_lr_empty");
+    return SPC_OK;
+}
+
+template <typename TT, bool ORDERED>
+spc_status launch_fwd(const void* gate, const void* x, const LrArgs& p, const float* h0, void* out, float* h_last, float* carry,
+                      hipStream_t stream) {
+    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
+    if (p.k.tiles == 1) {
+        hipLaunchKernelGGL((k_lr_fwd<TT, ORDERED, true>), grid, dim3(NT), 0, stream, gate, x, p, h0, out, h_last, carry);
+    } else {
+        const spc_status st = launch_reduce<TT, ORDERED, false>(gate, x, p, h0, stream);
+        if (st != SPC_OK) return st;
+        hipLaunchKernelGGL((k_lr_fwd<TT, ORDERED, false>), grid, dim3(NT), 0, stream, gate, x, p, h0, out, h_last, carry);
+    }
+    SPC_LAUNCHED("k_lr_fwd");
+    return SPC_OK;
+}
+
+template <typename TT, bool ORDERED>
+spc_status launch_bwd(const void* dout, const void* gate, const void* x, const LrArgs& p, const float* h0, const float* carry,
+                      const float* dh_last, void* dgate, void* dx, float* dh0, hipStream_t stream) {
+    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
+    if (p.k.tiles == 1) {
+        hipLaunchKernelGGL((k_lr_bwd<TT, ORDERED, true>), grid, dim3(NT), 0, stream, dout, gate, x, p, h0, carry, dh_last, dgate, dx, dh0);
+    } else {
+        const spc_status st = launch_reduce<TT, ORDERED, true>(gate, dout, p, dh_last, stream);
+        if (st != SPC_OK) return st;
+        hipLaunchKernelGGL((k_lr_bwd<TT, ORDERED, false>), grid, dim3(NT), 0, stream, dout, gate, x, p, h0, carry, dh_last, dgate, dx, dh0);
+    }
+    SPC_LAUNCHED("k_lr_bwd");
     return SPC_OK;
 }
 
@@ -687,20 +737,20 @@ using namespace spc;
         SPC_LAUNCHED(#name);                                                                                      \
     } while (0)
 
-#define LR_DISPATCH2(name, flag, grid, block, ...)                                                                \
-    do {                                                                                                          \
-        if (dtype == SPC_F32) hipLaunchKernelGGL((name<F32, flag>), grid, block, 0, stream, __VA_ARGS__);         \
-        if (dtype == SPC_F16) hipLaunchKernelGGL((name<F16, flag>), grid, block, 0, stream, __VA_ARGS__);         \
-        if (dtype == SPC_BF16) hipLaunchKernelGGL((name<BF16, flag>), grid, block, 0, stream, __VA_ARGS__);       \
-        SPC_LAUNCHED(#name);                                                                                      \
-    } while (0)
+#define LR_ORDERED(fn, ...)                                                                                        \
+    switch (dtype) {                                                                                              \
+        case SPC_F32: return order ? fn<F32, true>(__VA_ARGS__) : fn<F32, false>(__VA_ARGS__);                    \
+        case SPC_F16: return order ? fn<F16, true>(__VA_ARGS__) : fn<F16, false>(__VA_ARGS__);                    \
+        case SPC_BF16: return order ? fn<BF16, true>(__VA_ARGS__) : fn<BF16, false>(__VA_ARGS__);                 \
+    }                                                                                                             \
+    return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype))
 
 extern "C" spc_status spc_linear_recurrence_workspace(spc_dtype dtype, int64_t n, int32_t C, int64_t n_seg, size_t* ws,
                                                       size_t* carry) {
     clear_error();
     if (!ws || !carry) return fail(SPC_ERR_ARG, "ws or carry is NULL");
     const spc_status st = check_sizes(dtype, n, C, n_seg);
-    if (st == SPC_OK) *ws = ws_need(dtype, n, C), *carry = carry_bytes(dtype, n, C);
+    if (st == SPC_OK) *ws = ws_need(n, C), *carry = carry_bytes(n, C);
     return st;
 }
 
@@ -715,12 +765,8 @@ extern "C" spc_status spc_linear_recurrence_fwd(spc_dtype dtype, const void* gat
     if (n > 0 && (!gate || !x || !out)) return fail(SPC_ERR_ARG, "gate, x or out is NULL");
     for (const void* q : {gate, x, (const void*)h0, (const void*)out, (const void*)h_last, (const void*)carry})
         if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
-    const spc_status cs = clear(p, h0, h_last, stream);
-    if (cs != SPC_OK || n == 0) return cs;
-    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
-    if (order) LR_DISPATCH2(k_lr_fwd, true, grid, dim3(NT), gate, x, p, h0, out, h_last, carry);
-    else LR_DISPATCH2(k_lr_fwd, false, grid, dim3(NT), gate, x, p, h0, out, h_last, carry);
-    return SPC_OK;
+    if (n == 0) return launch_empty(p, h0, h_last, stream);
+    LR_ORDERED(launch_fwd, gate, x, p, h0, out, h_last, carry, stream);
 }
 
 extern "C" spc_status spc_linear_recurrence_bwd(spc_dtype dtype, const void* dout, const void* gate, const void* x,
@@ -739,12 +785,8 @@ extern "C" spc_status spc_linear_recurrence_bwd(spc_dtype dtype, const void* dou
                           (const void*)dx, (const void*)dh0})
         if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     p.ldg = ldg;
-    st = clear(p, dh_last, dh0, stream);
-    if (st != SPC_OK || n == 0) return st;
-    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
-    if (order) LR_DISPATCH2(k_lr_bwd, true, grid, dim3(NT), dout, gate, x, p, h0, carry, dh_last, dgate, dx, dh0);
-    else LR_DISPATCH2(k_lr_bwd, false, grid, dim3(NT), dout, gate, x, p, h0, carry, dh_last, dgate, dx, dh0);
-    return SPC_OK;
+    if (n == 0) return launch_empty(p, dh_last, dh0, stream);
+    LR_ORDERED(launch_bwd, dout, gate, x, p, h0, carry, dh_last, dgate, dx, dh0, stream);
 }
 
 extern "C" spc_status spc_linear_recurrence_step(spc_dtype dtype, const void* gate, const void* x, int64_t ld, int64_t n,
