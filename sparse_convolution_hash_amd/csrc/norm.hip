@@ -19,56 +19,99 @@
 namespace spc {
 namespace {
 
-constexpr int NT = 256;   // threads per workgroup
-constexpr int CPR = 8;    // threads per row: 8 x 8 = 64 channels per workgroup
-constexpr int RL = NT / CPR;  // rows in flight per workgroup step
-constexpr int R = 128;    // rows per tile
+constexpr int NT = 256;      // threads per workgroup
+constexpr int OPR = 8;       // most lanes (of 8 channels) per row: slabs of up to 64 channels
+constexpr int U = 4;         // rows that a thread loads at a time
+
+// How [n, C] is cut: slabs of CW channels, CPR lanes to a row, RL rows side by
+// side, tiles of R rows.
+struct Cut {
+    int32_t nslab, CPR, CW, RL, R;
+    int32_t tiles;
+};
+
+inline Cut cut_of(int64_t n, int32_t C) {
+    Cut k;
+    k.nslab = int32_t(ceil_div(C / 8, OPR));
+    k.CPR = int32_t(ceil_div(C / 8, k.nslab));
+    k.CW = 8 * k.CPR;
+    k.RL = NT / k.CPR;
+    // the longest tiles that still give every CU 8 workgroups
+    k.R = k.RL * U;
+    while (k.R < k.RL * U * 4 && ceil_div(n, 2 * k.R) * k.nslab >= 8 * 256) k.R *= 2;
+    k.tiles = int32_t(ceil_div(n, k.R));
+    return k;
+}
 
 struct NormArgs {
     Segs segs;
     int32_t C, G;
     float eps;
     Drop drop;
+    Cut k;
 };
 
-// v summed over the lanes of a wave that share threadIdx.x % CPR.
-__device__ __forceinline__ float sum_rows(float v) {
-#pragma unroll
-    for (int o = CPR; o < WAVE; o <<= 1) v += __shfl_xor(v, o);
-    return v;
-}
-
-// Sums over the rows of a workgroup of two 8-channel values per thread; the
-// result is valid in the threads of the first row (threadIdx.x < CPR).
-__device__ __forceinline__ void reduce_rows(f32x8_t& a, f32x8_t& b, float (*lds)[CPR][16]) {
-    const int oct = threadIdx.x % CPR, wave = threadIdx.x / WAVE;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = sum_rows(a[j]), b[j] = sum_rows(b[j]);
-    if (threadIdx.x % WAVE < CPR)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) lds[wave][oct][j] = a[j], lds[wave][oct][8 + j] = b[j];
-    __syncthreads();
-    if (threadIdx.x < CPR)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            a[j] = lds[0][oct][j], b[j] = lds[0][oct][8 + j];
-#pragma unroll
-            for (int w = 1; w < NT / WAVE; ++w) a[j] += lds[w][oct][j], b[j] += lds[w][oct][8 + j];
-        }
-    __syncthreads();
-}
-
-// Calls f(sample, first row, end row) for every run of tile t.
-template <typename F>
-__device__ __forceinline__ void for_runs(const Segs& g, int t, F f) {
-    const int r0 = t * R, r1 = r0 + R < g.n ? r0 + R : g.n;
-    for (int s = g.find(r0); s < g.n_seg; ++s) {
-        int a = g.at(s), b = g.at(s + 1);
-        if (a >= r1) break;
-        a = a > r0 ? a : r0;
-        b = b < r1 ? b : r1;
-        if (a < b) f(s, a, b);
+// A thread's place: 8 channels from ch, rows rl, rl + RL, ... of a run.
+struct Place {
+    int tile, slab, rl, ch, c;   // c: ch within the slab
+    bool on;
+    __device__ __forceinline__ explicit Place(const NormArgs& p) {
+        tile = int(blockIdx.x) / p.k.nslab;
+        slab = int(blockIdx.x) - tile * p.k.nslab;
+        rl = int(threadIdx.x) / p.k.CPR;
+        c = (int(threadIdx.x) - rl * p.k.CPR) * 8;
+        ch = slab * p.k.CW + c;
+        on = rl < p.k.RL && ch < p.C;
+        if (!on) ch = 0;
     }
+};
+
+// Calls f(sample, first row, end row) for every run of a tile.  Lane i of
+// every wave reads the offset of sample s0 + i: one load, with up to 62
+// samples, instead of a search and a walk.
+template <typename F>
+__device__ __forceinline__ void for_runs(const NormArgs& p, int tile, F f) {
+    const Segs& g = p.segs;
+    const int r0 = tile * p.k.R, r1 = p.k.R < g.n - r0 ? r0 + p.k.R : g.n;
+    int s = g.n_seg < WAVE - 1 ? 0 : g.find(r0);
+    while (s < g.n_seg) {
+        const int i = s + int(threadIdx.x) % WAVE;
+        const int off = g.at(i < g.n_seg ? i : g.n_seg);
+        for (int j = 0; j < WAVE - 1 && s < g.n_seg; ++j, ++s) {
+            int a = __builtin_amdgcn_readlane(off, j), b = __builtin_amdgcn_readlane(off, j + 1);
+            if (a >= r1) return;
+            a = a > r0 ? a : r0;
+            b = b < r1 ? b : r1;
+            if (a < b) f(s, a, b);
+        }
+    }
+}
+
+// Sums over the rows of a workgroup of two values per channel: f(channel in
+// the slab, sum of a, sum of b) in one thread per channel.
+template <typename F>
+__device__ __forceinline__ void reduce_rows(const NormArgs& p, const Place& q, const f32x8_t& a, const f32x8_t& b, float2* lds,
+                                            float2* part, F f) {
+    const int CW = p.k.CW, RL = p.k.RL, parts = NT / CW, per = (RL + parts - 1) / parts;   // 8 or 9 rows
+    if (q.rl < RL) {
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(lds + q.rl * CW + q.c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = f32x4_t{a[2 * j], b[2 * j], a[2 * j + 1], b[2 * j + 1]};
+    }
+    __syncthreads();
+    const int i = int(threadIdx.x) / CW, c = int(threadIdx.x) - i * CW;
+    if (i < parts) {
+        float2 t{0.f, 0.f};
+        for (int r = i * per; r < (i + 1) * per && r < RL; ++r) t.x += lds[r * CW + c].x, t.y += lds[r * CW + c].y;
+        part[i * CW + c] = t;
+    }
+    __syncthreads();
+    if (i == 0) {
+        float2 t = part[c];
+        for (int r = 1; r < parts; ++r) t.x += part[r * CW + c].x, t.y += part[r * CW + c].y;
+        f(c, t.x, t.y);
+    }
+    __syncthreads();
 }
 
 // Mean and sum of squared differences of every run, per channel.  The sums
@@ -78,267 +121,336 @@ __device__ __forceinline__ void for_runs(const Segs& g, int t, F f) {
 template <typename TT>
 __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, NormArgs p, float2* __restrict__ part) {
     using S = typename TT::storage;
-    __shared__ float lds[NT / WAVE][CPR][16];
+    __shared__ float2 lds[NT * 8], sums[NT];
+    __shared__ float base[8 * OPR];
     const S* x = static_cast<const S*>(x_);
-    const int oct = blockIdx.y * CPR + threadIdx.x % CPR, rl = threadIdx.x / CPR;
-    const bool on = oct * 8 < p.C;
-    const int ch = on ? oct * 8 : 0;
-    for_runs(p.segs, blockIdx.x, [&](int s, int a, int b) {
-        const f32x8_t k = widen<TT>(ld8<TT>(x + int64_t(a) * p.C + ch));
+    const Place q(p);
+    for_runs(p, q.tile, [&](int s, int a, int b) {
+        const f32x8_t k = widen<TT>(ld8<TT>(x + int64_t(a) * p.C + q.ch));
+        if (q.rl == 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) base[q.c + j] = k[j];
         f32x8_t s1 = 0.f, s2 = 0.f;
-        for (int r = a + rl; r < b; r += RL) {
-            const f32x8_t d = widen<TT>(ld8<TT>(x + int64_t(r) * p.C + ch)) - k;
-            s1 += d;
-            s2 += d * d;
+        for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
+            Raw8<TT> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {   // beyond the end: the last row once more, not counted
+                const int ru = r + u * p.k.RL;
+                v[u] = ld8<TT>(x + int64_t(ru < b ? ru : b - 1) * p.C + q.ch);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * p.k.RL < b) {
+                    const f32x8_t d = widen<TT>(v[u]) - k;
+                    s1 += d;
+                    s2 += d * d;
+                }
         }
-        reduce_rows(s1, s2, lds);
-        if (rl == 0 && on) {
-            float2* o = part + int64_t(blockIdx.x + s) * p.C + ch;
-            const float inv = 1.f / float(b - a);
+        reduce_rows(p, q, s1, s2, lds, sums, [&](int c, float t1, float t2) {
+            if (q.slab * p.k.CW + c >= p.C) return;
+            const float m = t1 / float(b - a), m2 = t2 - t1 * m;
+            part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + c] = float2{base[c] + m, m2 > 0.f || m2 != m2 ? m2 : 0.f};
+        });
+    });
+}
+
+// Sums of two doubles over a workgroup, in every thread.
+constexpr int NG = 512;   // threads of the reductions across runs
+__device__ __forceinline__ void sum_block(double& a, double& b, double2* lds) {
+#pragma unroll
+    for (int o = 1; o < WAVE; o <<= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
+    if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = double2{a, b};
+    __syncthreads();
+    a = lds[0].x, b = lds[0].y;
+#pragma unroll
+    for (int w = 1; w < NG / WAVE; ++w) a += lds[w].x, b += lds[w].y;
+}
+
+// Calls f(slot, rows, channel) for the runs and channels of (sample, group),
+// a workgroup's threads side by side over the channels, then over the runs.
+template <typename F>
+__device__ __forceinline__ void for_parts(const NormArgs& p, int s, int g, F f) {
+    const int a = p.segs.at(s), b = p.segs.at(s + 1), cg = p.C / p.G, R = p.k.R;
+    if (a >= b) return;
+    const int w = cg < NG ? cg : NG, i = int(threadIdx.x) / w, step = NG / w;
+    if (i >= step) return;
+    for (int c = int(threadIdx.x) - i * w; c < cg; c += w)
+        for (int t = a / R + i; t <= (b - 1) / R; t += step) {
+            const int ra = a > t * R ? a : t * R, rb = b - t * R < R ? b : (t + 1) * R;
+            f(int64_t(t) + s, rb - ra, g * cg + c);
+        }
+}
+
+// Group mean and reciprocal deviation from the runs' means and spreads, whose
+// squares are taken around the first of the means; an empty sample gets mean 0
+// and variance 0.
+__global__ __launch_bounds__(NG) void k_norm_group(NormArgs p, const float2* __restrict__ part, float2* __restrict__ stats) {
+    __shared__ double2 lds[NG / WAVE];
+    const int s = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
+    const int a = p.segs.at(s), b = p.segs.at(s + 1);
+    double mean = 0, var = 0;
+    if (a < b) {
+        const double k = part[(int64_t(a / p.k.R) + s) * p.C + g * (p.C / p.G)].x;
+        double s1 = 0, s2 = 0;
+        for_parts(p, s, g, [&](int64_t slot, int rows, int c) {
+            const float2 v = part[slot * p.C + c];
+            const double d = double(v.x) - k;
+            s1 += double(rows) * d;
+            s2 += double(v.y) + double(rows) * d * d;
+        });
+        sum_block(s1, s2, lds);
+        const double cnt = double(b - a) * (p.C / p.G), m = s1 / cnt;
+        mean = k + m;
+        var = s2 / cnt - m * m;
+        var = var > 0 || var != var ? var : 0;
+    }
+    if (threadIdx.x == 0) stats[blockIdx.x] = float2{float(mean), float(1.0 / sqrt(var + double(p.eps)))};
+}
+
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+}
+// act(z), and act'(z) in the second form.
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+    if (ACT == SPC_ACT_RELU) return z < 0.f ? 0.f : z;
+    if (ACT == SPC_ACT_SILU) return z * sigmoid(z);
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float act_d(float z) {
+    if (ACT == SPC_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (ACT == SPC_ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    return 1.f;
+}
+
+// The constants of a thread's eight channels: a run's mean and rstd (of the
+// channel's group), and z = scale (x - mean) + beta.
+struct Chan8 {
+    f32x8_t gamma, beta, mean, rstd, scale;
+    int cg, g0, first;   // channels per group, the first channel's group, and its place there
+    __device__ __forceinline__ Chan8(const NormArgs& p, const float* g, const float* b, int ch) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gamma[j] = g ? g[ch + j] : 1.f, beta[j] = b ? b[ch + j] : 0.f;
+        cg = p.C / p.G;
+        g0 = ch / cg;
+        first = ch - g0 * cg;
+    }
+    // v[j] = the pair of channel j's group
+    template <typename F>
+    __device__ __forceinline__ void groups(const float2* row, F f) const {
+        if (cg % 8 == 0) {
+            const float2 v = row[g0];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f(j, v);
+        } else {
+            int g = g0, i = first;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float m = s1[j] * inv, m2 = s2[j] - s1[j] * m;
-                o[j] = float2{k[j] + m, m2 > 0.f || m2 != m2 ? m2 : 0.f};
+                f(j, row[g]);
+                if (++i == cg) i = 0, ++g;
+            }
+        }
+    }
+    __device__ __forceinline__ void run(const float2* stats, int s, int G) {
+        groups(stats + int64_t(s) * G, [&](int j, const float2& v) { mean[j] = v.x, rstd[j] = v.y, scale[j] = v.y * gamma[j]; });
+    }
+};
+
+template <typename TT, int ACT, bool DROP>
+__global__ __launch_bounds__(NT) void k_norm_apply(const void* x_, NormArgs p, const float* __restrict__ gamma,
+                                                   const float* __restrict__ beta, const float2* __restrict__ stats, void* y_) {
+    using S = typename TT::storage;
+    const S* x = static_cast<const S*>(x_);
+    S* y = static_cast<S*>(y_);
+    const Place q(p);
+    const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
+    Chan8 c(p, gamma, beta, q.ch);
+    for_runs(p, q.tile, [&](int s, int a, int b) {
+        c.run(stats, s, p.G);
+        for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
+            Raw8<TT> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int ru = r + u * p.k.RL;
+                v[u] = ld8<TT>(x + int64_t(ru < b ? ru : b - 1) * p.C + q.ch);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = int64_t(r + u * p.k.RL) * p.C + q.ch;
+                if (r + u * p.k.RL >= b) break;
+                f32x8_t z = widen<TT>(v[u]) - c.mean;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = act_f<ACT>(fmaf(z[j], c.scale[j], c.beta[j]));
+                if (DROP) z = drop8(z, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr, p.drop.scale);
+                st8<TT>(y + i, narrow<TT>(z));
             }
         }
     });
 }
 
-// Sum of a double over a workgroup, in every thread.
-__device__ __forceinline__ double sum_block(double v, double* lds) {
+// d = x - mean and dz of eight elements.
+template <typename TT, int ACT, bool DROP>
+__device__ __forceinline__ void grad8(const Raw8<TT>& x, const Raw8<TT>& dy, const Chan8& c, const NormArgs& p, uint64_t seed,
+                                      uint64_t offset, int64_t i, f32x8_t& d, f32x8_t& dz) {
+    d = widen<TT>(x) - c.mean;
+    dz = widen<TT>(dy);
+    if (DROP) dz = drop8(dz, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr, p.drop.scale);
 #pragma unroll
-    for (int o = 1; o < WAVE; o <<= 1) v += __shfl_xor(v, o);
-    if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = v;
-    __syncthreads();
-    double t = lds[0];
-#pragma unroll
-    for (int w = 1; w < NT / WAVE; ++w) t += lds[w];
-    __syncthreads();
-    return t;
+    for (int j = 0; j < 8; ++j) dz[j] *= act_d<ACT>(fmaf(d[j], c.scale[j], c.beta[j]));
 }
 
-// Calls f(slot, rows, channel) for the runs and channels of (sample, group).
-template <typename F>
-__device__ __forceinline__ void for_parts(const NormArgs& p, int s, int g, F f) {
-    const int a = p.segs.at(s), b = p.segs.at(s + 1), cg = p.C / p.G;
-    if (a >= b) return;
-    const int t0 = a / R, nt = (b - 1) / R - t0 + 1;
-    for (int64_t i = threadIdx.x; i < int64_t(nt) * cg; i += NT) {
-        const int q = int(i / cg), t = t0 + q;
-        const int ra = a > t * R ? a : t * R, rb = b < (t + 1) * R ? b : (t + 1) * R;
-        f(int64_t(t) + s, rb - ra, g * cg + int(i - int64_t(q) * cg));
-    }
-}
-
-// Group mean and reciprocal deviation from the runs' means and spreads; an
-// empty sample gets mean 0 and variance 0.
-__global__ __launch_bounds__(NT) void k_norm_group(NormArgs p, const float2* __restrict__ part, float2* __restrict__ stats) {
-    __shared__ double lds[NT / WAVE];
-    const int s = blockIdx.x, g = blockIdx.y;
-    double sum = 0, cnt = 0;
-    for_parts(p, s, g, [&](int64_t slot, int rows, int c) {
-        sum += double(rows) * part[slot * p.C + c].x;
-        cnt += rows;
-    });
-    sum = sum_block(sum, lds);
-    cnt = sum_block(cnt, lds);
-    const double mean = cnt > 0 ? sum / cnt : 0.0;
-    double m2 = 0;
-    for_parts(p, s, g, [&](int64_t slot, int rows, int c) {
-        const float2 v = part[slot * p.C + c];
-        const double d = double(v.x) - mean;
-        m2 += double(v.y) + double(rows) * d * d;
-    });
-    m2 = sum_block(m2, lds);
-    if (threadIdx.x == 0)
-        stats[int64_t(s) * p.G + g] = float2{float(mean), float(1.0 / sqrt((cnt > 0 ? m2 / cnt : 0.0) + double(p.eps)))};
-}
-
-// act(z), and act'(z) in the second form.
-__device__ __forceinline__ float act_f(float z, int act) {
-    if (act == SPC_ACT_RELU) return z < 0.f ? 0.f : z;
-    if (act == SPC_ACT_SILU) return z / (1.f + __expf(-z));
-    return z;
-}
-__device__ __forceinline__ float act_d(float z, int act) {
-    if (act == SPC_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (act == SPC_ACT_SILU) {
-        const float s = 1.f / (1.f + __expf(-z));
-        return s * (1.f + z * (1.f - s));
-    }
-    return 1.f;
-}
-
-// One run's constants of a thread's eight channels.
-struct Chan8 {
-    f32x8_t mean, rstd, gamma, beta;
-    __device__ __forceinline__ void affine(const float* g, const float* b, int ch) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) gamma[j] = g ? g[ch + j] : 1.f, beta[j] = b ? b[ch + j] : 0.f;
-    }
-    __device__ __forceinline__ void stats(const float2* st, int s, int G, int cg, int ch) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 v = st[int64_t(s) * G + (ch + j) / cg];
-            mean[j] = v.x, rstd[j] = v.y;
-        }
-    }
-};
-
-template <typename TT>
-__global__ __launch_bounds__(NT) void k_norm_apply(const void* x_, NormArgs p, const float* __restrict__ gamma,
-                                                   const float* __restrict__ beta, const float2* __restrict__ stats, int act,
-                                                   void* y_) {
-    using S = typename TT::storage;
-    const S* x = static_cast<const S*>(x_);
-    S* y = static_cast<S*>(y_);
-    const int oct = blockIdx.y * CPR + threadIdx.x % CPR, rl = threadIdx.x / CPR;
-    const bool on = oct * 8 < p.C;
-    const int ch = on ? oct * 8 : 0;
-    const uint64_t seed = p.drop.rng ? p.drop.rng[0] : 0, offset = p.drop.rng ? p.drop.rng[1] : 0;
-    Chan8 c;
-    c.affine(gamma, beta, ch);
-    for_runs(p.segs, blockIdx.x, [&](int s, int a, int b) {
-        c.stats(stats, s, p.G, p.C / p.G, ch);
-        for (int r = a + rl; r < b && on; r += RL) {
-            const int64_t i = int64_t(r) * p.C + ch;
-            f32x8_t z = (widen<TT>(ld8<TT>(x + i)) - c.mean) * c.rstd * c.gamma + c.beta;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] = act_f(z[j], act);
-            if (p.drop.rng) z = drop8(z, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr, p.drop.scale);
-            st8<TT>(y + i, narrow<TT>(z));
-        }
-    });
-}
-
-// xhat and dz of eight elements.
-template <typename TT>
-__device__ __forceinline__ void grad8(const void* x, const void* dy, const Chan8& c, const NormArgs& p, uint64_t seed,
-                                      uint64_t offset, int64_t i, int act, f32x8_t& xhat, f32x8_t& dz) {
-    using S = typename TT::storage;
-    xhat = (widen<TT>(ld8<TT>(static_cast<const S*>(x) + i)) - c.mean) * c.rstd;
-    dz = widen<TT>(ld8<TT>(static_cast<const S*>(dy) + i));
-    if (p.drop.rng) dz = drop8(dz, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr, p.drop.scale);
-    const f32x8_t z = xhat * c.gamma + c.beta;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dz[j] *= act_d(z[j], act);
-}
-
-// Sums of dz and dz * xhat of every run, per channel.
-template <typename TT>
-__global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x, const void* __restrict__ dy, NormArgs p,
+// Sums of dz and dz * xhat of every run, and (tot, NULL ok) of every tile, per channel.
+template <typename TT, int ACT, bool DROP>
+__global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x_, const void* __restrict__ dy_, NormArgs p,
                                                       const float* __restrict__ gamma, const float* __restrict__ beta,
-                                                      const float2* __restrict__ stats, int act, float2* __restrict__ part) {
-    __shared__ float lds[NT / WAVE][CPR][16];
-    const int oct = blockIdx.y * CPR + threadIdx.x % CPR, rl = threadIdx.x / CPR;
-    const bool on = oct * 8 < p.C;
-    const int ch = on ? oct * 8 : 0;
-    const uint64_t seed = p.drop.rng ? p.drop.rng[0] : 0, offset = p.drop.rng ? p.drop.rng[1] : 0;
-    Chan8 c;
-    c.affine(gamma, beta, ch);
-    for_runs(p.segs, blockIdx.x, [&](int s, int a, int b) {
-        c.stats(stats, s, p.G, p.C / p.G, ch);
+                                                      const float2* __restrict__ stats, float2* __restrict__ part,
+                                                      float2* __restrict__ tot) {
+    using S = typename TT::storage;
+    __shared__ float2 lds[NT * 8], sums[NT];
+    const S *x = static_cast<const S*>(x_), *dy = static_cast<const S*>(dy_);
+    const Place q(p);
+    const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
+    Chan8 c(p, gamma, beta, q.ch);
+    float2 t{0.f, 0.f};
+    for_runs(p, q.tile, [&](int s, int a, int b) {
+        c.run(stats, s, p.G);
         f32x8_t s1 = 0.f, s2 = 0.f;
-        for (int r = a + rl; r < b; r += RL) {
-            f32x8_t xhat, dz;
-            grad8<TT>(x, dy, c, p, seed, offset, int64_t(r) * p.C + ch, act, xhat, dz);
-            s1 += dz;
-            s2 += dz * xhat;
-        }
-        reduce_rows(s1, s2, lds);
-        if (rl == 0 && on) {
-            float2* o = part + int64_t(blockIdx.x + s) * p.C + ch;
+        for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
+            Raw8<TT> v[U], w[U];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = float2{s1[j], s2[j]};
+            for (int u = 0; u < U; ++u) {
+                const int ru = r + u * p.k.RL;
+                const int64_t i = int64_t(ru < b ? ru : b - 1) * p.C + q.ch;
+                v[u] = ld8<TT>(x + i);
+                w[u] = ld8<TT>(dy + i);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r + u * p.k.RL >= b) break;
+                f32x8_t d, dz;
+                grad8<TT, ACT, DROP>(v[u], w[u], c, p, seed, offset, int64_t(r + u * p.k.RL) * p.C + q.ch, d, dz);
+                s1 += dz;
+                s2 += dz * d;
+            }
         }
+        s2 *= c.rstd;
+        reduce_rows(p, q, s1, s2, lds, sums, [&](int k, float t1, float t2) {
+            if (q.slab * p.k.CW + k >= p.C) return;
+            part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + k] = float2{t1, t2};
+            t.x += t1, t.y += t2;
+        });
     });
+    if (tot && int(threadIdx.x) < p.k.CW && q.slab * p.k.CW + int(threadIdx.x) < p.C)
+        tot[int64_t(q.tile) * p.C + q.slab * p.k.CW + threadIdx.x] = t;
 }
 
 // Workgroups [0, samples * G): the group's means of gamma dz and gamma dz
-// xhat.  Workgroups after them: one channel's dbeta and dgamma each.
-__global__ __launch_bounds__(NT) void k_norm_bwd_group(NormArgs p, const float* __restrict__ gamma,
-                                                       const float2* __restrict__ part, float2* __restrict__ means,
-                                                       float* __restrict__ dgamma, float* __restrict__ dbeta) {
-    __shared__ double lds[NT / WAVE];
+// xhat.  Workgroups after them: dbeta and dgamma of 8 channels each.
+__global__ __launch_bounds__(NG) void k_norm_bwd_group(NormArgs p, const float* __restrict__ gamma,
+                                                       const float2* __restrict__ part, const float2* __restrict__ tot,
+                                                       float2* __restrict__ means, float* __restrict__ dgamma,
+                                                       float* __restrict__ dbeta) {
+    __shared__ double2 lds[NG / WAVE];
     const int64_t groups = int64_t(p.segs.n_seg) * p.G;
-    double a = 0, b = 0, cnt = 0;
+    double a = 0, b = 0;
     if (int64_t(blockIdx.x) < groups) {
         const int s = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
-        for_parts(p, s, g, [&](int64_t slot, int rows, int c) {
+        for_parts(p, s, g, [&](int64_t slot, int, int c) {
             const float2 v = part[slot * p.C + c];
             const double w = gamma ? gamma[c] : 1.f;
             a += w * v.x;
             b += w * v.y;
-            cnt += rows;
         });
-        a = sum_block(a, lds);
-        b = sum_block(b, lds);
-        cnt = sum_block(cnt, lds);
+        sum_block(a, b, lds);
+        const double cnt = double(p.segs.at(s + 1) - p.segs.at(s)) * (p.C / p.G);
         if (threadIdx.x == 0) means[blockIdx.x] = cnt > 0 ? float2{float(a / cnt), float(b / cnt)} : float2{0.f, 0.f};
         return;
     }
-    const int c = int(blockIdx.x - groups);
-    for (int s = 0; s < p.segs.n_seg; ++s) {
-        const int ra = p.segs.at(s), rb = p.segs.at(s + 1);
-        if (ra >= rb) continue;
-        for (int t = ra / R + int(threadIdx.x); t <= (rb - 1) / R; t += NT) {
-            const float2 v = part[(int64_t(t) + s) * p.C + c];
-            a += v.x;
-            b += v.y;
-        }
+    const int c = int(blockIdx.x - groups) * 8 + int(threadIdx.x) % 8;
+#pragma unroll 4
+    for (int t = int(threadIdx.x) / 8; t < p.k.tiles; t += NG / 8) {
+        const float2 v = tot[int64_t(t) * p.C + c];
+        a += v.x;
+        b += v.y;
     }
-    a = sum_block(a, lds);
-    b = sum_block(b, lds);
-    if (threadIdx.x == 0) {
+    // 8 channels side by side: over the lanes 8 apart, then over the waves
+#pragma unroll
+    for (int o = 8; o < WAVE; o <<= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
+    __shared__ double2 ch[NG / WAVE][8];
+    if (threadIdx.x % WAVE < 8) ch[threadIdx.x / WAVE][threadIdx.x % WAVE] = double2{a, b};
+    __syncthreads();
+    if (threadIdx.x < 8) {
+        a = b = 0;
+#pragma unroll
+        for (int w = 0; w < NG / WAVE; ++w) a += ch[w][threadIdx.x].x, b += ch[w][threadIdx.x].y;
         if (dbeta) dbeta[c] = float(a);
         if (dgamma) dgamma[c] = float(b);
     }
 }
 
-template <typename TT>
-__global__ __launch_bounds__(NT) void k_norm_bwd_apply(const void* __restrict__ x, const void* dy, NormArgs p,
+template <typename TT, int ACT, bool DROP>
+__global__ __launch_bounds__(NT) void k_norm_bwd_apply(const void* __restrict__ x_, const void* dy_, NormArgs p,
                                                        const float* __restrict__ gamma, const float* __restrict__ beta,
                                                        const float2* __restrict__ stats, const float2* __restrict__ means,
-                                                       int act, void* dx_) {
+                                                       void* dx_) {
     using S = typename TT::storage;
+    const S *x = static_cast<const S*>(x_), *dy = static_cast<const S*>(dy_);
     S* dx = static_cast<S*>(dx_);
-    const int oct = blockIdx.y * CPR + threadIdx.x % CPR, rl = threadIdx.x / CPR;
-    const bool on = oct * 8 < p.C;
-    const int ch = on ? oct * 8 : 0, cg = p.C / p.G;
-    const uint64_t seed = p.drop.rng ? p.drop.rng[0] : 0, offset = p.drop.rng ? p.drop.rng[1] : 0;
-    Chan8 c;
-    c.affine(gamma, beta, ch);
-    for_runs(p.segs, blockIdx.x, [&](int s, int a, int b) {
-        c.stats(stats, s, p.G, cg, ch);
-        f32x8_t m1, m2;
+    const Place q(p);
+    const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
+    Chan8 c(p, gamma, beta, q.ch);
+    for_runs(p, q.tile, [&](int s, int a, int b) {
+        c.run(stats, s, p.G);
+        // dx = scale dz - (rstd m1 + rstd^2 m2 (x - mean))
+        f32x8_t k1, k2;
+        c.groups(means + int64_t(s) * p.G, [&](int j, const float2& v) { k1[j] = c.rstd[j] * v.x, k2[j] = c.rstd[j] * c.rstd[j] * v.y; });
+        for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
+            Raw8<TT> v[U], w[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 v = means[int64_t(s) * p.G + (ch + j) / cg];
-            m1[j] = v.x, m2[j] = v.y;
-        }
-        for (int r = a + rl; r < b && on; r += RL) {
-            const int64_t i = int64_t(r) * p.C + ch;
-            f32x8_t xhat, dz;
-            grad8<TT>(x, dy, c, p, seed, offset, i, act, xhat, dz);
-            st8<TT>(dx + i, narrow<TT>((dz * c.gamma - m1 - xhat * m2) * c.rstd));
+            for (int u = 0; u < U; ++u) {
+                const int ru = r + u * p.k.RL;
+                const int64_t i = int64_t(ru < b ? ru : b - 1) * p.C + q.ch;
+                v[u] = ld8<TT>(x + i);
+                w[u] = ld8<TT>(dy + i);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r + u * p.k.RL >= b) break;
+                const int64_t i = int64_t(r + u * p.k.RL) * p.C + q.ch;
+                f32x8_t d, dz;
+                grad8<TT, ACT, DROP>(v[u], w[u], c, p, seed, offset, i, d, dz);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dz[j] = fmaf(c.scale[j], dz[j], -fmaf(k2[j], d[j], k1[j]));
+                st8<TT>(dx + i, narrow<TT>(dz));
+            }
         }
     });
 }
 
 struct NormWs {
-    int64_t tiles, part, stats;  // counts: row tiles, float2 of the partial sums, float2 of the group values
-    size_t bytes() const { return align_up(size_t(part) * 8, 256) + size_t(stats) * 8; }
+    Cut k;
+    int64_t part, tot, stats;  // counts of float2: the runs' sums, the tiles' sums, the group values
+    size_t bytes() const { return align_up(size_t(part) * 8, 256) + align_up(size_t(tot) * 8, 256) + size_t(stats) * 8; }
+    float2* tot_of(void* ws) const { return reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(size_t(part) * 8, 256)); }
+    float2* means_of(void* ws) const {
+        return reinterpret_cast<float2*>(reinterpret_cast<char*>(tot_of(ws)) + align_up(size_t(tot) * 8, 256));
+    }
 };
 
 spc_status check_sizes(int64_t n, int32_t C, int32_t G, int64_t n_seg, NormWs& w) {
-    if (n < 0 || n >= (int64_t(1) << 31) - R) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
+    if (n < 0 || n >= (int64_t(1) << 31) - 8192) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
     if (n_seg < 1 || n_seg >= (int64_t(1) << 31) - 1) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)n_seg);
     if (C <= 0 || C % 16) return fail(SPC_ERR_UNSUPPORTED, "C=%d: channels must be a positive multiple of 16", C);
     if (G < 1 || C % G) return fail(SPC_ERR_ARG, "groups=%d does not divide C=%d", G, C);
-    if (ceil_div(C, 64) > 65535 || G > 65535) return fail(SPC_ERR_UNSUPPORTED, "C=%d is beyond one launch", C);
-    w.tiles = ceil_div(n, R);
-    w.part = (w.tiles + n_seg) * C;
+    w.k = cut_of(n, C);
+    w.part = (w.k.tiles + n_seg) * C;
+    w.tot = int64_t(w.k.tiles) * C;
     w.stats = n_seg * G;
+    if (int64_t(w.k.tiles) * w.k.nslab >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
     if (w.stats + C >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld groups are beyond one launch", (long long)w.stats);
     return SPC_OK;
 }
@@ -354,25 +466,37 @@ spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int32_t G, const in
     if (!ws || !aligned16(ws)) return fail(SPC_ERR_ARG, "ws is NULL or not 16-byte aligned");
     if (ws_bytes < w.bytes()) return fail(SPC_ERR_WORKSPACE, "ws_bytes=%zu, need %zu", ws_bytes, w.bytes());
     p.segs = Segs{seg_ptr, int32_t(n_seg), int32_t(n)};
-    p.C = C, p.G = G, p.eps = 0.f;
+    p.C = C, p.G = G, p.eps = 0.f, p.k = w.k;
     return make_drop(drop, p.drop);
 }
+
+// One kernel of the activations' and dropout's variants.
+#define NORM_VARIANT(name, ...)                                                                              \
+    do {                                                                                                      \
+        const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));                                           \
+        if (p.drop.rng) {                                                                                     \
+            if (act == SPC_ACT_RELU) hipLaunchKernelGGL((name<TT, SPC_ACT_RELU, true>), grid, dim3(NT), 0, stream, __VA_ARGS__);  \
+            else if (act == SPC_ACT_SILU) hipLaunchKernelGGL((name<TT, SPC_ACT_SILU, true>), grid, dim3(NT), 0, stream, __VA_ARGS__); \
+            else hipLaunchKernelGGL((name<TT, SPC_ACT_NONE, true>), grid, dim3(NT), 0, stream, __VA_ARGS__);  \
+        } else {                                                                                              \
+            if (act == SPC_ACT_RELU) hipLaunchKernelGGL((name<TT, SPC_ACT_RELU, false>), grid, dim3(NT), 0, stream, __VA_ARGS__); \
+            else if (act == SPC_ACT_SILU) hipLaunchKernelGGL((name<TT, SPC_ACT_SILU, false>), grid, dim3(NT), 0, stream, __VA_ARGS__); \
+            else hipLaunchKernelGGL((name<TT, SPC_ACT_NONE, false>), grid, dim3(NT), 0, stream, __VA_ARGS__); \
+        }                                                                                                     \
+        SPC_LAUNCHED(#name);                                                                                  \
+    } while (0)
 
 template <typename TT>
 spc_status launch_fwd(const void* x, const NormArgs& p, const NormWs& w, const float* gamma, const float* beta, int act,
                       void* y, float2* stats, void* ws, hipStream_t stream) {
     float2* part = static_cast<float2*>(ws);
-    const dim3 grid(unsigned(w.tiles), unsigned(ceil_div(p.C, 8 * CPR)));
-    if (w.tiles) {
-        hipLaunchKernelGGL(k_norm_stats<TT>, grid, dim3(NT), 0, stream, x, p, part);
+    if (p.k.tiles) {
+        hipLaunchKernelGGL(k_norm_stats<TT>, dim3(unsigned(p.k.tiles) * unsigned(p.k.nslab)), dim3(NT), 0, stream, x, p, part);
         SPC_LAUNCHED("k_norm_stats");
     }
-    hipLaunchKernelGGL(k_norm_group, dim3(unsigned(p.segs.n_seg), unsigned(p.G)), dim3(NT), 0, stream, p, part, stats);
+    hipLaunchKernelGGL(k_norm_group, dim3(unsigned(w.stats)), dim3(NG), 0, stream, p, part, stats);
     SPC_LAUNCHED("k_norm_group");
-    if (w.tiles) {
-        hipLaunchKernelGGL(k_norm_apply<TT>, grid, dim3(NT), 0, stream, x, p, gamma, beta, stats, act, y);
-        SPC_LAUNCHED("k_norm_apply");
-    }
+    if (p.k.tiles) NORM_VARIANT(k_norm_apply, x, p, gamma, beta, stats, y);
     return SPC_OK;
 }
 
@@ -380,20 +504,13 @@ template <typename TT>
 spc_status launch_bwd(const void* dy, const void* x, const NormArgs& p, const NormWs& w, const float* gamma,
                       const float* beta, const float2* stats, int act, void* dx, float* dgamma, float* dbeta, void* ws,
                       hipStream_t stream) {
-    float2* part = static_cast<float2*>(ws);
-    float2* means = reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(size_t(w.part) * 8, 256));
-    const dim3 grid(unsigned(w.tiles), unsigned(ceil_div(p.C, 8 * CPR)));
-    if (w.tiles) {
-        hipLaunchKernelGGL(k_norm_bwd_sums<TT>, grid, dim3(NT), 0, stream, x, dy, p, gamma, beta, stats, act, part);
-        SPC_LAUNCHED("k_norm_bwd_sums");
-    }
-    const int64_t blocks = w.stats + (dgamma || dbeta ? p.C : 0);
-    hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(blocks)), dim3(NT), 0, stream, p, gamma, part, means, dgamma, dbeta);
+    const bool affine = dgamma || dbeta;
+    float2 *part = static_cast<float2*>(ws), *tot = affine ? w.tot_of(ws) : nullptr, *means = w.means_of(ws);
+    if (p.k.tiles) NORM_VARIANT(k_norm_bwd_sums, x, dy, p, gamma, beta, stats, part, tot);
+    const int64_t blocks = w.stats + (affine ? p.C / 8 : 0);
+    hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(blocks)), dim3(NG), 0, stream, p, gamma, part, tot, means, dgamma, dbeta);
     SPC_LAUNCHED("k_norm_bwd_group");
-    if (w.tiles) {
-        hipLaunchKernelGGL(k_norm_bwd_apply<TT>, grid, dim3(NT), 0, stream, x, dy, p, gamma, beta, stats, means, act, dx);
-        SPC_LAUNCHED("k_norm_bwd_apply");
-    }
+    if (p.k.tiles) NORM_VARIANT(k_norm_bwd_apply, x, dy, p, gamma, beta, stats, means, dx);
     return SPC_OK;
 }
 
