@@ -24,7 +24,7 @@ __global__ __launch_bounds__(DT) void k_dropout(const void* x_, const void* res_
         const int64_t i = g * 8;
         const u32x4 bits = philox(seed, offset + uint64_t(g), d.layer);
         if (i + 8 <= numel) {
-            f32x8_t v = drop8(widen<TT>(ld8<TT>(x + i)), bits, d.thr, d.scale);
+            f32x8_t v = drop8(widen<TT>(ld8<TT>(x + i)) * d.scale, bits, d.thr);
             if constexpr (RES) v += widen<TT>(ld8<TT>(res + i));
             st8<TT>(out + i, narrow<TT>(v));
         } else {  // the last, short group, element by element
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(DT) void k_dropout(const void* x_, const void* res_
                 reinterpret_cast<S*>(&rx)[j] = x[i + j];
                 if constexpr (RES) reinterpret_cast<S*>(&rr)[j] = res[i + j];
             }
-            f32x8_t v = drop8(widen<TT>(rx), bits, d.thr, d.scale);
+            f32x8_t v = drop8(widen<TT>(rx) * d.scale, bits, d.thr);
             if constexpr (RES) v += widen<TT>(rr);
             const Raw8<TT> ro = narrow<TT>(v);
 #pragma unroll

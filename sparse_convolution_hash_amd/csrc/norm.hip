@@ -207,21 +207,24 @@ __global__ __launch_bounds__(NG) void k_norm_group(NormArgs p, const float2* __r
     if (threadIdx.x == 0) stats[blockIdx.x] = float2{float(mean), float(1.0 / sqrt(var + double(p.eps)))};
 }
 
-__device__ __forceinline__ float sigmoid(float z) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+// v sigmoid(z), v = 1 / inv
+__device__ __forceinline__ float sigmoid(float z, float inv) {
+    const float e = __builtin_amdgcn_exp2f(-1.44269504f * z);
+    return __builtin_amdgcn_rcpf(fmaf(e, inv, inv));
 }
-// act(z), and act'(z) in the second form.
+// act(z) / inv of an activation that scales with its argument (z comes
+// multiplied) or of silu, and act'(z) in the second form.
 template <int ACT>
-__device__ __forceinline__ float act_f(float z) {
+__device__ __forceinline__ float act_f(float z, float inv) {
     if (ACT == SPC_ACT_RELU) return z < 0.f ? 0.f : z;
-    if (ACT == SPC_ACT_SILU) return z * sigmoid(z);
+    if (ACT == SPC_ACT_SILU) return z * sigmoid(z, inv);
     return z;
 }
 template <int ACT>
 __device__ __forceinline__ float act_d(float z) {
     if (ACT == SPC_ACT_RELU) return z > 0.f ? 1.f : 0.f;
     if (ACT == SPC_ACT_SILU) {
-        const float s = sigmoid(z);
+        const float s = sigmoid(z, 1.f);
         return s * fmaf(z, 1.f - s, 1.f);
     }
     return 1.f;
@@ -269,6 +272,8 @@ __global__ __launch_bounds__(NT) void k_norm_apply(const void* x_, NormArgs p, c
     const Place q(p);
     const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
     Chan8 c(p, gamma, beta, q.ch);
+    // dropout's factor goes into the affine step, silu's into its division
+    if (DROP && ACT != SPC_ACT_SILU) c.gamma *= p.drop.scale, c.beta *= p.drop.scale;
     for_runs(p, q.tile, [&](int s, int a, int b) {
         c.run(stats, s, p.G);
         for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
@@ -284,21 +289,21 @@ __global__ __launch_bounds__(NT) void k_norm_apply(const void* x_, NormArgs p, c
                 if (r + u * p.k.RL >= b) break;
                 f32x8_t z = widen<TT>(v[u]) - c.mean;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = act_f<ACT>(fmaf(z[j], c.scale[j], c.beta[j]));
-                if (DROP) z = drop8(z, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr, p.drop.scale);
+                for (int j = 0; j < 8; ++j) z[j] = act_f<ACT>(fmaf(z[j], c.scale[j], c.beta[j]), DROP ? p.drop.inv : 1.f);
+                if (DROP) z = drop8(z, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr);
                 st8<TT>(y + i, narrow<TT>(z));
             }
         }
     });
 }
 
-// d = x - mean and dz of eight elements.
+// d = x - mean and dz / (dropout's factor) of eight elements.
 template <typename TT, int ACT, bool DROP>
 __device__ __forceinline__ void grad8(const Raw8<TT>& x, const Raw8<TT>& dy, const Chan8& c, const NormArgs& p, uint64_t seed,
                                       uint64_t offset, int64_t i, f32x8_t& d, f32x8_t& dz) {
     d = widen<TT>(x) - c.mean;
     dz = widen<TT>(dy);
-    if (DROP) dz = drop8(dz, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr, p.drop.scale);
+    if (DROP) dz = drop8(dz, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dz[j] *= act_d<ACT>(fmaf(d[j], c.scale[j], c.beta[j]));
 }
@@ -337,7 +342,8 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
                 s2 += dz * d;
             }
         }
-        s2 *= c.rstd;
+        s1 *= p.drop.scale;
+        s2 *= c.rstd * p.drop.scale;
         reduce_rows(p, q, s1, s2, lds, sums, [&](int k, float t1, float t2) {
             if (q.slab * p.k.CW + k >= p.C) return;
             part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + k] = float2{t1, t2};
@@ -407,6 +413,7 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_apply(const void* __restrict__ 
         c.run(stats, s, p.G);
         // dx = scale dz - (rstd m1 + rstd^2 m2 (x - mean))
         f32x8_t k1, k2;
+        const f32x8_t k0 = c.scale * p.drop.scale;
         c.groups(means + int64_t(s) * p.G, [&](int j, const float2& v) { k1[j] = c.rstd[j] * v.x, k2[j] = c.rstd[j] * c.rstd[j] * v.y; });
         for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
             Raw8<TT> v[U], w[U];
@@ -424,7 +431,7 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_apply(const void* __restrict__ 
                 f32x8_t d, dz;
                 grad8<TT, ACT, DROP>(v[u], w[u], c, p, seed, offset, i, d, dz);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dz[j] = fmaf(c.scale[j], dz[j], -fmaf(k2[j], d[j], k1[j]));
+                for (int j = 0; j < 8; ++j) dz[j] = fmaf(k0[j], dz[j], -fmaf(k2[j], d[j], k1[j]));
                 st8<TT>(dx + i, narrow<TT>(dz));
             }
         }

@@ -117,7 +117,11 @@ struct Drop {
     uint32_t layer;
     uint32_t thr;         // an element is dropped iff its 16 bits are below thr
     float scale;          // of the kept ones: 65536 / (65536 - thr)
+    float inv;            // its reciprocal, exact
 };
+
+// a ^ b ^ c in one instruction.
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
 
 __device__ __forceinline__ u32x4 philox(uint64_t seed, uint64_t ctr, uint32_t layer) {
     uint32_t c0 = uint32_t(ctr), c1 = uint32_t(ctr >> 32), c2 = layer, c3 = 0;
@@ -125,9 +129,9 @@ __device__ __forceinline__ u32x4 philox(uint64_t seed, uint64_t ctr, uint32_t la
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t p0 = uint64_t(c0) * 0xD2511F53u, p1 = uint64_t(c2) * 0xCD9E8D57u;
-        c0 = uint32_t(p1 >> 32) ^ c1 ^ k0;
+        c0 = xor3(uint32_t(p1 >> 32), c1, k0);
         c1 = uint32_t(p1);
-        c2 = uint32_t(p0 >> 32) ^ c3 ^ k1;
+        c2 = xor3(uint32_t(p0 >> 32), c3, k1);
         c3 = uint32_t(p0);
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
@@ -135,14 +139,14 @@ __device__ __forceinline__ u32x4 philox(uint64_t seed, uint64_t ctr, uint32_t la
     return u32x4{c0, c1, c2, c3};
 }
 
-// v[j] * scale where the element stays, 0 where it is dropped (also for an
-// infinite or NaN v[j]).
-__device__ __forceinline__ f32x8_t drop8(f32x8_t v, const u32x4& bits, uint32_t thr, float scale) {
+// v[j] where the element stays, 0 where it is dropped (also for an infinite
+// or NaN v[j]).
+__device__ __forceinline__ f32x8_t drop8(f32x8_t v, const u32x4& bits, uint32_t thr) {
     const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = (w[i] & 0xffffu) >= thr ? v[2 * i] * scale : 0.f;
-        v[2 * i + 1] = (w[i] >> 16) >= thr ? v[2 * i + 1] * scale : 0.f;
+        v[2 * i] = (w[i] & 0xffffu) >= thr ? v[2 * i] : 0.f;
+        v[2 * i + 1] = (w[i] >> 16) >= thr ? v[2 * i + 1] : 0.f;
     }
     return v;
 }
@@ -150,7 +154,7 @@ __device__ __forceinline__ f32x8_t drop8(f32x8_t v, const u32x4& bits, uint32_t 
 // Host: checks a dropout descriptor (NULL: none) and turns it into kernel
 // arguments.
 inline spc_status make_drop(const spc_dropout* d, Drop& out) {
-    out = Drop{nullptr, 0, 0, 1.f};
+    out = Drop{nullptr, 0, 0, 1.f, 1.f};
     if (!d) return SPC_OK;
     if (!(d->p >= 0.f && d->p <= 1.f)) return fail(SPC_ERR_ARG, "dropout p=%g is outside [0, 1]", double(d->p));
     if (!d->rng || !aligned16(d->rng)) return fail(SPC_ERR_ARG, "dropout rng is NULL or not 16-byte aligned");
@@ -159,6 +163,7 @@ inline spc_status make_drop(const spc_dropout* d, Drop& out) {
     out.thr = uint32_t(d->p * 65536.f + 0.5f);
     // p = 1 drops everything: no element is left to scale
     out.scale = out.thr < 65536u ? 65536.f / float(65536u - out.thr) : 0.f;
+    out.inv = float(65536u - out.thr) / 65536.f;
     return SPC_OK;
 }
 
