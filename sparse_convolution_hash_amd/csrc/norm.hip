@@ -87,14 +87,15 @@ __device__ __forceinline__ void for_runs(const NormArgs& p, int tile, F f) {
     }
 }
 
-// Sums over the rows of a workgroup of two values per channel: f(channel in
-// the slab, sum of a, sum of b) in one thread per channel.
-template <typename F>
-__device__ __forceinline__ void reduce_rows(const NormArgs& p, const Place& q, const f32x8_t& a, const f32x8_t& b, float2* lds,
-                                            float2* part, F f) {
-    const int CW = p.k.CW, RL = p.k.RL, parts = NT / CW, per = (RL + parts - 1) / parts;   // 8 or 9 rows
-    if (q.rl < RL) {
-        f32x4_t* o = reinterpret_cast<f32x4_t*>(lds + q.rl * CW + q.c);
+// Sums over the RL rows of a workgroup of THREADS of two values per channel
+// (of CW, a thread's eight from c): f(channel, sum of a, sum of b) in one
+// thread per channel, side by side over the first CW threads.
+template <int THREADS, typename F>
+__device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, const f32x8_t& a, const f32x8_t& b, float2* lds, float2* part,
+                                            F f) {
+    const int parts = THREADS / CW, per = (RL + parts - 1) / parts;   // 8 or 9 rows
+    if (rl < RL) {
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(lds + rl * CW + c8);
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = f32x4_t{a[2 * j], b[2 * j], a[2 * j + 1], b[2 * j + 1]};
     }
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, 
                     s2 += d * d;
                 }
         }
-        reduce_rows(p, q, s1, s2, lds, sums, [&](int c, float t1, float t2) {
+        reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int c, float t1, float t2) {
             if (q.slab * p.k.CW + c >= p.C) return;
             const float m = t1 / float(b - a), m2 = t2 - t1 * m;
             part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + c] = float2{base[c] + m, m2 > 0.f || m2 != m2 ? m2 : 0.f};
@@ -344,7 +345,7 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
         }
         s1 *= p.drop.scale;
         s2 *= c.rstd * p.drop.scale;
-        reduce_rows(p, q, s1, s2, lds, sums, [&](int k, float t1, float t2) {
+        reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int k, float t1, float t2) {
             if (q.slab * p.k.CW + k >= p.C) return;
             part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + k] = float2{t1, t2};
             t.x += t1, t.y += t2;
@@ -354,14 +355,14 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
         tot[int64_t(q.tile) * p.C + q.slab * p.k.CW + threadIdx.x] = t;
 }
 
-// Workgroups [0, samples * G): the group's means of gamma dz and gamma dz
-// xhat.  Workgroups after them: dbeta and dgamma of 8 channels each.
-__global__ __launch_bounds__(NG) void k_norm_bwd_group(NormArgs p, const float* __restrict__ gamma,
+// Workgroups [0, groups), groups = samples * G: the group's means of gamma dz
+// and gamma dz xhat.  Workgroups after them: dbeta and dgamma of 8 channels
+// each, from ntot rows of tot.
+__global__ __launch_bounds__(NG) void k_norm_bwd_group(NormArgs p, int64_t groups, const float* __restrict__ gamma,
                                                        const float2* __restrict__ part, const float2* __restrict__ tot,
-                                                       float2* __restrict__ means, float* __restrict__ dgamma,
+                                                       int ntot, float2* __restrict__ means, float* __restrict__ dgamma,
                                                        float* __restrict__ dbeta) {
     __shared__ double2 lds[NG / WAVE];
-    const int64_t groups = int64_t(p.segs.n_seg) * p.G;
     double a = 0, b = 0;
     if (int64_t(blockIdx.x) < groups) {
         const int s = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(NG) void k_norm_bwd_group(NormArgs p, const float* 
     }
     const int c = int(blockIdx.x - groups) * 8 + int(threadIdx.x) % 8;
 #pragma unroll 4
-    for (int t = int(threadIdx.x) / 8; t < p.k.tiles; t += NG / 8) {
+    for (int t = int(threadIdx.x) / 8; t < ntot; t += NG / 8) {
         const float2 v = tot[int64_t(t) * p.C + c];
         a += v.x;
         b += v.y;
@@ -438,6 +439,173 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_apply(const void* __restrict__ 
     });
 }
 
+// ------------------------------------------------------------ small inputs
+
+// One launch (and one for dgamma and dbeta) does it all: a workgroup takes one
+// sample and CW channels, the fewest that are whole groups and whole loads, and
+// goes over its rows twice (the second time from the cache).  The three
+// launches above take 11 us (backward 13) at the least, 14 (17) with several
+// samples; this takes 6 (8) for 500 elements of a workgroup, 7 (9) for 4,000,
+// 8 to 13 (12 to 18) for 16,000 (and 4 us of the host's time less), 15 to 34
+// (26 to 86) for 64,000.  So it takes
+// calls with SMALL elements at most in the channels of a workgroup, or SMALL_MAX
+// if the samples have SMALL_MEAN on average, whatever their lengths.
+constexpr int NS = 512;
+constexpr int64_t SMALL = 16384, SMALL_MEAN = 8192, SMALL_MAX = 32768;
+
+inline int small_width(int32_t C, int32_t G) {
+    int w = C / G;
+    while (w % 8) w *= 2;
+    return w;
+}
+
+// A thread's place in such a workgroup.
+struct Corner {
+    int s, a, b, CW, CPR, RL, rl, c, ch;
+    bool on;
+    __device__ __forceinline__ Corner(const NormArgs& p, int CW_) : CW(CW_) {
+        const int n = p.C / CW;
+        s = int(blockIdx.x) / n;
+        a = p.segs.at(s), b = p.segs.at(s + 1);
+        CPR = CW / 8;
+        RL = NS / CPR;
+        rl = int(threadIdx.x) / CPR;
+        c = (int(threadIdx.x) - rl * CPR) * 8;
+        on = rl < RL;
+        ch = (int(blockIdx.x) - s * n) * CW + c;
+    }
+    __device__ __forceinline__ int c0() const { return ch - c; }
+};
+
+// Adds up v(channel) over each group of a workgroup's channels, one wave a
+// group, in double: f(group in the workgroup, sums of the pair).
+template <typename V, typename F>
+__device__ __forceinline__ void sum_groups(int CW, int cg, V v, F f) {
+    for (int g = int(threadIdx.x) / WAVE; g < CW / cg; g += NS / WAVE) {
+        double a = 0, b = 0;
+        for (int c = int(threadIdx.x) % WAVE; c < cg; c += WAVE) {
+            const double2 t = v(g, g * cg + c);
+            a += t.x, b += t.y;
+        }
+#pragma unroll
+        for (int o = 1; o < WAVE; o <<= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
+        if (threadIdx.x % WAVE == 0) f(g, a, b);
+    }
+    __syncthreads();
+}
+
+template <typename TT, int ACT, bool DROP>
+__global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, int CW, const float* __restrict__ gamma,
+                                                   const float* __restrict__ beta, float2* __restrict__ stats, void* y_) {
+    using S = typename TT::storage;
+    __shared__ float2 lds[NS * 8], sums[NS];
+    const S* x = static_cast<const S*>(x_);
+    S* y = static_cast<S*>(y_);
+    const Corner q(p, CW);
+    const int cg = p.C / p.G, g0 = q.c0() / cg;
+    float2* row = stats + int64_t(q.s) * p.G;
+    if (q.a >= q.b) {
+        for (int g = threadIdx.x; g < CW / cg; g += NS) row[g0 + g] = float2{0.f, float(1.0 / sqrt(double(p.eps)))};
+        return;
+    }
+    const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
+    Chan8 c(p, gamma, beta, q.ch);
+    if (DROP && ACT != SPC_ACT_SILU) c.gamma *= p.drop.scale, c.beta *= p.drop.scale;
+    const f32x8_t k = widen<TT>(ld8<TT>(x + int64_t(q.a) * p.C + q.ch));
+    __shared__ float2 chan[NS];   // a channel's sums around its value in the first row, and that value
+    __shared__ float base[NS];
+    if (q.rl == 0)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) base[q.c + j] = k[j];
+    f32x8_t s1 = 0.f, s2 = 0.f;
+#pragma unroll 4
+    for (int r = q.a + q.rl; r < q.b && q.on; r += q.RL) {
+        const f32x8_t d = widen<TT>(ld8<TT>(x + int64_t(r) * p.C + q.ch)) - k;
+        s1 += d;
+        s2 += d * d;
+    }
+    reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, float t1, float t2) { chan[i] = float2{t1, t2}; });
+    // around the value of the group's first channel k: sum (x - k) and its square
+    const double rows = double(q.b - q.a), cnt = rows * cg;
+    sum_groups(CW, cg,
+               [&](int g, int i) {
+                   const double o = double(base[i]) - double(base[g * cg]), t1 = chan[i].x, t2 = chan[i].y;
+                   return double2{t1 + rows * o, t2 + o * (2 * t1 + rows * o)};
+               },
+               [&](int g, double t1, double t2) {
+                   const double m = t1 / cnt, v = t2 / cnt - m * m;
+                   sums[g] = float2{float(double(base[g * cg]) + m), float(1.0 / sqrt((v > 0 || v != v ? v : 0) + double(p.eps)))};
+                   row[g0 + g] = sums[g];
+               });
+    c.g0 -= g0;
+    c.run(sums, 0, 0);
+#pragma unroll 4
+    for (int r = q.a + q.rl; r < q.b && q.on; r += q.RL) {
+        const int64_t i = int64_t(r) * p.C + q.ch;
+        f32x8_t z = widen<TT>(ld8<TT>(x + i)) - c.mean;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = act_f<ACT>(fmaf(z[j], c.scale[j], c.beta[j]), DROP ? p.drop.inv : 1.f);
+        if (DROP) z = drop8(z, philox(seed, offset + uint64_t(i / 8), p.drop.layer), p.drop.thr);
+        st8<TT>(y + i, narrow<TT>(z));
+    }
+}
+
+// tot (NULL ok): every sample's sums of dz and dz * xhat, per channel.
+template <typename TT, int ACT, bool DROP>
+__global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ x_, const void* dy_, NormArgs p, int CW,
+                                                       const float* __restrict__ gamma, const float* __restrict__ beta,
+                                                       const float2* __restrict__ stats, float2* __restrict__ tot, void* dx_) {
+    using S = typename TT::storage;
+    __shared__ float2 lds[NS * 8], sums[NS], chan[NS];
+    const S *x = static_cast<const S*>(x_), *dy = static_cast<const S*>(dy_);
+    S* dx = static_cast<S*>(dx_);
+    const Corner q(p, CW);
+    const int cg = p.C / p.G;
+    if (q.a >= q.b) {
+        for (int i = threadIdx.x; tot && i < CW; i += NS) tot[int64_t(q.s) * p.C + q.c0() + i] = float2{0.f, 0.f};
+        return;
+    }
+    const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
+    Chan8 c(p, gamma, beta, q.ch);
+    c.run(stats, q.s, p.G);
+    f32x8_t s1 = 0.f, s2 = 0.f;
+#pragma unroll 2
+    for (int r = q.a + q.rl; r < q.b && q.on; r += q.RL) {
+        const int64_t i = int64_t(r) * p.C + q.ch;
+        f32x8_t d, dz;
+        grad8<TT, ACT, DROP>(ld8<TT>(x + i), ld8<TT>(dy + i), c, p, seed, offset, i, d, dz);
+        s1 += dz;
+        s2 += dz * d;
+    }
+    s1 *= p.drop.scale;
+    s2 *= c.rstd * p.drop.scale;
+    reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, float t1, float t2) {
+        chan[i] = float2{t1, t2};
+        if (tot) tot[int64_t(q.s) * p.C + q.c0() + i] = float2{t1, t2};
+    });
+    const double cnt = double(q.b - q.a) * cg;
+    const float* ga = gamma ? gamma + q.c0() : nullptr;
+    sum_groups(CW, cg,
+               [&](int, int i) {
+                   const double w = ga ? ga[i] : 1.f;
+                   return double2{w * chan[i].x, w * chan[i].y};
+               },
+               [&](int g, double t1, double t2) { sums[g] = float2{float(t1 / cnt), float(t2 / cnt)}; });
+    c.g0 -= q.c0() / cg;
+    f32x8_t k1, k2;
+    const f32x8_t k0 = c.scale * p.drop.scale;
+    c.groups(sums, [&](int j, const float2& v) { k1[j] = c.rstd[j] * v.x, k2[j] = c.rstd[j] * c.rstd[j] * v.y; });
+#pragma unroll 2
+    for (int r = q.a + q.rl; r < q.b && q.on; r += q.RL) {
+        const int64_t i = int64_t(r) * p.C + q.ch;
+        f32x8_t d, dz;
+        grad8<TT, ACT, DROP>(ld8<TT>(x + i), ld8<TT>(dy + i), c, p, seed, offset, i, d, dz);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dz[j] = fmaf(k0[j], dz[j], -fmaf(k2[j], d[j], k1[j]));
+        st8<TT>(dx + i, narrow<TT>(dz));
+    }
+}
+
 struct NormWs {
     Cut k;
     int64_t part, tot, stats;  // counts of float2: the runs' sums, the tiles' sums, the group values
@@ -478,9 +646,8 @@ spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int32_t G, const in
 }
 
 // One kernel of the activations' and dropout's variants.
-#define NORM_VARIANT(name, ...)                                                                              \
+#define NORM_VARIANT(name, grid, NT, ...)                                                                    \
     do {                                                                                                      \
-        const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));                                           \
         if (p.drop.rng) {                                                                                     \
             if (act == SPC_ACT_RELU) hipLaunchKernelGGL((name<TT, SPC_ACT_RELU, true>), grid, dim3(NT), 0, stream, __VA_ARGS__);  \
             else if (act == SPC_ACT_SILU) hipLaunchKernelGGL((name<TT, SPC_ACT_SILU, true>), grid, dim3(NT), 0, stream, __VA_ARGS__); \
@@ -493,17 +660,30 @@ spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int32_t G, const in
         SPC_LAUNCHED(#name);                                                                                  \
     } while (0)
 
+// Whether one launch does: CW channels, at most one for each thread of the sums.
+inline bool is_small(const NormArgs& p, const NormWs& w, int& CW) {
+    CW = small_width(p.C, p.G);
+    const int64_t all = int64_t(p.segs.n) * CW;
+    return CW <= NS && (all <= SMALL || (all <= SMALL_MAX && all <= SMALL_MEAN * p.segs.n_seg)) && w.stats <= (int64_t(1) << 24);
+}
+
 template <typename TT>
 spc_status launch_fwd(const void* x, const NormArgs& p, const NormWs& w, const float* gamma, const float* beta, int act,
                       void* y, float2* stats, void* ws, hipStream_t stream) {
+    int CW;
+    if (is_small(p, w, CW)) {
+        NORM_VARIANT(k_norm_small, dim3(unsigned(p.segs.n_seg) * unsigned(p.C / CW)), NS, x, p, CW, gamma, beta, stats, y);
+        return SPC_OK;
+    }
     float2* part = static_cast<float2*>(ws);
+    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
     if (p.k.tiles) {
-        hipLaunchKernelGGL(k_norm_stats<TT>, dim3(unsigned(p.k.tiles) * unsigned(p.k.nslab)), dim3(NT), 0, stream, x, p, part);
+        hipLaunchKernelGGL(k_norm_stats<TT>, grid, dim3(NT), 0, stream, x, p, part);
         SPC_LAUNCHED("k_norm_stats");
     }
     hipLaunchKernelGGL(k_norm_group, dim3(unsigned(w.stats)), dim3(NG), 0, stream, p, part, stats);
     SPC_LAUNCHED("k_norm_group");
-    if (p.k.tiles) NORM_VARIANT(k_norm_apply, x, p, gamma, beta, stats, y);
+    if (p.k.tiles) NORM_VARIANT(k_norm_apply, grid, NT, x, p, gamma, beta, stats, y);
     return SPC_OK;
 }
 
@@ -513,11 +693,23 @@ spc_status launch_bwd(const void* dy, const void* x, const NormArgs& p, const No
                       hipStream_t stream) {
     const bool affine = dgamma || dbeta;
     float2 *part = static_cast<float2*>(ws), *tot = affine ? w.tot_of(ws) : nullptr, *means = w.means_of(ws);
-    if (p.k.tiles) NORM_VARIANT(k_norm_bwd_sums, x, dy, p, gamma, beta, stats, part, tot);
+    int CW;
+    if (is_small(p, w, CW)) {
+        tot = affine ? part : nullptr;      // by sample: no more than there are slots
+        NORM_VARIANT(k_norm_bwd_small, dim3(unsigned(p.segs.n_seg) * unsigned(p.C / CW)), NS, x, dy, p, CW, gamma, beta, stats, tot, dx);
+        if (affine) {
+            hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(p.C / 8)), dim3(NG), 0, stream, p, 0, gamma, part, tot, p.segs.n_seg, means,
+                               dgamma, dbeta);
+            SPC_LAUNCHED("k_norm_bwd_group");
+        }
+        return SPC_OK;
+    }
+    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
+    if (p.k.tiles) NORM_VARIANT(k_norm_bwd_sums, grid, NT, x, dy, p, gamma, beta, stats, part, tot);
     const int64_t blocks = w.stats + (affine ? p.C / 8 : 0);
-    hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(blocks)), dim3(NG), 0, stream, p, gamma, part, tot, means, dgamma, dbeta);
+    hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(blocks)), dim3(NG), 0, stream, p, w.stats, gamma, part, tot, p.k.tiles, means, dgamma, dbeta);
     SPC_LAUNCHED("k_norm_bwd_group");
-    if (p.k.tiles) NORM_VARIANT(k_norm_bwd_apply, x, dy, p, gamma, beta, stats, means, dx);
+    if (p.k.tiles) NORM_VARIANT(k_norm_bwd_apply, grid, NT, x, dy, p, gamma, beta, stats, means, dx);
     return SPC_OK;
 }
 
