@@ -24,13 +24,14 @@ constexpr int OPR = 8;       // most lanes (of 8 channels) per row: slabs of up 
 constexpr int U = 4;         // rows that a thread loads at a time
 
 // How [n, C] is cut: slabs of CW channels, CPR lanes to a row, RL rows side by
-// side, tiles of R rows.
+// side, tiles of R rows.  Workgroup y of Y takes every Y-th run of its tile.
 struct Cut {
     int32_t nslab, CPR, CW, RL, R;
-    int32_t tiles;
+    int32_t tiles, Y;
+    unsigned blocks() const { return unsigned(tiles) * unsigned(Y) * unsigned(nslab); }
 };
 
-inline Cut cut_of(int64_t n, int32_t C) {
+inline Cut cut_of(int64_t n, int32_t C, int64_t n_seg) {
     Cut k;
     k.nslab = int32_t(ceil_div(C / 8, OPR));
     k.CPR = int32_t(ceil_div(C / 8, k.nslab));
@@ -40,6 +41,10 @@ inline Cut cut_of(int64_t n, int32_t C) {
     k.R = k.RL * U;
     while (k.R < k.RL * U * 4 && ceil_div(n, 2 * k.R) * k.nslab >= 8 * 256) k.R *= 2;
     k.tiles = int32_t(ceil_div(n, k.R));
+    // a run takes a round trip to memory and three barriers, 2 us: two go side by
+    // side where CUs are idle (20,011 x 48 fp32 in 37 samples, both ways: 42 -> 37 us
+    // with Y = 2, 37 with 4, 47 with 8, whose workgroups mostly find nothing to do)
+    k.Y = n_seg > 1 && int64_t(k.tiles) * k.nslab <= 2 * 256 ? 2 : 1;
     return k;
 }
 
@@ -53,11 +58,13 @@ struct NormArgs {
 
 // A thread's place: 8 channels from ch, rows rl, rl + RL, ... of a run.
 struct Place {
-    int tile, slab, rl, ch, c;   // c: ch within the slab
+    int tile, y, slab, rl, ch, c;   // c: ch within the slab
     bool on;
     __device__ __forceinline__ explicit Place(const NormArgs& p) {
         tile = int(blockIdx.x) / p.k.nslab;
         slab = int(blockIdx.x) - tile * p.k.nslab;
+        y = tile % p.k.Y;
+        tile /= p.k.Y;
         rl = int(threadIdx.x) / p.k.CPR;
         c = (int(threadIdx.x) - rl * p.k.CPR) * 8;
         ch = slab * p.k.CW + c;
@@ -66,23 +73,29 @@ struct Place {
     }
 };
 
-// Calls f(sample, first row, end row) for every run of a tile.  Lane i of
+// Calls f(sample, first row, end row) for the workgroup's runs.  Lane i of
 // every wave reads the offset of sample s0 + i: one load, with up to 62
 // samples, instead of a search and a walk.
 template <typename F>
-__device__ __forceinline__ void for_runs(const NormArgs& p, int tile, F f) {
+__device__ __forceinline__ void for_runs(const NormArgs& p, const Place& q, F f) {
     const Segs& g = p.segs;
-    const int r0 = tile * p.k.R, r1 = p.k.R < g.n - r0 ? r0 + p.k.R : g.n;
-    int s = g.n_seg < WAVE - 1 ? 0 : g.find(r0);
+    const int r0 = q.tile * p.k.R, r1 = p.k.R < g.n - r0 ? r0 + p.k.R : g.n;
+    int s = g.n_seg < WAVE - 1 ? 0 : g.find(r0), turn = 0;
     while (s < g.n_seg) {
         const int i = s + int(threadIdx.x) % WAVE;
         const int off = g.at(i < g.n_seg ? i : g.n_seg);
-        for (int j = 0; j < WAVE - 1 && s < g.n_seg; ++j, ++s) {
+        // the first sample that reaches past r0
+        const uint64_t ends = __ballot(off > r0) >> 1;
+        const int skip = ends ? __builtin_ctzll(ends) : WAVE - 1;
+        s += skip;
+        for (int j = skip; j < WAVE - 1 && s < g.n_seg; ++j, ++s) {
             int a = __builtin_amdgcn_readlane(off, j), b = __builtin_amdgcn_readlane(off, j + 1);
             if (a >= r1) return;
             a = a > r0 ? a : r0;
             b = b < r1 ? b : r1;
-            if (a < b) f(s, a, b);
+            if (a >= b) continue;
+            if (turn == q.y) f(s, a, b);
+            turn = turn + 1 == p.k.Y ? 0 : turn + 1;
         }
     }
 }
@@ -126,7 +139,7 @@ __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, 
     __shared__ float base[8 * OPR];
     const S* x = static_cast<const S*>(x_);
     const Place q(p);
-    for_runs(p, q.tile, [&](int s, int a, int b) {
+    for_runs(p, q, [&](int s, int a, int b) {
         const f32x8_t k = widen<TT>(ld8<TT>(x + int64_t(a) * p.C + q.ch));
         if (q.rl == 0)
 #pragma unroll
@@ -237,8 +250,9 @@ struct Chan8 {
     f32x8_t gamma, beta, mean, rstd, scale;
     int cg, g0, first;   // channels per group, the first channel's group, and its place there
     __device__ __forceinline__ Chan8(const NormArgs& p, const float* g, const float* b, int ch) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) gamma[j] = g ? g[ch + j] : 1.f, beta[j] = b ? b[ch + j] : 0.f;
+        gamma = 1.f, beta = 0.f;
+        if (g) gamma = widen<F32>(ld8<F32>(g + ch));
+        if (b) beta = widen<F32>(ld8<F32>(b + ch));
         cg = p.C / p.G;
         g0 = ch / cg;
         first = ch - g0 * cg;
@@ -275,7 +289,7 @@ __global__ __launch_bounds__(NT) void k_norm_apply(const void* x_, NormArgs p, c
     Chan8 c(p, gamma, beta, q.ch);
     // dropout's factor goes into the affine step, silu's into its division
     if (DROP && ACT != SPC_ACT_SILU) c.gamma *= p.drop.scale, c.beta *= p.drop.scale;
-    for_runs(p, q.tile, [&](int s, int a, int b) {
+    for_runs(p, q, [&](int s, int a, int b) {
         c.run(stats, s, p.G);
         for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
             Raw8<TT> v[U];
@@ -309,7 +323,7 @@ __device__ __forceinline__ void grad8(const Raw8<TT>& x, const Raw8<TT>& dy, con
     for (int j = 0; j < 8; ++j) dz[j] *= act_d<ACT>(fmaf(d[j], c.scale[j], c.beta[j]));
 }
 
-// Sums of dz and dz * xhat of every run, and (tot, NULL ok) of every tile, per channel.
+// Sums of dz and dz * xhat of every run, and (tot, NULL ok) of the workgroup's runs, per channel.
 template <typename TT, int ACT, bool DROP>
 __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x_, const void* __restrict__ dy_, NormArgs p,
                                                       const float* __restrict__ gamma, const float* __restrict__ beta,
@@ -322,7 +336,7 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
     const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
     Chan8 c(p, gamma, beta, q.ch);
     float2 t{0.f, 0.f};
-    for_runs(p, q.tile, [&](int s, int a, int b) {
+    for_runs(p, q, [&](int s, int a, int b) {
         c.run(stats, s, p.G);
         f32x8_t s1 = 0.f, s2 = 0.f;
         for (int r = a + q.rl; r < b && q.on; r += p.k.RL * U) {
@@ -352,7 +366,7 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
         });
     });
     if (tot && int(threadIdx.x) < p.k.CW && q.slab * p.k.CW + int(threadIdx.x) < p.C)
-        tot[int64_t(q.tile) * p.C + q.slab * p.k.CW + threadIdx.x] = t;
+        tot[(int64_t(q.tile) * p.k.Y + q.y) * p.C + q.slab * p.k.CW + threadIdx.x] = t;
 }
 
 // Workgroups [0, groups), groups = samples * G: the group's means of gamma dz
@@ -410,7 +424,7 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_apply(const void* __restrict__ 
     const Place q(p);
     const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
     Chan8 c(p, gamma, beta, q.ch);
-    for_runs(p, q.tile, [&](int s, int a, int b) {
+    for_runs(p, q, [&](int s, int a, int b) {
         c.run(stats, s, p.G);
         // dx = scale dz - (rstd m1 + rstd^2 m2 (x - mean))
         f32x8_t k1, k2;
@@ -608,7 +622,7 @@ __global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ 
 
 struct NormWs {
     Cut k;
-    int64_t part, tot, stats;  // counts of float2: the runs' sums, the tiles' sums, the group values
+    int64_t part, tot, stats;  // counts of float2: the runs' sums, the workgroups' sums, the group values
     size_t bytes() const { return align_up(size_t(part) * 8, 256) + align_up(size_t(tot) * 8, 256) + size_t(stats) * 8; }
     float2* tot_of(void* ws) const { return reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(size_t(part) * 8, 256)); }
     float2* means_of(void* ws) const {
@@ -621,9 +635,9 @@ spc_status check_sizes(int64_t n, int32_t C, int32_t G, int64_t n_seg, NormWs& w
     if (n_seg < 1 || n_seg >= (int64_t(1) << 31) - 1) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)n_seg);
     if (C <= 0 || C % 16) return fail(SPC_ERR_UNSUPPORTED, "C=%d: channels must be a positive multiple of 16", C);
     if (G < 1 || C % G) return fail(SPC_ERR_ARG, "groups=%d does not divide C=%d", G, C);
-    w.k = cut_of(n, C);
+    w.k = cut_of(n, C, n_seg);
     w.part = (w.k.tiles + n_seg) * C;
-    w.tot = int64_t(w.k.tiles) * C;
+    w.tot = int64_t(w.k.tiles) * w.k.Y * C;
     w.stats = n_seg * G;
     if (int64_t(w.k.tiles) * w.k.nslab >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
     if (w.stats + C >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld groups are beyond one launch", (long long)w.stats);
@@ -676,7 +690,7 @@ spc_status launch_fwd(const void* x, const NormArgs& p, const NormWs& w, const f
         return SPC_OK;
     }
     float2* part = static_cast<float2*>(ws);
-    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
+    const dim3 grid(p.k.blocks());
     if (p.k.tiles) {
         hipLaunchKernelGGL(k_norm_stats<TT>, grid, dim3(NT), 0, stream, x, p, part);
         SPC_LAUNCHED("k_norm_stats");
@@ -704,10 +718,10 @@ spc_status launch_bwd(const void* dy, const void* x, const NormArgs& p, const No
         }
         return SPC_OK;
     }
-    const dim3 grid(unsigned(p.k.tiles) * unsigned(p.k.nslab));
+    const dim3 grid(p.k.blocks());
     if (p.k.tiles) NORM_VARIANT(k_norm_bwd_sums, grid, NT, x, dy, p, gamma, beta, stats, part, tot);
     const int64_t blocks = w.stats + (affine ? p.C / 8 : 0);
-    hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(blocks)), dim3(NG), 0, stream, p, w.stats, gamma, part, tot, p.k.tiles, means, dgamma, dbeta);
+    hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(blocks)), dim3(NG), 0, stream, p, w.stats, gamma, part, tot, p.k.tiles * p.k.Y, means, dgamma, dbeta);
     SPC_LAUNCHED("k_norm_bwd_group");
     if (p.k.tiles) NORM_VARIANT(k_norm_bwd_apply, grid, NT, x, dy, p, gamma, beta, stats, means, dx);
     return SPC_OK;
