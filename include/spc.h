@@ -487,9 +487,9 @@ spc_status spc_group_norm_workspace(int64_t n, int32_t C, int32_t groups, int64_
  * groups divides C.  gamma, beta fp32 [C] (NULL: 1 and 0); act one of
  * SPC_ACT_*; drop NULL for none.  x, y [n, C]; y may be x.
  * stats fp32 [n_seg, groups, 2] receives mean and rstd for the backward (an
- * empty sample: mean 0, variance 0).  Sums are fp32 over at most 2048 rows,
+ * empty sample: mean 0, variance 0).  Sums are fp32 over at most 8192 rows,
  * of differences from a row of the data, and double above that.
- * ws: spc_group_norm_workspace bytes, scratch.
+ * ws: spc_group_norm_workspace bytes, scratch (NULL ok if that is 0).
  */
 spc_status spc_group_norm_fwd(spc_dtype dtype, const void* x, int64_t n, int32_t C, int32_t groups,
                               const int32_t* seg_ptr, int64_t n_seg, const float* gamma, const float* beta, float eps,

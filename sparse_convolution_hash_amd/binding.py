@@ -684,7 +684,7 @@ class Dropout:
 
     def __init__(self, rng: torch.Tensor, p: float, layer: int = 0):
         _need(rng, "rng", torch.int64)
-        if tuple(rng.shape) != (2,):
+        if rng.shape != (2,):
             raise ValueError(f"rng must be [2] {{seed, offset}}, got {tuple(rng.shape)}")
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p={p} is outside [0, 1]")
@@ -706,7 +706,7 @@ def _drop_arg(dropout, dev):
 
 def _need_like(t, name, dtype, dev, shape):
     _need(t, name, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
 
 
@@ -785,9 +785,9 @@ def _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace):
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, got {act!r}")
     need = group_norm_workspace(n, C, int(groups), n_seg)
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    return dev, n, C, n_seg, workspace
+    if need and (workspace is None or workspace.numel() < need):
+        workspace = x.new_empty((need,), dtype=torch.uint8)
+    return dev, n, C, n_seg, workspace, 0 if workspace is None else workspace.numel()
 
 
 def group_norm_fwd(x: torch.Tensor, groups: int, seg_ptr: Optional[torch.Tensor] = None,
@@ -798,15 +798,15 @@ def group_norm_fwd(x: torch.Tensor, groups: int, seg_ptr: Optional[torch.Tensor]
     [S + 1] (None: one sample) (spc_group_norm_fwd).  gamma, beta fp32 [C].
     Returns ``(y, stats fp32 [S, groups, 2])``, stats for group_norm_bwd;
     ``out`` may be x."""
-    dev, n, C, n_seg, workspace = _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace)
+    dev, n, C, n_seg, workspace, ws_bytes = _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace)
     if out is None:
         out = torch.empty_like(x)
     else:
         _need_like(out, "out", x.dtype, dev, x.shape)
-    stats = torch.empty((n_seg, groups, 2), dtype=torch.float32, device=dev)
+    stats = x.new_empty((n_seg, groups, 2), dtype=torch.float32)
     st = lib().spc_group_norm_fwd(_DTYPES[x.dtype], _ptr(x), n, C, int(groups), _ptr(seg_ptr), n_seg, _ptr(gamma),
                                   _ptr(beta), eps, ACTIVATIONS[act], _drop_arg(dropout, dev), _ptr(out), _ptr(stats),
-                                  _ptr(workspace), workspace.numel(), _stream(dev))
+                                  _ptr(workspace), ws_bytes, _stream(dev))
     _check(st, "spc_group_norm_fwd")
     return out, stats
 
@@ -817,7 +817,7 @@ def group_norm_bwd(dout: torch.Tensor, x: torch.Tensor, groups: int, seg_ptr: Op
                    dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Gradients of group_norm_fwd (spc_group_norm_bwd) from its x and stats:
     ``(dx, dgamma, dbeta)``, the last two fp32 [C] or None; ``dx`` may be dout."""
-    dev, n, C, n_seg, workspace = _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace)
+    dev, n, C, n_seg, workspace, ws_bytes = _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace)
     _need_like(dout, "dout", x.dtype, dev, x.shape)
     _need_like(stats, "stats", torch.float32, dev, (n_seg, groups, 2))
     if dx is None:
@@ -826,12 +826,10 @@ def group_norm_bwd(dout: torch.Tensor, x: torch.Tensor, groups: int, seg_ptr: Op
         _need_like(dx, "dx", x.dtype, dev, x.shape)
     dgamma = dbeta = None
     if want_affine:
-        dgamma = torch.empty(C, dtype=torch.float32, device=dev)
-        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
+        dgamma, dbeta = x.new_empty((C,), dtype=torch.float32), x.new_empty((C,), dtype=torch.float32)
     st = lib().spc_group_norm_bwd(_DTYPES[x.dtype], _ptr(dout), _ptr(x), n, C, int(groups), _ptr(seg_ptr), n_seg,
                                   _ptr(gamma), _ptr(beta), _ptr(stats), ACTIVATIONS[act], _drop_arg(dropout, dev),
-                                  _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(),
-                                  _stream(dev))
+                                  _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), ws_bytes, _stream(dev))
     _check(st, "spc_group_norm_bwd")
     return dx, dgamma, dbeta
 
@@ -876,7 +874,7 @@ def _lr_checks(gate, x, seg_ptr, h0, order, workspace):
         _need_like(order, "order", torch.int32, dev, (n,))
     ws, carry = linear_recurrence_workspace(x.dtype, n, C, n_seg)
     if workspace is None or workspace.numel() < ws:
-        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+        workspace = x.new_empty((ws,), dtype=torch.uint8)
     return dev, n, C, n_seg, ld, workspace, carry
 
 
@@ -890,11 +888,11 @@ def linear_recurrence_fwd(gate: torch.Tensor, x: torch.Tensor, seg_ptr: Optional
     [S, C], carry or None)``; carry is for linear_recurrence_bwd."""
     dev, n, C, n_seg, ld, workspace, carry_bytes = _lr_checks(gate, x, seg_ptr, h0, order, workspace)
     if out is None:
-        out = torch.empty((n, C), dtype=x.dtype, device=dev)
+        out = x.new_empty((n, C))
     else:
         _need_like(out, "out", x.dtype, dev, (n, C))
-    h_last = torch.empty((n_seg, C), dtype=torch.float32, device=dev)
-    carry = torch.empty(max(carry_bytes // 4, 4), dtype=torch.float32, device=dev) if want_carry else None
+    h_last = x.new_empty((n_seg, C), dtype=torch.float32)
+    carry = x.new_empty((max(carry_bytes // 4, 4),), dtype=torch.float32) if want_carry else None
     st = lib().spc_linear_recurrence_fwd(_DTYPES[x.dtype], _ptr(gate), _ptr(x), ld, n, C, _ptr(seg_ptr), n_seg,
                                          _ptr(order), 1 if reverse else 0, _ptr(h0), _ptr(out), _ptr(h_last),
                                          _ptr(carry), _ptr(workspace), workspace.numel(), _stream(dev))
@@ -918,14 +916,13 @@ def linear_recurrence_bwd(dout: torch.Tensor, gate: torch.Tensor, x: torch.Tenso
     if (dgate is None) != (dx is None):
         raise ValueError("dgate and dx: give both or neither")
     if dgate is None:
-        dgate = torch.empty((n, C), dtype=x.dtype, device=dev)
-        dx = torch.empty((n, C), dtype=x.dtype, device=dev)
+        dgate, dx = x.new_empty((n, C)), x.new_empty((n, C))
         ldg = C
     else:
         ldg = _gate_x(dgate, dx, ("dgate", "dx"))
         if dx.dtype != x.dtype or dx.shape != x.shape or dx.device != dev:
             raise ValueError("dgate and dx must agree with x in dtype, shape and device")
-    dh0 = torch.empty((n_seg, C), dtype=torch.float32, device=dev) if want_dh0 else None
+    dh0 = x.new_empty((n_seg, C), dtype=torch.float32) if want_dh0 else None
     st = lib().spc_linear_recurrence_bwd(_DTYPES[x.dtype], _ptr(dout), _ptr(gate), _ptr(x), ld, n, C, _ptr(seg_ptr),
                                          n_seg, _ptr(order), 1 if reverse else 0, _ptr(h0), _ptr(carry), _ptr(dh_last),
                                          _ptr(dgate), _ptr(dx), ldg, _ptr(dh0), _ptr(workspace), workspace.numel(),
@@ -947,7 +944,7 @@ def linear_recurrence_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Ten
     else:
         _need_like(new_state, "new_state", torch.float32, dev, (n, C))
     if out is None:
-        out = torch.empty((n, C), dtype=x.dtype, device=dev)
+        out = x.new_empty((n, C))
     else:
         _need_like(out, "out", x.dtype, dev, (n, C))
     st = lib().spc_linear_recurrence_step(_DTYPES[x.dtype], _ptr(gate), _ptr(x), ld, n, C, _ptr(state), _ptr(new_state),

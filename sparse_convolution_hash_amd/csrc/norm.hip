@@ -564,11 +564,13 @@ __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, i
     }
 }
 
-// tot (NULL ok): every sample's sums of dz and dz * xhat, per channel.
+// tot (NULL ok): every sample's sums of dz and dz * xhat, per channel; dgamma
+// and dbeta (NULL ok) directly, where there is one sample.
 template <typename TT, int ACT, bool DROP>
 __global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ x_, const void* dy_, NormArgs p, int CW,
                                                        const float* __restrict__ gamma, const float* __restrict__ beta,
-                                                       const float2* __restrict__ stats, float2* __restrict__ tot, void* dx_) {
+                                                       const float2* __restrict__ stats, float2* __restrict__ tot,
+                                                       float* __restrict__ dgamma, float* __restrict__ dbeta, void* dx_) {
     using S = typename TT::storage;
     __shared__ float2 lds[NS * 8], sums[NS], chan[NS];
     const S *x = static_cast<const S*>(x_), *dy = static_cast<const S*>(dy_);
@@ -576,7 +578,11 @@ __global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ 
     const Corner q(p, CW);
     const int cg = p.C / p.G;
     if (q.a >= q.b) {
-        for (int i = threadIdx.x; tot && i < CW; i += NS) tot[int64_t(q.s) * p.C + q.c0() + i] = float2{0.f, 0.f};
+        for (int i = threadIdx.x; i < CW; i += NS) {
+            if (tot) tot[int64_t(q.s) * p.C + q.c0() + i] = float2{0.f, 0.f};
+            if (dgamma) dgamma[q.c0() + i] = 0.f;
+            if (dbeta) dbeta[q.c0() + i] = 0.f;
+        }
         return;
     }
     const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
@@ -596,6 +602,8 @@ __global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ 
     reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, float t1, float t2) {
         chan[i] = float2{t1, t2};
         if (tot) tot[int64_t(q.s) * p.C + q.c0() + i] = float2{t1, t2};
+        if (dgamma) dgamma[q.c0() + i] = t2;
+        if (dbeta) dbeta[q.c0() + i] = t1;
     });
     const double cnt = double(q.b - q.a) * cg;
     const float* ga = gamma ? gamma + q.c0() : nullptr;
@@ -622,8 +630,9 @@ __global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ 
 
 struct NormWs {
     Cut k;
+    int32_t CW;                // one launch does: its channels to a workgroup; 0: it does not
     int64_t part, tot, stats;  // counts of float2: the runs' sums, the workgroups' sums, the group values
-    size_t bytes() const { return align_up(size_t(part) * 8, 256) + align_up(size_t(tot) * 8, 256) + size_t(stats) * 8; }
+    size_t bytes() const { return CW ? size_t(part) * 8 : align_up(size_t(part) * 8, 256) + align_up(size_t(tot) * 8, 256) + size_t(stats) * 8; }
     float2* tot_of(void* ws) const { return reinterpret_cast<float2*>(static_cast<char*>(ws) + align_up(size_t(part) * 8, 256)); }
     float2* means_of(void* ws) const {
         return reinterpret_cast<float2*>(reinterpret_cast<char*>(tot_of(ws)) + align_up(size_t(tot) * 8, 256));
@@ -635,10 +644,15 @@ spc_status check_sizes(int64_t n, int32_t C, int32_t G, int64_t n_seg, NormWs& w
     if (n_seg < 1 || n_seg >= (int64_t(1) << 31) - 1) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)n_seg);
     if (C <= 0 || C % 16) return fail(SPC_ERR_UNSUPPORTED, "C=%d: channels must be a positive multiple of 16", C);
     if (G < 1 || C % G) return fail(SPC_ERR_ARG, "groups=%d does not divide C=%d", G, C);
+    if (ceil_div(C, 64) > 65535) return fail(SPC_ERR_UNSUPPORTED, "C=%d is beyond one launch", C);
     w.k = cut_of(n, C, n_seg);
     w.part = (w.k.tiles + n_seg) * C;
     w.tot = int64_t(w.k.tiles) * w.k.Y * C;
     w.stats = n_seg * G;
+    w.CW = small_width(C, G);
+    const int64_t all = n * w.CW;
+    if (!(w.CW <= NS && (all <= SMALL || (all <= SMALL_MAX && all <= SMALL_MEAN * n_seg)) && w.stats <= (int64_t(1) << 24))) w.CW = 0;
+    if (w.CW) w.part = n_seg > 1 ? n_seg * C : 0, w.tot = 0;      // the samples' sums of the backward
     if (int64_t(w.k.tiles) * w.k.nslab >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
     if (w.stats + C >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld groups are beyond one launch", (long long)w.stats);
     return SPC_OK;
@@ -652,7 +666,7 @@ spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int32_t G, const in
     if (act != SPC_ACT_NONE && act != SPC_ACT_RELU && act != SPC_ACT_SILU) return fail(SPC_ERR_ARG, "unknown activation %d", act);
     if (!seg_ptr && n_seg != 1) return fail(SPC_ERR_ARG, "seg_ptr is NULL with n_seg=%lld", (long long)n_seg);
     if (seg_ptr && !aligned16(seg_ptr)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
-    if (!ws || !aligned16(ws)) return fail(SPC_ERR_ARG, "ws is NULL or not 16-byte aligned");
+    if ((!ws && w.bytes()) || !aligned16(ws)) return fail(SPC_ERR_ARG, "ws is NULL or not 16-byte aligned");
     if (ws_bytes < w.bytes()) return fail(SPC_ERR_WORKSPACE, "ws_bytes=%zu, need %zu", ws_bytes, w.bytes());
     p.segs = Segs{seg_ptr, int32_t(n_seg), int32_t(n)};
     p.C = C, p.G = G, p.eps = 0.f, p.k = w.k;
@@ -674,18 +688,10 @@ spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int32_t G, const in
         SPC_LAUNCHED(#name);                                                                                  \
     } while (0)
 
-// Whether one launch does: CW channels, at most one for each thread of the sums.
-inline bool is_small(const NormArgs& p, const NormWs& w, int& CW) {
-    CW = small_width(p.C, p.G);
-    const int64_t all = int64_t(p.segs.n) * CW;
-    return CW <= NS && (all <= SMALL || (all <= SMALL_MAX && all <= SMALL_MEAN * p.segs.n_seg)) && w.stats <= (int64_t(1) << 24);
-}
-
 template <typename TT>
 spc_status launch_fwd(const void* x, const NormArgs& p, const NormWs& w, const float* gamma, const float* beta, int act,
                       void* y, float2* stats, void* ws, hipStream_t stream) {
-    int CW;
-    if (is_small(p, w, CW)) {
+    if (const int CW = w.CW) {
         NORM_VARIANT(k_norm_small, dim3(unsigned(p.segs.n_seg) * unsigned(p.C / CW)), NS, x, p, CW, gamma, beta, stats, y);
         return SPC_OK;
     }
@@ -707,11 +713,12 @@ spc_status launch_bwd(const void* dy, const void* x, const NormArgs& p, const No
                       hipStream_t stream) {
     const bool affine = dgamma || dbeta;
     float2 *part = static_cast<float2*>(ws), *tot = affine ? w.tot_of(ws) : nullptr, *means = w.means_of(ws);
-    int CW;
-    if (is_small(p, w, CW)) {
-        tot = affine ? part : nullptr;      // by sample: no more than there are slots
-        NORM_VARIANT(k_norm_bwd_small, dim3(unsigned(p.segs.n_seg) * unsigned(p.C / CW)), NS, x, dy, p, CW, gamma, beta, stats, tot, dx);
-        if (affine) {
+    if (const int CW = w.CW) {
+        const bool one = p.segs.n_seg == 1;
+        tot = affine && !one ? part : nullptr;
+        NORM_VARIANT(k_norm_bwd_small, dim3(unsigned(p.segs.n_seg) * unsigned(p.C / CW)), NS, x, dy, p, CW, gamma, beta, stats, tot,
+                     one ? dgamma : nullptr, one ? dbeta : nullptr, dx);
+        if (tot) {
             hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(p.C / 8)), dim3(NG), 0, stream, p, 0, gamma, part, tot, p.segs.n_seg, means,
                                dgamma, dbeta);
             SPC_LAUNCHED("k_norm_bwd_group");
