@@ -109,25 +109,24 @@ __device__ __forceinline__ void str<BF16>(void* p, const f32x4_t& f) {
     *static_cast<uint2*>(p) = __builtin_bit_cast(uint2, __builtin_convertvector(f, bf16x4v_t));
 }
 
-// The smaller of sigmoid(g) and sigmoid(-g) to full relative precision (2 and
-// 1 units of exp and rcp), and the larger as its complement to 1.
-__device__ __forceinline__ float gate_small(float g, float& big) {
+// The smaller of sigmoid(g) and sigmoid(-g), to full relative precision (exp,
+// rcp and two roundings: 4 units at most).
+__device__ __forceinline__ float gate_small(float g) {
     const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(g));
-    big = __builtin_amdgcn_rcpf(1.f + e);
-    return e * big;
+    return e * __builtin_amdgcn_rcpf(1.f + e);
 }
-// a = sigmoid(g) and na = 1 - a = sigmoid(-g), each to full relative precision.
+// a = sigmoid(g) and na = 1 - a = sigmoid(-g).  The larger is 1 less the
+// smaller, half a unit off where that is near 1: there products of thousands of
+// gates add up their errors, and rcp(1 + e) would be off by three times as much.
 __device__ __forceinline__ void gates(float g, float& a, float& na) {
-    float big;
-    const float small = gate_small(g, big);
+    const float small = gate_small(g), big = 1.f - small;
     a = g >= 0.f ? big : small;
     na = g >= 0.f ? small : big;
 }
 // Both from the smaller one with the gate's sign, which is what a chunk keeps
 // of its gates: half the registers of the two, and no second exp and rcp.
 __device__ __forceinline__ float keep(float g) {
-    float big;
-    return __builtin_copysignf(gate_small(g, big), g);
+    return __builtin_copysignf(gate_small(g), g);
 }
 __device__ __forceinline__ void gates_of(float kept, float& a, float& na) {
     const float small = fabsf(kept), big = 1.f - small;
