@@ -100,11 +100,11 @@ __device__ __forceinline__ void for_runs(const NormArgs& p, const Place& q, F f)
     }
 }
 
-// Sums over the RL rows of a workgroup of THREADS of two values per channel
+// Sums in double over the RL rows of a workgroup of THREADS of two values per channel
 // (of CW, a thread's eight from c): f(channel, sum of a, sum of b) in one
 // thread per channel, side by side over the first CW threads.
 template <int THREADS, typename F>
-__device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, const f32x8_t& a, const f32x8_t& b, float2* lds, float2* part,
+__device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, const f32x8_t& a, const f32x8_t& b, float2* lds, double2* part,
                                             F f) {
     const int parts = THREADS / CW, per = (RL + parts - 1) / parts;   // 8 or 9 rows
     if (rl < RL) {
@@ -115,13 +115,13 @@ __device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, cons
     __syncthreads();
     const int i = int(threadIdx.x) / CW, c = int(threadIdx.x) - i * CW;
     if (i < parts) {
-        float2 t{0.f, 0.f};
+        double2 t{0., 0.};
         for (int r = i * per; r < (i + 1) * per && r < RL; ++r) t.x += lds[r * CW + c].x, t.y += lds[r * CW + c].y;
         part[i * CW + c] = t;
     }
     __syncthreads();
     if (i == 0) {
-        float2 t = part[c];
+        double2 t = part[c];
         for (int r = 1; r < parts; ++r) t.x += part[r * CW + c].x, t.y += part[r * CW + c].y;
         f(c, t.x, t.y);
     }
@@ -135,7 +135,8 @@ __device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, cons
 template <typename TT>
 __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, NormArgs p, float2* __restrict__ part) {
     using S = typename TT::storage;
-    __shared__ float2 lds[NT * 8], sums[NT];
+    __shared__ float2 lds[NT * 8];
+    __shared__ double2 sums[NT];
     __shared__ float base[8 * OPR];
     const S* x = static_cast<const S*>(x_);
     const Place q(p);
@@ -160,9 +161,9 @@ __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, 
                     s2 += d * d;
                 }
         }
-        reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int c, float t1, float t2) {
+        reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int c, double t1, double t2) {
             if (q.slab * p.k.CW + c >= p.C) return;
-            const float m = t1 / float(b - a), m2 = t2 - t1 * m;
+            const float inv = 1.f / float(b - a), m = float(t1) * inv, m2 = float(t2 - t1 * m);
             part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + c] = float2{base[c] + m, m2 > 0.f || m2 != m2 ? m2 : 0.f};
         });
     });
@@ -330,12 +331,13 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
                                                       const float2* __restrict__ stats, float2* __restrict__ part,
                                                       float2* __restrict__ tot) {
     using S = typename TT::storage;
-    __shared__ float2 lds[NT * 8], sums[NT];
+    __shared__ float2 lds[NT * 8];
+    __shared__ double2 sums[NT];
     const S *x = static_cast<const S*>(x_), *dy = static_cast<const S*>(dy_);
     const Place q(p);
     const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
     Chan8 c(p, gamma, beta, q.ch);
-    float2 t{0.f, 0.f};
+    double2 t{0., 0.};
     for_runs(p, q, [&](int s, int a, int b) {
         c.run(stats, s, p.G);
         f32x8_t s1 = 0.f, s2 = 0.f;
@@ -359,14 +361,14 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
         }
         s1 *= p.drop.scale;
         s2 *= c.rstd * p.drop.scale;
-        reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int k, float t1, float t2) {
+        reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int k, double t1, double t2) {
             if (q.slab * p.k.CW + k >= p.C) return;
-            part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + k] = float2{t1, t2};
+            part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + k] = float2{float(t1), float(t2)};
             t.x += t1, t.y += t2;
         });
     });
     if (tot && int(threadIdx.x) < p.k.CW && q.slab * p.k.CW + int(threadIdx.x) < p.C)
-        tot[(int64_t(q.tile) * p.k.Y + q.y) * p.C + q.slab * p.k.CW + threadIdx.x] = t;
+        tot[(int64_t(q.tile) * p.k.Y + q.y) * p.C + q.slab * p.k.CW + threadIdx.x] = float2{float(t.x), float(t.y)};
 }
 
 // Workgroups [0, groups), groups = samples * G: the group's means of gamma dz
@@ -512,7 +514,9 @@ template <typename TT, int ACT, bool DROP>
 __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, int CW, const float* __restrict__ gamma,
                                                    const float* __restrict__ beta, float2* __restrict__ stats, void* y_) {
     using S = typename TT::storage;
-    __shared__ float2 lds[NS * 8], sums[NS];
+    __shared__ float2 lds[NS * 8];
+    __shared__ double2 sums[NS], chan[NS];   // chan: a channel's sums around its value in the first row, base
+    __shared__ float base[NS];
     const S* x = static_cast<const S*>(x_);
     S* y = static_cast<S*>(y_);
     const Corner q(p, CW);
@@ -526,8 +530,6 @@ __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, i
     Chan8 c(p, gamma, beta, q.ch);
     if (DROP && ACT != SPC_ACT_SILU) c.gamma *= p.drop.scale, c.beta *= p.drop.scale;
     const f32x8_t k = widen<TT>(ld8<TT>(x + int64_t(q.a) * p.C + q.ch));
-    __shared__ float2 chan[NS];   // a channel's sums around its value in the first row, and that value
-    __shared__ float base[NS];
     if (q.rl == 0)
 #pragma unroll
         for (int j = 0; j < 8; ++j) base[q.c + j] = k[j];
@@ -538,7 +540,8 @@ __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, i
         s1 += d;
         s2 += d * d;
     }
-    reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, float t1, float t2) { chan[i] = float2{t1, t2}; });
+    reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, double t1, double t2) { chan[i] = double2{t1, t2}; });
+    float2* const group = lds;   // free again
     // around the value of the group's first channel k: sum (x - k) and its square
     const double rows = double(q.b - q.a), cnt = rows * cg;
     sum_groups(CW, cg,
@@ -548,11 +551,11 @@ __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, i
                },
                [&](int g, double t1, double t2) {
                    const double m = t1 / cnt, v = t2 / cnt - m * m;
-                   sums[g] = float2{float(double(base[g * cg]) + m), float(1.0 / sqrt((v > 0 || v != v ? v : 0) + double(p.eps)))};
-                   row[g0 + g] = sums[g];
+                   group[g] = float2{float(double(base[g * cg]) + m), float(1.0 / sqrt((v > 0 || v != v ? v : 0) + double(p.eps)))};
+                   row[g0 + g] = group[g];
                });
     c.g0 -= g0;
-    c.run(sums, 0, 0);
+    c.run(group, 0, 0);
 #pragma unroll 4
     for (int r = q.a + q.rl; r < q.b && q.on; r += q.RL) {
         const int64_t i = int64_t(r) * p.C + q.ch;
@@ -572,7 +575,8 @@ __global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ 
                                                        const float2* __restrict__ stats, float2* __restrict__ tot,
                                                        float* __restrict__ dgamma, float* __restrict__ dbeta, void* dx_) {
     using S = typename TT::storage;
-    __shared__ float2 lds[NS * 8], sums[NS], chan[NS];
+    __shared__ float2 lds[NS * 8];
+    __shared__ double2 sums[NS], chan[NS];
     const S *x = static_cast<const S*>(x_), *dy = static_cast<const S*>(dy_);
     S* dx = static_cast<S*>(dx_);
     const Corner q(p, CW);
@@ -599,24 +603,25 @@ __global__ __launch_bounds__(NS) void k_norm_bwd_small(const void* __restrict__ 
     }
     s1 *= p.drop.scale;
     s2 *= c.rstd * p.drop.scale;
-    reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, float t1, float t2) {
-        chan[i] = float2{t1, t2};
-        if (tot) tot[int64_t(q.s) * p.C + q.c0() + i] = float2{t1, t2};
-        if (dgamma) dgamma[q.c0() + i] = t2;
-        if (dbeta) dbeta[q.c0() + i] = t1;
+    reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, double t1, double t2) {
+        chan[i] = double2{t1, t2};
+        if (tot) tot[int64_t(q.s) * p.C + q.c0() + i] = float2{float(t1), float(t2)};
+        if (dgamma) dgamma[q.c0() + i] = float(t2);
+        if (dbeta) dbeta[q.c0() + i] = float(t1);
     });
     const double cnt = double(q.b - q.a) * cg;
+    float2* const group = lds;   // free again
     const float* ga = gamma ? gamma + q.c0() : nullptr;
     sum_groups(CW, cg,
                [&](int, int i) {
                    const double w = ga ? ga[i] : 1.f;
                    return double2{w * chan[i].x, w * chan[i].y};
                },
-               [&](int g, double t1, double t2) { sums[g] = float2{float(t1 / cnt), float(t2 / cnt)}; });
+               [&](int g, double t1, double t2) { group[g] = float2{float(t1 / cnt), float(t2 / cnt)}; });
     c.g0 -= q.c0() / cg;
     f32x8_t k1, k2;
     const f32x8_t k0 = c.scale * p.drop.scale;
-    c.groups(sums, [&](int j, const float2& v) { k1[j] = c.rstd[j] * v.x, k2[j] = c.rstd[j] * c.rstd[j] * v.y; });
+    c.groups(group, [&](int j, const float2& v) { k1[j] = c.rstd[j] * v.x, k2[j] = c.rstd[j] * c.rstd[j] * v.y; });
 #pragma unroll 2
     for (int r = q.a + q.rl; r < q.b && q.on; r += q.RL) {
         const int64_t i = int64_t(r) * p.C + q.ch;
