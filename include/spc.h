@@ -438,7 +438,8 @@ spc_status spc_gather_by_voxel_id(spc_dtype dtype, const void* seg_features, int
  * defined value, never an access outside the arrays.
  * Values are read and written in the call's dtype and computed in fp32, with
  * one rounding to nearest even at the end.  Every result is run-to-run
- * identical.  Every call is asynchronous, issues kernels only (no memset or
+ * identical.  Outputs overlap neither inputs nor each other but where it is
+ * said.  Every call is asynchronous, issues kernels only (no memset or
  * copy, so it can be captured into a graph) and allocates nothing.
  */
 
@@ -487,7 +488,7 @@ spc_status spc_group_norm_workspace(int64_t n, int32_t C, int32_t groups, int64_
  * groups divides C.  gamma, beta fp32 [C] (NULL: 1 and 0); act one of
  * SPC_ACT_*; drop NULL for none.  x, y [n, C]; y may be x.
  * stats fp32 [n_seg, groups, 2] receives mean and rstd for the backward (an
- * empty sample: mean 0, variance 0).  Sums are fp32 over at most 8192 rows,
+ * empty sample: mean 0, variance 0).  Sums are fp32 over at most 16 rows,
  * of differences from a row of the data, and double above that.
  * ws: spc_group_norm_workspace bytes, scratch (NULL ok if that is 0).
  */

@@ -12,8 +12,16 @@
 // the next and one of them rises, so slots are distinct, there are at most
 // tiles + samples of them, and a sample's runs lie side by side.  Three
 // launches each way: per-channel sums of every run, their reduction to group
-// (and channel) values, the elementwise pass.  All sums are fp32 within a run
-// and double across runs, in a fixed order (no atomics).
+// (and channel) values, the elementwise pass.  A thread's sums are fp32, over
+// at most 16 rows; all above are double, in a fixed order (no atomics).
+//
+// What bounds it: x is read twice forward, x and dy twice backward, the second
+// time mostly from the 256 MB cache, so on 266,426 x 128 bf16 (68 MB a tensor)
+// the passes over memory would take 14 + 22 and 27 + 35 us.  Statistics: 14 us
+// (4.9 TB/s).  The other three are held by the vector units next to that:
+// with silu and dropout an element costs 20 to 28 instructions, a third of them
+// the generator's, which each pass draws anew: 27 us (apply), 35 (sums), 38
+// (backward apply).  Forward and backward with all launches: 135 us.
 #include "rows.h"
 
 namespace spc {
@@ -21,7 +29,7 @@ namespace {
 
 constexpr int NT = 256;      // threads per workgroup
 constexpr int OPR = 8;       // most lanes (of 8 channels) per row: slabs of up to 64 channels
-constexpr int U = 4;         // rows that a thread loads at a time
+constexpr int U = 4;         // rows that a thread loads at a time (2: 120,000 x 64 fp16 forward 22 -> 28 us)
 
 // How [n, C] is cut: slabs of CW channels, CPR lanes to a row, RL rows side by
 // side, tiles of R rows.  Workgroup y of Y takes every Y-th run of its tile.
@@ -37,7 +45,8 @@ inline Cut cut_of(int64_t n, int32_t C, int64_t n_seg) {
     k.CPR = int32_t(ceil_div(C / 8, k.nslab));
     k.CW = 8 * k.CPR;
     k.RL = NT / k.CPR;
-    // the longest tiles that still give every CU 8 workgroups
+    // the longest tiles that still give every CU 8 workgroups (266,426 x 128 both
+    // ways: 145 us; with 4 151, with 16 158)
     k.R = k.RL * U;
     while (k.R < k.RL * U * 4 && ceil_div(n, 2 * k.R) * k.nslab >= 8 * 256) k.R *= 2;
     k.tiles = int32_t(ceil_div(n, k.R));
@@ -460,10 +469,10 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_apply(const void* __restrict__ 
 // One launch (and one for dgamma and dbeta) does it all: a workgroup takes one
 // sample and CW channels, the fewest that are whole groups and whole loads, and
 // goes over its rows twice (the second time from the cache).  The three
-// launches above take 11 us (backward 13) at the least, 14 (17) with several
-// samples; this takes 6 (8) for 500 elements of a workgroup, 7 (9) for 4,000,
-// 8 to 13 (12 to 18) for 16,000 (and 4 us of the host's time less), 15 to 34
-// (26 to 86) for 64,000.  So it takes
+// launches above take 11 us (backward 13 to 15) at the least; this takes 6 (6) for
+// 500 elements of a workgroup, 7 (7 to 8) for 4,000, 7 to 13 (9 to 17) for 16,000
+// (and 4 us of the host's time less), 15 to 34 (26 to 86) for 64,000.  Eight
+// samples of 2,000 elements each: 7 (9).  So it takes
 // calls with SMALL elements at most in the channels of a workgroup, or SMALL_MAX
 // if the samples have SMALL_MEAN on average, whatever their lengths.
 constexpr int NS = 512;
