@@ -853,15 +853,17 @@ def _gate_x(gate, x, names=("gate", "x")):
             raise TypeError(f"unsupported dtype {t.dtype}")
         if t.dim() != 2:
             raise ValueError(f"{nm} must be [N, C]")
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{nm}'s channels must be contiguous")
-    if gate.dtype != x.dtype or gate.shape != x.shape or gate.device != x.device:
+    if gate.shape != x.shape or gate.dtype != x.dtype or gate.device != x.device:
         raise ValueError(f"{names[0]} and {names[1]} must agree in dtype, shape and device")
-    if x.shape[0] <= 1:
-        return x.shape[1]
-    if gate.stride(0) != x.stride(0):
+    n, C = x.shape
+    (lg, cg), (lx, cx) = gate.stride(), x.stride()
+    if C > 1 and (cg != 1 or cx != 1):
+        raise ValueError(f"the channels of {names[0]} and {names[1]} must be contiguous")
+    if n <= 1:
+        return C
+    if lg != lx:
         raise ValueError(f"{names[0]} and {names[1]} must have one row stride")
-    return x.stride(0)
+    return lx
 
 
 def _lr_checks(gate, x, seg_ptr, h0, order, workspace):
