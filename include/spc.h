@@ -432,7 +432,7 @@ spc_status spc_gather_by_voxel_id(spc_dtype dtype, const void* seg_features, int
  * Samples.  seg_ptr, device int32 [n_seg + 1], ascending: sample s owns the
  * rows [seg_ptr[s], seg_ptr[s+1]), of any length, 0 and 1 included (the rows
  * of a strided map come out sorted by sample; searchsorted of their batch
- * column gives seg_ptr).  Rows in no sample are neither read nor written.
+ * column gives seg_ptr).  Rows in no sample enter no result and are not written.
  * NULL with n_seg = 1 is one sample of all n rows.  The offsets are read on
  * the device, each clamped to [0, n]; offsets that fall give rows of no
  * defined value, never an access outside the arrays.

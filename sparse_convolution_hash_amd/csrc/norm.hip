@@ -125,13 +125,16 @@ __device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, cons
     const int i = int(threadIdx.x) / CW, c = int(threadIdx.x) - i * CW;
     if (i < parts) {
         double2 t{0., 0.};
-        for (int r = i * per; r < (i + 1) * per && r < RL; ++r) t.x += lds[r * CW + c].x, t.y += lds[r * CW + c].y;
+        const int end = (i + 1) * per < RL ? (i + 1) * per : RL;
+#pragma unroll 8
+        for (int r = i * per; r < end; ++r) t.x += lds[r * CW + c].x, t.y += lds[r * CW + c].y;
         part[i * CW + c] = t;
     }
     __syncthreads();
     if (i == 0) {
-        double2 t = part[c];
-        for (int r = 1; r < parts; ++r) t.x += part[r * CW + c].x, t.y += part[r * CW + c].y;
+        double2 t{0., 0.};
+#pragma unroll 8
+        for (int r = 0; r < parts; ++r) t.x += part[r * CW + c].x, t.y += part[r * CW + c].y;
         f(c, t.x, t.y);
     }
     __syncthreads();

@@ -356,6 +356,7 @@ __device__ __forceinline__ void join(const LrArgs& p, Shared& sh, const Strip& k
     }
     __syncthreads();
     Map m{1.f, 0.f};
+#pragma unroll 4
     for (int i = k0; i < k1; ++i) {
         const float2 v = sh.map[i * CW + c];
         m = after(Map{v.x, v.y}, m);
@@ -364,10 +365,12 @@ __device__ __forceinline__ void join(const LrArgs& p, Shared& sh, const Strip& k
     __syncthreads();
     if (part < parts) {
         m = Map{1.f, 0.f};
+#pragma unroll 4
         for (int i = 0; i < part; ++i) {
             const float2 v = sh.part[i * CW + c];
             m = after(Map{v.x, v.y}, m);
         }
+#pragma unroll 4
         for (int i = k0; i < k1; ++i) {
             const float2 v = sh.map[i * CW + c];
             out(i, c, m);
@@ -378,8 +381,8 @@ __device__ __forceinline__ void join(const LrArgs& p, Shared& sh, const Strip& k
 }
 
 template <typename TT, bool ORDERED, bool BACK>
-__global__ __launch_bounds__(NT, TT::E == 8 ? 5 : 4) void k_lr_reduce(const void* __restrict__ gate, const void* __restrict__ v, LrArgs p,
-                                                  const float* __restrict__ from) {
+__global__ __launch_bounds__(NT, TT::E == 8 ? 5 : 4) void k_lr_reduce(const void* __restrict__ gate, const void* __restrict__ v,
+                                                                             LrArgs p, const float* __restrict__ from) {
     __shared__ Shared sh;
     const int tile = int(blockIdx.x) / p.k.nslab, slab = int(blockIdx.x) - tile * p.k.nslab;
     const Span span(p, tile);
@@ -431,6 +434,7 @@ __global__ __launch_bounds__(TN) void k_lr_tiles(LrArgs p, bool back) {
         if (lane < 4) before = Map{1.f, 0.f};
         __syncthreads();
         float g = h;
+#pragma unroll
         for (int i = 0; i < TN / WAVE; ++i) {
             if (i == int(threadIdx.x) / WAVE) h = g;
             g = apply(Map{wave[i][c].x, wave[i][c].y}, g);
@@ -486,8 +490,8 @@ __device__ __forceinline__ void walk_tile(const LrArgs& p, int& tile, int& slab)
 // ONE: a single tile, whose strips are reduced and joined here.
 template <typename TT, bool ORDERED, bool ONE>
 __global__ __launch_bounds__(NT, TT::E == 8 ? 5 : 4) void k_lr_fwd(const void* __restrict__ gate, const void* __restrict__ x, LrArgs p,
-                                               const float* __restrict__ h0, void* __restrict__ out_,
-                                               float* __restrict__ h_last, float* __restrict__ carry) {
+                                                                          const float* __restrict__ h0, void* __restrict__ out_,
+                                                                          float* __restrict__ h_last, float* __restrict__ carry) {
     typename TT::storage* out = static_cast<typename TT::storage*>(out_);
     __shared__ Shared sh;
     __shared__ float in[ONE ? NT * 4 : 4];
@@ -543,8 +547,8 @@ struct Triple {
     Rows<ORDERED> rows;
     Raw4<TT> g[T], v[T], d[T];
     f32x4_t h;
-    __device__ __forceinline__ void load(const LrArgs& p, const Window& w, const void* gate, const void* x, const void* dout, const float* carry, int pos,
-                                         int c) {
+    __device__ __forceinline__ void load(const LrArgs& p, const Window& w, const void* gate, const void* x, const void* dout,
+                                         const float* carry, int pos, int c) {
         using S = typename TT::storage;
         rows.numbers(p, w, pos);
         h = ld4(carry + int64_t(pos / T) * p.C + c);
