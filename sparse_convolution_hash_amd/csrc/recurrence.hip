@@ -12,9 +12,9 @@
 // E -> a_t (dh_t + E), over the rows in the opposite order.
 //
 // A thread walks a strip of L rows x 4 channels.  Launches: the strips' maps,
-// folded within each workgroup's tile of strips (k_lr_reduce_*); the tiles'
+// folded within each workgroup's tile of strips (k_lr_reduce); the tiles'
 // maps to the states they start from (k_lr_tiles); the walk again from its
-// start state, with the outputs (k_lr_apply_*).  Up to FEW tiles the walk folds
+// start state, with the outputs (k_lr_fwd, k_lr_bwd).  Up to FEW tiles the walk folds
 // the tiles before its own itself, and a single tile takes one launch.  The
 // order of all folds is fixed by the sizes, so results do not depend on timing.
 //
