@@ -58,8 +58,8 @@ inline Cut cut_of(int64_t n, int32_t C) {
     // the longest strips that still leave 6 waves to each SIMD (half and twice as
     // many: 194 us of training on 266,426 x 128 become 202 and 210); LMAX 16: 147 us
     // forward on 1,000,003 x 64 become 165
-    k.L = T;
-    while (k.L < LMAX && n * (C / 4) / (2 * k.L) >= 6 * 1024 * WAVE) k.L *= 2;
+    k.L = T;   // longer ones never leave a single tile
+    while (k.L < LMAX && n > k.NCH * k.L * 2 && n * (C / 4) / (2 * k.L) >= 6 * 1024 * WAVE) k.L *= 2;
     k.rows = k.NCH * k.L;
     k.tiles = int32_t(ceil_div(n, k.rows));
     return k;
@@ -306,7 +306,33 @@ struct Pair {
     }
 };
 
-// The map of a strip.  from: h0, or dh_last.
+// T rows onto a strip's map, from row i of it.  from: h0, or dh_last.
+template <typename TT, bool ORDERED, bool BACK>
+__device__ __forceinline__ void fold(const Rows<ORDERED>& rows, const Raw4<TT> (&g)[T], const Raw4<TT> (&x)[T], const float* from,
+                                     const LrArgs& p, const Shared& sh, const Strip& k, int i, f32x4_t& A, f32x4_t& B) {
+    const auto step = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, na;
+            gates(elem<TT>(g[t], j), a, na);
+            A[j] *= a;
+            B[j] = BACK ? a * (elem<TT>(x[t], j) + B[j]) : fmaf(a, B[j], na * elem<TT>(x[t], j));
+        }
+    };
+    if (rows.simple) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) step(BACK ? T - 1 - t : t);
+    } else {
+#pragma unroll
+        for (int u = 0; u < T; ++u) {
+            const int t = BACK ? T - 1 - u : u;
+            if ((BACK ? rows.last : rows.first) >> t & 1) A = -0.f, B = state_of(from, p, sh, k.i0 + i + t, k.c);
+            if (rows.r[t] >= 0) step(t);
+        }
+    }
+}
+
+// The map of a strip.
 template <typename TT, bool ORDERED, bool BACK>
 __device__ __forceinline__ void reduce(const void* gate, const void* v, const float* from, const LrArgs& p, const Shared& sh,
                                        const Window& w, bool marked, const Strip& k, f32x4_t& A, f32x4_t& B) {
@@ -317,26 +343,7 @@ __device__ __forceinline__ void reduce(const void* gate, const void* v, const fl
         Pair<TT, ORDERED> b;
         b.load(p, w, gate, v, BACK ? p.C : p.ld, k.pos + i, k.c);
         b.rows.marks(sh, marked, k.i0 + i);
-        const auto step = [&](int t) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float a, na;
-                gates(elem<TT>(b.g[t], j), a, na);
-                A[j] *= a;
-                B[j] = BACK ? a * (elem<TT>(b.x[t], j) + B[j]) : fmaf(a, B[j], na * elem<TT>(b.x[t], j));
-            }
-        };
-        if (b.rows.simple) {
-#pragma unroll
-            for (int t = 0; t < T; ++t) step(BACK ? T - 1 - t : t);
-        } else {
-#pragma unroll
-            for (int u = 0; u < T; ++u) {
-                const int t = BACK ? T - 1 - u : u;
-                if ((BACK ? b.rows.last : b.rows.first) >> t & 1) A = -0.f, B = state_of(from, p, sh, k.i0 + i + t, k.c);
-                if (b.rows.r[t] >= 0) step(t);
-            }
-        }
+        fold<TT, ORDERED, BACK>(b.rows, b.g, b.x, from, p, sh, k, i, A, B);
     }
 }
 
@@ -502,9 +509,14 @@ __global__ __launch_bounds__(NT, TT::E == 8 ? 5 : 4) void k_lr_fwd(const void* _
     const Window w = open_window(p, span);
     const bool marked = mark(p, sh, span, w);
     f32x4_t h = 0.f;
-    if constexpr (ONE) {
-        f32x4_t A, B;
-        reduce<TT, ORDERED, false>(gate, x, h0, p, sh, w, marked, k, A, B);
+    Pair<TT, ORDERED> b;
+    if constexpr (ONE) {   // L = T: the strip stays in registers
+        f32x4_t A = 1.f, B = 0.f;
+        if (k.on) {
+            b.load(p, w, gate, x, p.ld, k.pos, k.c);
+            b.rows.marks(sh, marked, k.i0);
+            fold<TT, ORDERED, false>(b.rows, b.g, b.x, h0, p, sh, k, 0, A, B);
+        }
         join(p, sh, k, A, B, [&](int i, int c, const Map& m) { in[i * p.k.CW + c] = apply(m, 0.f); }, [](int, const Map&) {});
         __syncthreads();
         if (k.on) h = ld4(&in[k.at]);
@@ -512,10 +524,11 @@ __global__ __launch_bounds__(NT, TT::E == 8 ? 5 : 4) void k_lr_fwd(const void* _
         h = start_of<false>(p, tile, k);
     }
     if (k.on)
-        for (int i = 0; i < p.k.L; i += T) {
-            Pair<TT, ORDERED> b;
-            b.load(p, w, gate, x, p.ld, k.pos + i, k.c);
-            b.rows.marks(sh, marked, k.i0 + i);
+        for (int i = 0; i < (ONE ? T : p.k.L); i += T) {
+            if (!ONE) {
+                b.load(p, w, gate, x, p.ld, k.pos + i, k.c);
+                b.rows.marks(sh, marked, k.i0 + i);
+            }
             if (carry && k.pos + i < p.segs.n) st4(carry + int64_t((k.pos + i) / T) * p.C + k.c, h);
             const auto step = [&](int t) {
 #pragma unroll
@@ -580,9 +593,14 @@ __global__ __launch_bounds__(NT, TT::E == 8 ? 3 : 2) void k_lr_bwd(const void* _
     const Window w = open_window(p, span);
     const bool marked = mark(p, sh, span, w);
     f32x4_t E = 0.f;
+    Triple<TT, ORDERED> b;
     if constexpr (ONE) {
-        f32x4_t A, B;
-        reduce<TT, ORDERED, true>(gate, dout, dh_last, p, sh, w, marked, k, A, B);
+        f32x4_t A = 1.f, B = 0.f;
+        if (k.on) {
+            b.load(p, w, gate, x, dout, carry, k.pos, k.c);
+            b.rows.marks(sh, marked, k.i0);
+            fold<TT, ORDERED, true>(b.rows, b.g, b.d, dh_last, p, sh, k, 0, A, B);
+        }
         join(p, sh, k, A, B, [&](int i, int c, const Map& m) { in[i * p.k.CW + c] = apply(m, 0.f); }, [](int, const Map&) {});
         __syncthreads();
         if (k.on) E = ld4(&in[k.at]);
@@ -590,11 +608,12 @@ __global__ __launch_bounds__(NT, TT::E == 8 ? 3 : 2) void k_lr_bwd(const void* _
         E = start_of<true>(p, tile, k);
     }
     if (k.on)
-        for (int i = p.k.L - T; i >= 0; i -= T) {
+        for (int i = ONE ? 0 : p.k.L - T; i >= 0; i -= T) {
             if (k.pos + i >= p.segs.n) continue;
-            Triple<TT, ORDERED> b;
-            b.load(p, w, gate, x, dout, carry, k.pos + i, k.c);
-            b.rows.marks(sh, marked, k.i0 + i);
+            if (!ONE) {
+                b.load(p, w, gate, x, dout, carry, k.pos + i, k.c);
+                b.rows.marks(sh, marked, k.i0 + i);
+            }
             const auto& rows = b.rows;
             f32x4_t h = b.h;
             f32x4_t a[T], u[T];   // the gates as kept, and h_{t-1} - x_t

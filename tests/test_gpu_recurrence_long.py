@@ -76,3 +76,32 @@ def test_recurrence_long_sequences(C, dtype, reverse):
           a * na * ((before - X).abs() * be + big.abs() * (he0 + K * (before.abs() + X.abs()))), dtype, "dgate")
     close(dh0[full], (a * big)[first], (a * be + K * (a * big).abs())[first], torch.float32, "dh0")
     assert torch.equal(dh0[1], dl[1])
+
+
+@pytest.mark.parametrize("n", [120, 200, 300])
+def test_recurrence_few_rows_of_very_many_channels(n):
+    # enough elements for long strips, but hardly a tile of rows
+    C, K = 180224, 8 * R.EPS
+    print(f"wide recurrence n={n} C={C}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    gate, x, dh = (torch.randn(n, C, generator=g, device="cuda").bfloat16() for _ in range(3))
+    out, last, carry = spc.linear_recurrence_fwd(gate, x, want_carry=True)
+    dg, dx, _ = spc.linear_recurrence_bwd(dh, gate, x, None, carry)
+    a, na, X = torch.sigmoid(gate.double()), torch.sigmoid(-gate.double()), x.double()
+    h, e = torch.zeros(C, dtype=torch.float64, device="cuda"), torch.zeros(C, dtype=torch.float64, device="cuda")
+    before = []
+    for t in range(n):
+        before.append((h, e))
+        e = a[t] * e + K * (h.abs() + X[t].abs())
+        h = a[t] * h + na[t] * X[t]
+        close(out[t], h, e, torch.bfloat16, f"out {t}")
+    close(last[0], h, e, torch.float32, "h_last")
+    d, e = torch.zeros_like(h), torch.zeros_like(h)
+    for t in range(n - 1, -1, -1):
+        hp, he = before[t]
+        d = d + dh[t].double()
+        e = e + K * (d.abs() + dh[t].double().abs())
+        close(dx[t], na[t] * d, na[t] * (e + K * d.abs()), torch.bfloat16, f"dx {t}")
+        close(dg[t], a[t] * na[t] * (hp - X[t]) * d,
+              a[t] * na[t] * ((hp - X[t]).abs() * e + d.abs() * (he + K * (hp.abs() + X[t].abs()))), torch.bfloat16, f"dgate {t}")
+        d, e = a[t] * d, a[t] * e + K * (a[t] * d).abs()
