@@ -680,18 +680,43 @@ class Dropout:
     """Dropout of one call (spc_dropout): ``rng`` int64 [2] on the GPU holds
     {seed, offset}, ``p`` the probability, ``layer`` tells the calls of one
     step apart.  The mask is a function of these alone and is drawn again by
-    the backward; advance ``rng`` on the device between steps."""
+    the backward; advance ``rng`` on the device between steps.  All three may
+    be set again, for the calls that follow."""
 
     def __init__(self, rng: torch.Tensor, p: float, layer: int = 0):
+        self._arg = _DropArg()
+        self.rng, self.p, self.layer = rng, p, layer
+
+    @property
+    def rng(self) -> torch.Tensor:
+        return self._rng
+
+    @rng.setter
+    def rng(self, rng: torch.Tensor):
         _need(rng, "rng", torch.int64)
         if rng.shape != (2,):
             raise ValueError(f"rng must be [2] {{seed, offset}}, got {tuple(rng.shape)}")
+        self._rng = rng
+
+    @property
+    def p(self) -> float:
+        return self._p
+
+    @p.setter
+    def p(self, p: float):
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p={p} is outside [0, 1]")
+        self._p = self._arg.p = float(p)
+
+    @property
+    def layer(self) -> int:
+        return self._arg.layer
+
+    @layer.setter
+    def layer(self, layer: int):
         if not 0 <= layer < 1 << 32:
             raise ValueError(f"layer={layer} is not a 32-bit number")
-        self.rng, self.p, self.layer = rng, float(p), int(layer)
-        self._arg = _DropArg(rng.data_ptr(), self.layer, self.p)
+        self._arg.layer = int(layer)
 
 
 def _drop_arg(dropout, dev):
@@ -699,8 +724,9 @@ def _drop_arg(dropout, dev):
         return None
     if not isinstance(dropout, Dropout):
         raise TypeError("dropout must be a Dropout")
-    if dropout.rng.device != dev:
-        raise ValueError(f"rng is on {dropout.rng.device}, expected {dev}")
+    if dropout._rng.device != dev:
+        raise ValueError(f"rng is on {dropout._rng.device}, expected {dev}")
+    dropout._arg.rng = dropout._rng.data_ptr()   # where the tensor is now
     return ctypes.byref(dropout._arg)
 
 
