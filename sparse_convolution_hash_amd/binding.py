@@ -165,6 +165,17 @@ def _need(t: torch.Tensor, name: str, dtype=None, dev=None):
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
+def _scratch(workspace, need: int, like: torch.Tensor, least: int = 0):
+    """The caller's workspace where it holds ``need`` bytes, else a new one of
+    them (``least`` at least; none for 0) on the device of ``like``."""
+    if workspace is not None:
+        _need(workspace, "workspace", None, like.device)
+        if workspace.numel() >= need:
+            return workspace
+    need = max(need, least)
+    return like.new_empty((need,), dtype=torch.uint8) if need else None
+
+
 def version() -> str:
     return lib().spc_version().decode()
 
@@ -249,8 +260,7 @@ def build_kmap(coords: torch.Tensor, batch: int, shape: Sequence[int], ksize, st
     if device_count and out_cap is None and not subm:
         raise ValueError("device_count needs out_cap (count_first waits for the count)")
     if not subm and out_cap is None:
-        ws = workspace if workspace is not None and workspace.numel() >= ws_bytes else \
-            torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
+        ws = _scratch(workspace, ws_bytes, coords, 256)
         st = lib().spc_build_kmap(ctypes.byref(g), coords.data_ptr(), n, None, 0, ctypes.byref(n_out), None, None,
                                   None, None, None, 0, None, None, None, ws.data_ptr(), ws.numel(), stream)
         _check(st, "spc_build_kmap")
@@ -277,8 +287,7 @@ def build_kmap(coords: torch.Tensor, batch: int, shape: Sequence[int], ksize, st
     sizes = []
     for _, v in parts:
         sizes += [v, (-v) % 64]
-    if workspace is None or workspace.numel() < ws_bytes:
-        workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
+    workspace = _scratch(workspace, ws_bytes, coords, 256)
     buf = torch.empty(sum(sizes), dtype=torch.int32, device=dev)
     base, addr, o = buf.data_ptr(), {}, 0
     for i, (name, _) in enumerate(parts):
@@ -553,8 +562,7 @@ def conv_bwd_filter(feats: torch.Tensor, dout: torch.Tensor, K: int, pair_ptr: O
             _need(t, nm, torch.int32, dev)
     cin, cout = feats.shape[1], dout.shape[1]
     ws = conv_bwd_filter_workspace(feats.shape[0], dout.shape[0], cin, cout, int(K), bool(want_dbias))
-    if workspace is None or workspace.numel() < ws:
-        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+    workspace = _scratch(workspace, ws, feats, 256)
     if dw is None:
         dw = torch.empty((K, cin, cout), dtype=torch.float32, device=dev)
     db = torch.empty(cout, dtype=torch.float32, device=dev) if want_dbias else None
@@ -810,9 +818,7 @@ def _norm_checks(x, groups, seg_ptr, gamma, beta, act, workspace):
             _need_like(t, nm, torch.float32, dev, (C,))
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, got {act!r}")
-    need = group_norm_workspace(n, C, int(groups), n_seg)
-    if need and (workspace is None or workspace.numel() < need):
-        workspace = x.new_empty((need,), dtype=torch.uint8)
+    workspace = _scratch(workspace, group_norm_workspace(n, C, int(groups), n_seg), x)
     return dev, n, C, n_seg, workspace, 0 if workspace is None else workspace.numel()
 
 
@@ -901,9 +907,7 @@ def _lr_checks(gate, x, seg_ptr, h0, order, workspace):
     if order is not None:
         _need_like(order, "order", torch.int32, dev, (n,))
     ws, carry = linear_recurrence_workspace(x.dtype, n, C, n_seg)
-    if workspace is None or workspace.numel() < ws:
-        workspace = x.new_empty((ws,), dtype=torch.uint8)
-    return dev, n, C, n_seg, ld, workspace, carry
+    return dev, n, C, n_seg, ld, _scratch(workspace, ws, x), carry
 
 
 def linear_recurrence_fwd(gate: torch.Tensor, x: torch.Tensor, seg_ptr: Optional[torch.Tensor] = None,

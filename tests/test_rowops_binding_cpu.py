@@ -3,6 +3,7 @@ tensors here are on the CPU, with the binding's own check of that taken out
 where a function would refuse them, and nothing is launched."""
 
 import ctypes
+import os
 
 import pytest
 import torch
@@ -44,3 +45,63 @@ def test_dropout_checks_later_values_too(cpu_tensors):
         with pytest.raises(error):
             setattr(d, name, bad)
     assert (passed(d).rng, passed(d).p, passed(d).layer) == (a.data_ptr(), 0.5, 7)
+
+
+class Quiet:
+    """The library with its size queries, whose other calls do nothing."""
+
+    def __getattr__(self, name):
+        return getattr(B._lib, name) if name.endswith("_workspace") else lambda *a: B.SPC_OK
+
+
+@pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="libspc.so not built")
+@pytest.mark.parametrize("name", ["group_norm_fwd", "group_norm_bwd", "linear_recurrence_fwd", "linear_recurrence_bwd",
+                                  "conv_bwd_filter", "build_kmap", "build_kmap_strided"])
+def test_workspaces_are_checked(monkeypatch, name):
+    """A workspace is checked as every other tensor is: on the GPU, on the
+    call's device, contiguous.  (All tensors are on the CPU here; the others
+    pass for GPU tensors.)"""
+    B.lib()
+    need = B._need
+
+    def others_pass(t, nm, dtype=None, dev=None):
+        if nm == "workspace":
+            need(t, nm, dtype, dev)
+    monkeypatch.setattr(B, "_need", others_pass)
+    monkeypatch.setattr(B, "_gate_x", lambda gate, x, names=None: x.shape[1])
+    monkeypatch.setattr(B, "lib", Quiet)
+    monkeypatch.setattr(B, "_stream", lambda dev: None)
+    n, C = 100, 32
+    x, i = torch.zeros(n, C), torch.zeros(n, dtype=torch.int32)
+    carry = torch.zeros(B.linear_recurrence_workspace(x.dtype, n, C, 1)[1] // 4)
+    call = {
+        "group_norm_fwd": lambda w: B.group_norm_fwd(x, 4, workspace=w),
+        "group_norm_bwd": lambda w: B.group_norm_bwd(x, x, 4, None, None, None, torch.zeros(1, 4, 2), workspace=w),
+        "linear_recurrence_fwd": lambda w: B.linear_recurrence_fwd(x, x, workspace=w),
+        "linear_recurrence_bwd": lambda w: B.linear_recurrence_bwd(x, x, x, None, carry, workspace=w),
+        "conv_bwd_filter": lambda w: B.conv_bwd_filter(x, x, 1, None, None, None, workspace=w),
+        "build_kmap": lambda w: B.build_kmap(torch.zeros(n, 4, dtype=torch.int32), 1, (9, 9, 9), 3, workspace=w),
+        "build_kmap_strided": lambda w: B.build_kmap(torch.zeros(n, 4, dtype=torch.int32), 1, (9, 9, 9), 3, 2, 1, 1,
+                                                     subm=False, count_first=True, workspace=w),
+    }[name]
+    if name != "build_kmap_strided":         # takes its own workspace, on the CPU here, from its first call to its second
+        call(None)
+    for bytes_ in (16, 1 << 22):             # too small for any call, large enough for each
+        with pytest.raises(TypeError, match="workspace"):
+            call(torch.zeros(bytes_, dtype=torch.uint8))
+
+
+def test_workspace_device_and_layout(monkeypatch):
+    # what passes for a GPU tensor: is_cuda, on device 0
+    class Fake(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda", 0)
+    w = torch.zeros(64, dtype=torch.uint8).as_subclass(Fake)
+    assert B._scratch(w, 64, w) is w and B._scratch(None, 0, w) is None
+    assert B._scratch(w, 65, torch.zeros(1).as_subclass(Fake)).numel() == 65
+    with pytest.raises(ValueError, match="workspace is on"):
+        B._scratch(w, 64, torch.zeros(1))
+    with pytest.raises(ValueError, match="contiguous"):
+        B._scratch(w[::2], 16, w)
+    with pytest.raises(ValueError, match="contiguous"):
+        B._scratch(w[:1].expand(64), 64, w)
