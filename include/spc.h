@@ -427,7 +427,8 @@ spc_status spc_gather_by_voxel_id(spc_dtype dtype, const void* seg_features, int
 /*
  * ----------------------------------------------------------------------------
  * Row operators: what a residual block puts next to the convolutions, on the
- * same features [n, C] (channels last, C a positive multiple of 16).
+ * same features [n, C] (channels last, C a positive multiple of 16, at most
+ * 64 * 65535; n and the count of samples below 2^31 - 4096).
  *
  * Samples.  seg_ptr, device int32 [n_seg + 1], ascending: sample s owns the
  * rows [seg_ptr[s], seg_ptr[s+1]), of any length, 0 and 1 included (the rows

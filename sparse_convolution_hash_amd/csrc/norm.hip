@@ -208,30 +208,44 @@ __device__ __forceinline__ void for_parts(const NormArgs& p, int s, int g, F f) 
         }
 }
 
+// The reductions across runs take a workgroup for each of `jobs` things, up to
+// a grid that one launch holds; beyond it the workgroups go round again.
+constexpr unsigned JOBS = unsigned(((int64_t(1) << 32) - 1) / NG / 2);
+inline dim3 job_grid(int64_t jobs) { return dim3(jobs < JOBS ? unsigned(jobs) : JOBS); }
+template <typename F>
+__device__ __forceinline__ void for_jobs(unsigned jobs, F f) {
+    for (unsigned i = blockIdx.x; i < jobs; i += gridDim.x) {
+        f(i);
+        __syncthreads();   // the LDS is free again
+    }
+}
+
 // Group mean and reciprocal deviation from the runs' means and spreads, whose
 // squares are taken around the first of the means; an empty sample gets mean 0
 // and variance 0.
-__global__ __launch_bounds__(NG) void k_norm_group(NormArgs p, const float2* __restrict__ part, float2* __restrict__ stats) {
+__global__ __launch_bounds__(NG) void k_norm_group(NormArgs p, unsigned groups, const float2* __restrict__ part, float2* __restrict__ stats) {
     __shared__ double2 lds[NG / WAVE];
-    const int s = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
-    const int a = p.segs.at(s), b = p.segs.at(s + 1);
-    double mean = 0, var = 0;
-    if (a < b) {
-        const double k = part[(int64_t(a / p.k.R) + s) * p.C + g * (p.C / p.G)].x;
-        double s1 = 0, s2 = 0;
-        for_parts(p, s, g, [&](int64_t slot, int rows, int c) {
-            const float2 v = part[slot * p.C + c];
-            const double d = double(v.x) - k;
-            s1 += double(rows) * d;
-            s2 += double(v.y) + double(rows) * d * d;
-        });
-        sum_block(s1, s2, lds);
-        const double cnt = double(b - a) * (p.C / p.G), m = s1 / cnt;
-        mean = k + m;
-        var = s2 / cnt - m * m;
-        var = var > 0 || var != var ? var : 0;
-    }
-    if (threadIdx.x == 0) stats[blockIdx.x] = float2{float(mean), float(1.0 / sqrt(var + double(p.eps)))};
+    for_jobs(groups, [&](unsigned job) {
+        const int s = int(job / p.G), g = int(job % p.G);
+        const int a = p.segs.at(s), b = p.segs.at(s + 1);
+        double mean = 0, var = 0;
+        if (a < b) {
+            const double k = part[(int64_t(a / p.k.R) + s) * p.C + g * (p.C / p.G)].x;
+            double s1 = 0, s2 = 0;
+            for_parts(p, s, g, [&](int64_t slot, int rows, int c) {
+                const float2 v = part[slot * p.C + c];
+                const double d = double(v.x) - k;
+                s1 += double(rows) * d;
+                s2 += double(v.y) + double(rows) * d * d;
+            });
+            sum_block(s1, s2, lds);
+            const double cnt = double(b - a) * (p.C / p.G), m = s1 / cnt;
+            mean = k + m;
+            var = s2 / cnt - m * m;
+            var = var > 0 || var != var ? var : 0;
+        }
+        if (threadIdx.x == 0) stats[job] = float2{float(mean), float(1.0 / sqrt(var + double(p.eps)))};
+    });
 }
 
 // v sigmoid(z), v = 1 / inv
@@ -383,48 +397,50 @@ __global__ __launch_bounds__(NT) void k_norm_bwd_sums(const void* __restrict__ x
         tot[(int64_t(q.tile) * p.k.Y + q.y) * p.C + q.slab * p.k.CW + threadIdx.x] = float2{float(t.x), float(t.y)};
 }
 
-// Workgroups [0, groups), groups = samples * G: the group's means of gamma dz
-// and gamma dz xhat.  Workgroups after them: dbeta and dgamma of 8 channels
-// each, from ntot rows of tot.
-__global__ __launch_bounds__(NG) void k_norm_bwd_group(NormArgs p, int64_t groups, const float* __restrict__ gamma,
+// Jobs [0, groups), groups = samples * G: the group's means of gamma dz and
+// gamma dz xhat.  Jobs after them: dbeta and dgamma of 8 channels each, from
+// ntot rows of tot.
+__global__ __launch_bounds__(NG) void k_norm_bwd_group(NormArgs p, unsigned jobs, unsigned groups, const float* __restrict__ gamma,
                                                        const float2* __restrict__ part, const float2* __restrict__ tot,
                                                        int ntot, float2* __restrict__ means, float* __restrict__ dgamma,
                                                        float* __restrict__ dbeta) {
     __shared__ double2 lds[NG / WAVE];
-    double a = 0, b = 0;
-    if (int64_t(blockIdx.x) < groups) {
-        const int s = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
-        for_parts(p, s, g, [&](int64_t slot, int, int c) {
-            const float2 v = part[slot * p.C + c];
-            const double w = gamma ? gamma[c] : 1.f;
-            a += w * v.x;
-            b += w * v.y;
-        });
-        sum_block(a, b, lds);
-        const double cnt = double(p.segs.at(s + 1) - p.segs.at(s)) * (p.C / p.G);
-        if (threadIdx.x == 0) means[blockIdx.x] = cnt > 0 ? float2{float(a / cnt), float(b / cnt)} : float2{0.f, 0.f};
-        return;
-    }
-    const int c = int(blockIdx.x - groups) * 8 + int(threadIdx.x) % 8;
-#pragma unroll 4
-    for (int t = int(threadIdx.x) / 8; t < ntot; t += NG / 8) {
-        const float2 v = tot[int64_t(t) * p.C + c];
-        a += v.x;
-        b += v.y;
-    }
-    // 8 channels side by side: over the lanes 8 apart, then over the waves
-#pragma unroll
-    for (int o = 8; o < WAVE; o <<= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
     __shared__ double2 ch[NG / WAVE][8];
-    if (threadIdx.x % WAVE < 8) ch[threadIdx.x / WAVE][threadIdx.x % WAVE] = double2{a, b};
-    __syncthreads();
-    if (threadIdx.x < 8) {
-        a = b = 0;
+    for_jobs(jobs, [&](unsigned job) {
+        double a = 0, b = 0;
+        if (job < groups) {
+            const int s = int(job / p.G), g = int(job % p.G);
+            for_parts(p, s, g, [&](int64_t slot, int, int c) {
+                const float2 v = part[slot * p.C + c];
+                const double w = gamma ? gamma[c] : 1.f;
+                a += w * v.x;
+                b += w * v.y;
+            });
+            sum_block(a, b, lds);
+            const double cnt = double(p.segs.at(s + 1) - p.segs.at(s)) * (p.C / p.G);
+            if (threadIdx.x == 0) means[job] = cnt > 0 ? float2{float(a / cnt), float(b / cnt)} : float2{0.f, 0.f};
+            return;
+        }
+        const int c = int(job - groups) * 8 + int(threadIdx.x) % 8;
+#pragma unroll 4
+        for (int t = int(threadIdx.x) / 8; t < ntot; t += NG / 8) {
+            const float2 v = tot[int64_t(t) * p.C + c];
+            a += v.x;
+            b += v.y;
+        }
+        // 8 channels side by side: over the lanes 8 apart, then over the waves
 #pragma unroll
-        for (int w = 0; w < NG / WAVE; ++w) a += ch[w][threadIdx.x].x, b += ch[w][threadIdx.x].y;
-        if (dbeta) dbeta[c] = float(a);
-        if (dgamma) dgamma[c] = float(b);
-    }
+        for (int o = 8; o < WAVE; o <<= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
+        if (threadIdx.x % WAVE < 8) ch[threadIdx.x / WAVE][threadIdx.x % WAVE] = double2{a, b};
+        __syncthreads();
+        if (threadIdx.x < 8) {
+            a = b = 0;
+#pragma unroll
+            for (int w = 0; w < NG / WAVE; ++w) a += ch[w][threadIdx.x].x, b += ch[w][threadIdx.x].y;
+            if (dbeta) dbeta[c] = float(a);
+            if (dgamma) dgamma[c] = float(b);
+        }
+    });
 }
 
 template <typename TT, int ACT, bool DROP>
@@ -657,21 +673,21 @@ struct NormWs {
 };
 
 spc_status check_sizes(int64_t n, int32_t C, int32_t G, int64_t n_seg, NormWs& w) {
-    if (n < 0 || n >= (int64_t(1) << 31) - 8192) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
-    if (n_seg < 1 || n_seg >= (int64_t(1) << 31) - 1) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)n_seg);
+    if (n < 0 || n >= ROWS_END) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
+    if (n_seg < 1 || n_seg >= ROWS_END) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)n_seg);
     if (C <= 0 || C % 16) return fail(SPC_ERR_UNSUPPORTED, "C=%d: channels must be a positive multiple of 16", C);
     if (G < 1 || C % G) return fail(SPC_ERR_ARG, "groups=%d does not divide C=%d", G, C);
-    if (ceil_div(C, 64) > 65535) return fail(SPC_ERR_UNSUPPORTED, "C=%d is beyond one launch", C);
+    if (C > C_MAX) return fail(SPC_ERR_UNSUPPORTED, "C=%d: at most %d channels", C, C_MAX);
     w.k = cut_of(n, C, n_seg);
     w.part = (w.k.tiles + n_seg) * C;
     w.tot = int64_t(w.k.tiles) * w.k.Y * C;
     w.stats = n_seg * G;
     w.CW = small_width(C, G);
     const int64_t all = n * w.CW;
-    if (!(w.CW <= NS && (all <= SMALL || (all <= SMALL_MAX && all <= SMALL_MEAN * n_seg)) && w.stats <= (int64_t(1) << 24))) w.CW = 0;
+    if (!(w.CW <= NS && (all <= SMALL || (all <= SMALL_MAX && all <= SMALL_MEAN * n_seg)) && launchable(n_seg * (C / w.CW), NS))) w.CW = 0;
     if (w.CW) w.part = n_seg > 1 ? n_seg * C : 0, w.tot = 0;      // the samples' sums of the backward
-    if (int64_t(w.k.tiles) * w.k.nslab >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
-    if (w.stats + C >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld groups are beyond one launch", (long long)w.stats);
+    if (!launchable(int64_t(w.k.tiles) * w.k.Y * w.k.nslab, NT)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
+    if (w.stats + C >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld groups are too many", (long long)w.stats);
     return SPC_OK;
 }
 
@@ -718,7 +734,7 @@ spc_status launch_fwd(const void* x, const NormArgs& p, const NormWs& w, const f
         hipLaunchKernelGGL(k_norm_stats<TT>, grid, dim3(NT), 0, stream, x, p, part);
         SPC_LAUNCHED("k_norm_stats");
     }
-    hipLaunchKernelGGL(k_norm_group, dim3(unsigned(w.stats)), dim3(NG), 0, stream, p, part, stats);
+    hipLaunchKernelGGL(k_norm_group, job_grid(w.stats), dim3(NG), 0, stream, p, unsigned(w.stats), part, stats);
     SPC_LAUNCHED("k_norm_group");
     if (p.k.tiles) NORM_VARIANT(k_norm_apply, grid, NT, x, p, gamma, beta, stats, y);
     return SPC_OK;
@@ -736,16 +752,17 @@ spc_status launch_bwd(const void* dy, const void* x, const NormArgs& p, const No
         NORM_VARIANT(k_norm_bwd_small, dim3(unsigned(p.segs.n_seg) * unsigned(p.C / CW)), NS, x, dy, p, CW, gamma, beta, stats, tot,
                      one ? dgamma : nullptr, one ? dbeta : nullptr, dx);
         if (tot) {
-            hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(p.C / 8)), dim3(NG), 0, stream, p, 0, gamma, part, tot, p.segs.n_seg, means,
-                               dgamma, dbeta);
+            hipLaunchKernelGGL(k_norm_bwd_group, job_grid(p.C / 8), dim3(NG), 0, stream, p, unsigned(p.C / 8), 0u, gamma, part, tot,
+                               p.segs.n_seg, means, dgamma, dbeta);
             SPC_LAUNCHED("k_norm_bwd_group");
         }
         return SPC_OK;
     }
     const dim3 grid(p.k.blocks());
     if (p.k.tiles) NORM_VARIANT(k_norm_bwd_sums, grid, NT, x, dy, p, gamma, beta, stats, part, tot);
-    const int64_t blocks = w.stats + (affine ? p.C / 8 : 0);
-    hipLaunchKernelGGL(k_norm_bwd_group, dim3(unsigned(blocks)), dim3(NG), 0, stream, p, w.stats, gamma, part, tot, p.k.tiles * p.k.Y, means, dgamma, dbeta);
+    const int64_t jobs = w.stats + (affine ? p.C / 8 : 0);
+    hipLaunchKernelGGL(k_norm_bwd_group, job_grid(jobs), dim3(NG), 0, stream, p, unsigned(jobs), unsigned(w.stats), gamma, part, tot,
+                       p.k.tiles * p.k.Y, means, dgamma, dbeta);
     SPC_LAUNCHED("k_norm_bwd_group");
     if (p.k.tiles) NORM_VARIANT(k_norm_bwd_apply, grid, NT, x, dy, p, gamma, beta, stats, means, dx);
     return SPC_OK;

@@ -683,10 +683,13 @@ __global__ __launch_bounds__(256) void k_lr_step(const void* gate, const void* x
 
 spc_status check_sizes(spc_dtype dtype, int64_t n, int32_t C, int64_t n_seg) {
     if (dtype != SPC_F32 && dtype != SPC_F16 && dtype != SPC_BF16) return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
-    if (n < 0 || n >= (int64_t(1) << 31) - 4096) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
-    if (n_seg < 1 || n_seg >= (int64_t(1) << 31) - 1) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)n_seg);
+    if (n < 0 || n >= ROWS_END) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
+    if (n_seg < 1 || n_seg >= ROWS_END) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)n_seg);
     if (C <= 0 || C % 16) return fail(SPC_ERR_UNSUPPORTED, "C=%d: channels must be a positive multiple of 16", C);
-    if (ceil_div(C, WAVE) > 65535) return fail(SPC_ERR_UNSUPPORTED, "C=%d is beyond one launch", C);
+    if (C > C_MAX) return fail(SPC_ERR_UNSUPPORTED, "C=%d: at most %d channels", C, C_MAX);
+    const Cut k = cut_of(n, C);
+    if (!launchable(int64_t(k.tiles) * k.nslab, NT))
+        return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
     return SPC_OK;
 }
 
@@ -719,7 +722,6 @@ spc_status check_call(spc_dtype dtype, int64_t n, int32_t C, int64_t ld, const i
     p.segs = Segs{seg_ptr, int32_t(n_seg), int32_t(n)};
     p.C = C, p.reverse = reverse != 0, p.ld = ld, p.ldg = C, p.order = order;
     p.k = cut_of(n, C);
-    if (int64_t(p.k.tiles) * p.k.nslab >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
     p.strip = static_cast<float2*>(ws);
     p.tile = p.strip + int64_t(p.k.tiles) * p.k.NCH * C;
     p.start = reinterpret_cast<float*>(p.tile + int64_t(p.k.tiles) * C);
@@ -854,7 +856,7 @@ extern "C" spc_status spc_linear_recurrence_step(spc_dtype dtype, const void* ga
     for (const void* q : {gate, x, (const void*)state, (const void*)new_state, (const void*)out})
         if (!aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     const int64_t blocks = ceil_div(n * C, 8 * 256);
-    if (blocks >= (int64_t(1) << 31)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
+    if (!launchable(blocks, 256)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
     LR_DISPATCH(k_lr_step, dim3(unsigned(blocks)), dim3(256), gate, x, ld, n, C, state, new_state, out);
     return SPC_OK;
 }

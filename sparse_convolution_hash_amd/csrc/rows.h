@@ -72,6 +72,15 @@ __device__ __forceinline__ Raw8<BF16> narrow<BF16>(const f32x8_t& f) {
 
 // --------------------------------------------------------- ragged samples
 
+// What the host checks hold every call to: n and n_seg below ROWS_END, so that
+// rounded up to tiles and waves they are still ints, and at most C_MAX channels.
+constexpr int64_t ROWS_END = (int64_t(1) << 31) - 4096;
+constexpr int32_t C_MAX = 64 * 65535;
+
+// Whether one launch can have that many workgroups: it holds fewer than 2^32
+// threads, and of a larger grid the runtime starts a part without an error.
+inline bool launchable(int64_t blocks, int threads) { return blocks * threads < (int64_t(1) << 32); }
+
 // Sample s owns the rows [at(s), at(s + 1)).  ptr NULL is one sample of all n
 // rows.  The offsets come from device memory unchecked, so each is clamped to
 // [0, n]: whatever they hold, no row outside the arrays is touched.
