@@ -13,7 +13,9 @@
 // tiles + samples of them, and a sample's runs lie side by side.  Three
 // launches each way: per-channel sums of every run, their reduction to group
 // (and channel) values, the elementwise pass.  A thread's sums are fp32, over
-// at most 16 rows; all above are double, in a fixed order (no atomics).
+// at most 16 rows; all above are double, in a fixed order (no atomics), with one
+// rounding to fp32 where a run's pair is stored for the next launch (half the
+// bytes; it is off by half a unit, next to a thread's 16 roundings).
 //
 // What bounds it: x is read twice forward, x and dy twice backward, the second
 // time mostly from the 256 MB cache, so on 266,426 x 128 bf16 (68 MB a tensor)
@@ -143,7 +145,8 @@ __device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, cons
 // Mean and sum of squared differences of every run, per channel.  The sums
 // are taken of differences from the run's first row, which lies within the
 // data: sum (x - k)^2 is then at most rows + 1 times the spread around the
-// mean, and the subtraction below costs at most that factor in precision.
+// mean (twice it for an ordinary row), and the roundings of a thread's squares
+// count by at most that factor.  (k_norm_small: the rows of its sample.)
 template <typename TT>
 __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, NormArgs p, float2* __restrict__ part) {
     using S = typename TT::storage;
@@ -175,8 +178,9 @@ __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, 
         }
         reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int c, double t1, double t2) {
             if (q.slab * p.k.CW + c >= p.C) return;
-            const float inv = 1.f / float(b - a), m = float(t1) * inv, m2 = float(t2 - t1 * m);
-            part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + c] = float2{base[c] + m, m2 > 0.f || m2 != m2 ? m2 : 0.f};
+            // in double: t1 m is up to (first row - mean)^2 / variance times what is left of t2
+            const double m = t1 / double(b - a), m2 = t2 - t1 * m;
+            part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + c] = float2{float(double(base[c]) + m), m2 > 0. || m2 != m2 ? float(m2) : 0.f};
         });
     });
 }
