@@ -695,6 +695,9 @@ class Dropout:
         self._arg = _DropArg()
         self.rng, self.p, self.layer = rng, p, layer
 
+    def __reduce__(self):   # a copy has a descriptor of its own
+        return type(self), (self._rng, self._p, self.layer)
+
     @property
     def rng(self) -> torch.Tensor:
         return self._rng

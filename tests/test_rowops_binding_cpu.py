@@ -2,6 +2,7 @@
 tensors here are on the CPU, with the binding's own check of that taken out
 where a function would refuse them, and nothing is launched."""
 
+import copy
 import ctypes
 import os
 
@@ -105,3 +106,14 @@ def test_workspace_device_and_layout(monkeypatch):
         B._scratch(w[::2], 16, w)
     with pytest.raises(ValueError, match="contiguous"):
         B._scratch(w[:1].expand(64), 64, w)
+
+
+def test_dropout_copies_are_their_own(cpu_tensors):
+    a = torch.tensor([1, 2])
+    d = B.Dropout(a, 0.5, 7)
+    for c in (copy.copy(d), copy.deepcopy(d)):
+        assert (c.p, c.layer) == (0.5, 7) and torch.equal(c.rng, a)
+        c.p, c.layer = 0.25, 9
+        assert (passed(c).rng, passed(c).p, passed(c).layer) == (c.rng.data_ptr(), 0.25, 9)
+        assert (passed(d).rng, passed(d).p, passed(d).layer) == (a.data_ptr(), 0.5, 7)
+    assert copy.copy(d).rng is a
