@@ -530,7 +530,8 @@ spc_status spc_linear_recurrence_workspace(spc_dtype dtype, int64_t n, int32_t C
  * [n_seg, C] (NULL ok) the ones after the last, h0 for an empty sample.
  * carry (NULL ok): states that spc_linear_recurrence_bwd starts from,
  * spc_linear_recurrence_workspace's bytes, of no documented layout.
- * A NaN or infinity stays within its channel and sample.
+ * A NaN or infinity stays within its channel and sample (an infinite state
+ * may turn into a NaN further along).
  */
 spc_status spc_linear_recurrence_fwd(spc_dtype dtype, const void* gate, const void* x, int64_t ld, int64_t n, int32_t C,
                                      const int32_t* seg_ptr, int64_t n_seg, const int32_t* order, int32_t reverse,

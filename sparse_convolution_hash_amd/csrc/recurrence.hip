@@ -25,9 +25,11 @@
 // 30 + 6 + 75 (5.0 TB/s).  1,000,003 x 64 bf16 forward: 54 + 7 + 70, 142 us with
 // the gaps between launches.  A single pass whose workgroups wait for the maps of
 // the tiles before theirs reads once, and measured 123 us there and 184 for the
-// 194 us of training above; but either its waits rest on the order in which
-// workgroups start, or the order is taken from one counter, which costs 11 ns a
-// workgroup (151 and 221 us).  Here no workgroup waits for another one.
+// 194 us of training above.  Two forms of it were built: with waits that rest on the
+// order in which workgroups start (those figures), and with the order taken from one
+// counter, which costs 11 ns a workgroup (151 and 221 us).  Here no workgroup waits
+// for another one.  A grid of workgroups that are all resident, and long sequences in
+// pieces whose second read stays in the cache, have not been measured.
 #include "rows.h"
 
 namespace spc {
