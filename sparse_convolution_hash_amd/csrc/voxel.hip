@@ -416,22 +416,21 @@ extern "C" spc_status spc_gather_by_voxel_id(spc_dtype dtype, const void* seg_fe
     for (const void* p : {seg_features, (const void*)pc_voxel_id, (const void*)out})
         if (p && !aligned16(p)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     const int32_t nv = n_voxels > 0 ? int32_t(n_voxels) : 0;
-    const int64_t threads = n_points * (C / (dtype == SPC_F32 ? 4 : 8));
-    const dim3 grid(unsigned(ceil_div(threads, VT)));
-    switch (dtype) {
-        case SPC_F32:
-            hipLaunchKernelGGL(k_gather_by_id<F32>, grid, dim3(VT), 0, stream, seg_features, nv, C, pc_voxel_id,
-                               int32_t(n_points), out);
-            break;
-        case SPC_F16:
-            hipLaunchKernelGGL(k_gather_by_id<F16>, grid, dim3(VT), 0, stream, seg_features, nv, C, pc_voxel_id,
-                               int32_t(n_points), out);
-            break;
-        case SPC_BF16:
-            hipLaunchKernelGGL(k_gather_by_id<BF16>, grid, dim3(VT), 0, stream, seg_features, nv, C, pc_voxel_id,
-                               int32_t(n_points), out);
-            break;
+    // a launch holds fewer than 2^32 threads (of a larger grid the runtime starts a part, without an error)
+    const int64_t cpr = C / (dtype == SPC_F32 ? 4 : 8);
+    const int64_t most = std::min<int64_t>(((int64_t(1) << 32) - VT) / cpr, (int64_t(1) << 31) - 1);
+    for (int64_t i = 0; i < n_points; i += most) {
+        const int64_t n = std::min(most, n_points - i);
+        const dim3 grid(unsigned(ceil_div(n * cpr, VT)));
+        const int32_t* ids = pc_voxel_id + i;
+        void* o = static_cast<char*>(out) + i * cpr * 16;
+        if (dtype == SPC_F32)
+            hipLaunchKernelGGL(k_gather_by_id<F32>, grid, dim3(VT), 0, stream, seg_features, nv, C, ids, int32_t(n), o);
+        else if (dtype == SPC_F16)
+            hipLaunchKernelGGL(k_gather_by_id<F16>, grid, dim3(VT), 0, stream, seg_features, nv, C, ids, int32_t(n), o);
+        else
+            hipLaunchKernelGGL(k_gather_by_id<BF16>, grid, dim3(VT), 0, stream, seg_features, nv, C, ids, int32_t(n), o);
+        SPC_LAUNCHED("k_gather_by_id");
     }
-    SPC_LAUNCHED("k_gather_by_id");
     return SPC_OK;
 }
