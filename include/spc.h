@@ -490,7 +490,7 @@ spc_status spc_group_norm_workspace(int64_t n, int32_t C, int32_t groups, int64_
  * SPC_ACT_*; drop NULL for none.  x, y [n, C]; y may be x.
  * stats fp32 [n_seg, groups, 2] receives mean and rstd for the backward (an
  * empty sample: mean 0, variance 0).  Sums are fp32 over at most 16 rows,
- * of differences from a row of the data, and double above that, rounded to
+ * of differences from a value of the data, and double above that, rounded to
  * fp32 once between launches.
  * ws: spc_group_norm_workspace bytes, scratch (NULL ok if that is 0).
  */

@@ -142,11 +142,24 @@ __device__ __forceinline__ void reduce_rows(int CW, int RL, int rl, int c8, cons
     __syncthreads();
 }
 
-// Mean and sum of squared differences of every run, per channel.  The sums
-// are taken of differences from the run's first row, which lies within the
-// data: sum (x - k)^2 is then at most rows + 1 times the spread around the
-// mean (twice it for an ordinary row), and the roundings of a thread's squares
-// count by at most that factor.  (k_norm_small: the rows of its sample.)
+// A value within rows [a, b) for sums of differences and their squares, per
+// channel: the median of the first, the middle and the last row.  The roundings of
+// (x - k)^2 count by 1 + (k - mean)^2 / variance, about twice for any ordinary
+// row; one far from all others would make it the count of rows (first tokens and
+// borders often are: on 1,000 constant rows after such a one the variance was off
+// by 430 units of 2^-24, with the median it is within 6), and the median takes it only
+// if two of the three are.  Each run or sample takes one: two loads more, side by side.
+template <typename TT>
+__device__ __forceinline__ f32x8_t middle_of(const typename TT::storage* x, int a, int b, const NormArgs& p, int ch) {
+    const f32x8_t u = widen<TT>(ld8<TT>(x + int64_t(a) * p.C + ch)), v = widen<TT>(ld8<TT>(x + int64_t(a + (b - a) / 2) * p.C + ch)),
+                  w = widen<TT>(ld8<TT>(x + int64_t(b - 1) * p.C + ch));
+    f32x8_t k;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k[j] = __builtin_amdgcn_fmed3f(u[j], v[j], w[j]);
+    return k;
+}
+
+// Mean and sum of squared differences of every run, per channel.
 template <typename TT>
 __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, NormArgs p, float2* __restrict__ part) {
     using S = typename TT::storage;
@@ -156,7 +169,7 @@ __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, 
     const S* x = static_cast<const S*>(x_);
     const Place q(p);
     for_runs(p, q, [&](int s, int a, int b) {
-        const f32x8_t k = widen<TT>(ld8<TT>(x + int64_t(a) * p.C + q.ch));
+        const f32x8_t k = middle_of<TT>(x, a, b, p, q.ch);
         if (q.rl == 0)
 #pragma unroll
             for (int j = 0; j < 8; ++j) base[q.c + j] = k[j];
@@ -178,7 +191,7 @@ __global__ __launch_bounds__(NT) void k_norm_stats(const void* __restrict__ x_, 
         }
         reduce_rows<NT>(p.k.CW, p.k.RL, q.rl, q.c, s1, s2, lds, sums, [&](int c, double t1, double t2) {
             if (q.slab * p.k.CW + c >= p.C) return;
-            // in double: t1 m is up to (first row - mean)^2 / variance times what is left of t2
+            // in double: t1 m is (base - mean)^2 / variance times what is left of t2
             const double m = t1 / double(b - a), m2 = t2 - t1 * m;
             part[int64_t(q.tile + s) * p.C + q.slab * p.k.CW + c] = float2{float(double(base[c]) + m), m2 > 0. || m2 != m2 ? float(m2) : 0.f};
         });
@@ -549,7 +562,7 @@ __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, i
                                                    const float* __restrict__ beta, float2* __restrict__ stats, void* y_) {
     using S = typename TT::storage;
     __shared__ float2 lds[NS * 8];
-    __shared__ double2 sums[NS], chan[NS];   // chan: a channel's sums around its value in the first row, base
+    __shared__ double2 sums[NS], chan[NS];   // chan: a channel's sums around base
     __shared__ float base[NS];
     const S* x = static_cast<const S*>(x_);
     S* y = static_cast<S*>(y_);
@@ -563,7 +576,7 @@ __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, i
     const uint64_t seed = DROP ? p.drop.rng[0] : 0, offset = DROP ? p.drop.rng[1] : 0;
     Chan8 c(p, gamma, beta, q.ch);
     if (DROP && ACT != SPC_ACT_SILU) c.gamma *= p.drop.scale, c.beta *= p.drop.scale;
-    const f32x8_t k = widen<TT>(ld8<TT>(x + int64_t(q.a) * p.C + q.ch));
+    const f32x8_t k = middle_of<TT>(x, q.a, q.b, p, q.ch);
     if (q.rl == 0)
 #pragma unroll
         for (int j = 0; j < 8; ++j) base[q.c + j] = k[j];
@@ -576,7 +589,7 @@ __global__ __launch_bounds__(NS) void k_norm_small(const void* x_, NormArgs p, i
     }
     reduce_rows<NS>(CW, q.RL, q.rl, q.c, s1, s2, lds, sums, [&](int i, double t1, double t2) { chan[i] = double2{t1, t2}; });
     float2* const group = lds;   // free again
-    // around the value of the group's first channel k: sum (x - k) and its square
+    // around the base of the group's first channel k: sum (x - k) and its square
     const double rows = double(q.b - q.a), cnt = rows * cg;
     sum_groups(CW, cg,
                [&](int g, int i) {

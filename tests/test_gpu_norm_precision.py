@@ -57,8 +57,8 @@ def whole(seed, n, C, top):
 
 @pytest.mark.parametrize("C,G,tile", [(16, 1, 512), (16, 2, 512), (64, 8, 128), (48, 3, 168)])
 def test_norm_first_rows_of_runs_are_outliers(C, G, tile):
-    # a run's spread is taken from sums around its first row, here 700 from all
-    # others: at a sample's start and at the start of a later tile, in runs of lengths that are no powers of two
+    # first rows 700 from all others: at a sample's start and at the start of a
+    # later tile, in runs of lengths that are no powers of two
     ptr = [0, 1733, 5000, 9000]
     x = whole(C, 9000, C, 2)
     for r in (0, 1536, 1733, 4608, 5000, 8704):
