@@ -562,6 +562,117 @@ spc_status spc_linear_recurrence_step(spc_dtype dtype, const void* gate, const v
                                       const float* state, float* new_state, void* out, hipStream_t stream);
 
 /*
+ * ----------------------------------------------------------------------------
+ * Attention block: what a block of attention over voxels puts next to the
+ * convolutions, by the row operators' conventions (samples, rounding, results
+ * that repeat, asynchronous calls of kernels only).
+ */
+
+/* Host only.  Workspace bytes of spc_layer_norm_bwd. */
+spc_status spc_layer_norm_workspace(int64_t n, int32_t C, size_t* bytes);
+
+/*
+ * Layer norm over the channels of each row, after the residual join:
+ *   u = x + residual (rounded as stored),  mean and variance (of the
+ *   population) over u's channels,  y = gamma (u - mean) rstd + beta,
+ *   rstd = (var + eps)^-1/2
+ * x, residual, y, total [n, C], C a positive multiple of 16 up to 4096; gamma,
+ * beta fp32 [C] (NULL: 1 and 0).  residual and total come together: total
+ * receives u (NULL both: u is x).  y may be x, total may be x or residual.
+ * stats fp32 [n, 2] receives mean and rstd.
+ */
+spc_status spc_layer_norm_fwd(spc_dtype dtype, const void* x, const void* residual, int64_t n, int32_t C,
+                              const float* gamma, const float* beta, float eps, void* y, void* total, float* stats,
+                              hipStream_t stream);
+
+/*
+ * Backward from u (x here: the forward's total, or its x) and stats: with
+ * h = (u - mean) rstd and w = gamma dout,
+ *   dx = rstd (w - mean(w) - h mean(w h)) + dtotal,
+ *   dgamma = sum dout h,  dbeta = sum dout  over the rows.
+ * dtotal [n, C] (NULL: 0) is the gradient that reaches u past the norm; dx is
+ * the gradient of x and of the residual alike.  dx may be dout or dtotal, not
+ * x; dgamma, dbeta fp32 [C], overwritten, each NULL ok.  Their sums are fp32
+ * over at most 16 rows and double above that, rounded to fp32 once between
+ * launches.  ws: spc_layer_norm_workspace bytes, scratch (NULL ok if that is 0,
+ * or without dgamma and dbeta).
+ */
+spc_status spc_layer_norm_bwd(spc_dtype dtype, const void* dout, const void* x, int64_t n, int32_t C,
+                              const float* gamma, const float* stats, const void* dtotal, void* dx, float* dgamma,
+                              float* dbeta, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Rotary positions of several axes.  x: n rows of heads x head_dim elements,
+ * ldx elements apart; head_dim a multiple of 16 up to 4096.  Pair j of a head
+ * is its elements (2j, 2j + 1).  The first pairs[0] pairs (HOST array, n_axes
+ * of 1 to 8 entries, at most head_dim / 2 in all) belong to axis 0, the next
+ * to axis 1, and so on; pair j of axis a of row i is rotated by
+ *   t = pos[i * ldp + a] * freq[j]:  (x, y) -> (x cos t - y sin t, x sin t + y cos t)
+ * and pairs past these are copied.  pos int32, aligned to 4 bytes (the
+ * coordinates' columns 1 to 3 are the axes z, y, x), freq fp32 [sum of pairs]
+ * in radians.  inverse != 0 rotates by -t, which is the gradient.  Angles lose
+ * nothing at far positions (products in double).  out: rows ldo elements
+ * apart; it may be x with ldo = ldx.
+ */
+spc_status spc_rotary(spc_dtype dtype, const void* x, int64_t ldx, int64_t n, int32_t heads, int32_t head_dim,
+                      const int32_t* pos, int64_t ldp, int32_t n_axes, const int32_t* pairs, const float* freq,
+                      int32_t inverse, void* out, int64_t ldo, hipStream_t stream);
+
+/*
+ * Attention of the queries of each sample to the keys of the same sample.
+ * Samples: q_ptr, kv_ptr int32 [n_seg + 1] as seg_ptr above, over n_q and n_kv
+ * rows (NULL with n_seg = 1: all rows).  Windows along a curve are samples.
+ * q_order, kv_order int32 [n_q], [n_kv] (NULL: rows in place): position t is
+ * row order[t], no row twice; an entry outside [0, n) is a position without a
+ * row.  heads a multiple of kv_heads: query head h reads key head
+ * h / (heads / kv_heads).  head_dim a multiple of 16 up to 128.  causal != 0:
+ * of a sample's lq queries and lk keys, query i sees the keys j <= i + lk - lq
+ * (its last query sees all).  scale positive and finite.
+ */
+typedef struct spc_attention {
+    int64_t n_q, n_kv, n_seg;
+    int32_t heads, kv_heads, head_dim, causal;
+    float scale;
+    const int32_t* q_ptr;
+    const int32_t* kv_ptr;
+    const int32_t* q_order;
+    const int32_t* kv_order;
+} spc_attention;
+
+/* Host only.  Workspace bytes of spc_attention_fwd and spc_attention_bwd. */
+spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size_t* fwd, size_t* bwd);
+
+/*
+ *   s_ij = scale q_i . k_j,  p = softmax of s_i over the keys that i sees,
+ *   out_i = sum_j p_ij v_j   (0 for a query that sees no key)
+ * q, out: n_q rows of heads x head_dim elements; k, v: n_kv rows of kv_heads x
+ * head_dim; each with its row stride in elements, a multiple of 16 bytes (one
+ * product may give q, k and v side by side).  Pairs that a mask hides enter no
+ * sum, whatever their rows hold.  Products are fp32; the probabilities are
+ * rounded to the dtype for the second product, their sum is not.
+ * stats fp32 [heads, n_q, 2] (NULL ok) receives (m, l) for the backward: the
+ * log of the row's sum of exp(s) is (m + log2 l) ln 2; l = 0: no key is seen.
+ * Rows of no sample are written neither in out nor in stats.
+ */
+spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a, const void* q, int64_t ldq, const void* k,
+                             int64_t ldk, const void* v, int64_t ldv, void* out, int64_t ldo, float* stats, void* ws,
+                             size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Backward of the forward of the same arguments, from its out and stats; the
+ * probabilities are computed again:
+ *   dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - dout_i . out_i),
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+ * with the sums of dk and dv over all heads that share a key head.  p and ds
+ * are rounded to the dtype for their products.  dq, dk, dv overlap no input.
+ * Rows of no sample are not written.
+ */
+spc_status spc_attention_bwd(spc_dtype dtype, const spc_attention* a, const void* dout, int64_t lddo, const void* q,
+                             int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, const void* out,
+                             int64_t ldo, const float* stats, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv,
+                             int64_t lddv, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * Measurement support (not part of the convolution): the dense MFMA rate of
  * this part, against which the convolutions' roofline fractions are read.
  * Launches `blocks` workgroups of 4 waves; each wave runs independent

@@ -8,6 +8,8 @@ from .binding import (  # noqa: F401
     EXPORTS,
     Dropout,
     SpcError,
+    attention_bwd,
+    attention_fwd,
     build_kmap,
     calibrate_mfma,
     conv_bwd_filter,
@@ -21,6 +23,8 @@ from .binding import (  # noqa: F401
     gather_by_voxel_id,
     group_norm_bwd,
     group_norm_fwd,
+    layer_norm_bwd,
+    layer_norm_fwd,
     lib,
     linear_recurrence_bwd,
     linear_recurrence_fwd,
@@ -29,6 +33,7 @@ from .binding import (  # noqa: F401
     out_shape,
     strided_out_bound,
     point_to_voxel,
+    rotary,
     sparse_conv_fwd,
     sparse_inverse_conv_fwd,
     sparse_maxpool_bwd,

@@ -33,7 +33,8 @@ EXPORTS = ("spc_out_shape", "spc_kmap_workspace", "spc_build_kmap", "spc_build_k
            "spc_point_to_voxel_workspace", "spc_point_to_voxel", "spc_gather_by_voxel_id", "spc_dropout_fwd",
            "spc_dropout_bwd", "spc_group_norm_workspace", "spc_group_norm_fwd", "spc_group_norm_bwd",
            "spc_linear_recurrence_workspace", "spc_linear_recurrence_fwd", "spc_linear_recurrence_bwd",
-           "spc_linear_recurrence_step", "spc_calibrate_mfma",
+           "spc_linear_recurrence_step", "spc_layer_norm_workspace", "spc_layer_norm_fwd", "spc_layer_norm_bwd",
+           "spc_rotary", "spc_attention_workspace", "spc_attention_fwd", "spc_attention_bwd", "spc_calibrate_mfma",
            "spc_last_error", "spc_version")
 
 
@@ -51,6 +52,13 @@ class Geom(ctypes.Structure):
 
 class _DropArg(ctypes.Structure):
     _fields_ = [("rng", ctypes.c_void_p), ("layer", ctypes.c_uint32), ("p", ctypes.c_float)]
+
+
+class _AttnArg(ctypes.Structure):
+    _fields_ = [("n_q", ctypes.c_int64), ("n_kv", ctypes.c_int64), ("n_seg", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q_ptr", ctypes.c_void_p), ("kv_ptr", ctypes.c_void_p),
+                ("q_order", ctypes.c_void_p), ("kv_order", ctypes.c_void_p)]
 
 
 TABLES = {"hash": 0, "grid": 1}   # SPC_TABLE_HASH, SPC_TABLE_GRID
@@ -84,7 +92,7 @@ def lib() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m sparse_convolution_hash_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
-    GP, DP = ctypes.POINTER(Geom), ctypes.POINTER(_DropArg)
+    GP, DP, AP = ctypes.POINTER(Geom), ctypes.POINTER(_DropArg), ctypes.POINTER(_AttnArg)
     sig = {
         "spc_out_shape": [GP, ctypes.POINTER(_I32)],
         "spc_kmap_workspace": [GP, _I64, ctypes.POINTER(_SZ)],
@@ -120,6 +128,14 @@ def lib() -> ctypes.CDLL:
         "spc_linear_recurrence_bwd": [_I32, _P, _P, _P, _I64, _I64, _I32, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _I64,
                                       _P, _P, _SZ, _P],
         "spc_linear_recurrence_step": [_I32, _P, _P, _I64, _I64, _I32, _P, _P, _P, _P],
+        "spc_layer_norm_workspace": [_I64, _I32, ctypes.POINTER(_SZ)],
+        "spc_layer_norm_fwd": [_I32, _P, _P, _I64, _I32, _P, _P, ctypes.c_float, _P, _P, _P, _P],
+        "spc_layer_norm_bwd": [_I32, _P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+        "spc_rotary": [_I32, _P, _I64, _I64, _I32, _I32, _P, _I64, _I32, _P, _P, _I32, _P, _I64, _P],
+        "spc_attention_workspace": [_I32, AP, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
+        "spc_attention_fwd": [_I32, AP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _SZ, _P],
+        "spc_attention_bwd": [_I32, AP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64,
+                              _P, _SZ, _P],
         "spc_calibrate_mfma": [_I32, _I32, _I32, _P, ctypes.POINTER(ctypes.c_double), _P],
     }
     for name, args in sig.items():
@@ -986,6 +1002,217 @@ def linear_recurrence_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Ten
                                           _ptr(out), _stream(dev))
     _check(st, "spc_linear_recurrence_step")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def layer_norm_workspace(n: int, C: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().spc_layer_norm_workspace(n, C, ctypes.byref(b)), "spc_layer_norm_workspace")
+    return b.value
+
+
+def layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   total: Optional[torch.Tensor] = None):
+    """Layer norm of x [N, C], or of x + residual, over the channels
+    (spc_layer_norm_fwd); gamma, beta fp32 [C].  Returns ``(y, stats fp32
+    [N, 2], total)``: total is x + residual as stored, None without a residual.
+    ``out`` may be x, ``total`` x or residual."""
+    _rows_checks(x)
+    dev, (n, C) = x.device, x.shape
+    for t, nm in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _need_like(t, nm, torch.float32, dev, (C,))
+    if residual is not None:
+        _need_like(residual, "residual", x.dtype, dev, x.shape)
+        if total is None:
+            total = torch.empty_like(x)
+        else:
+            _need_like(total, "total", x.dtype, dev, x.shape)
+    elif total is not None:
+        raise ValueError("total goes with a residual")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need_like(out, "out", x.dtype, dev, x.shape)
+    stats = x.new_empty((n, 2), dtype=torch.float32)
+    st = lib().spc_layer_norm_fwd(_DTYPES[x.dtype], _ptr(x), _ptr(residual), n, C, _ptr(gamma), _ptr(beta), eps, _ptr(out),
+                                  _ptr(total), _ptr(stats), _stream(dev))
+    _check(st, "spc_layer_norm_fwd")
+    return out, stats, total
+
+
+def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor], stats: torch.Tensor,
+                   dtotal: Optional[torch.Tensor] = None, want_affine: bool = True, dx: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gradients of layer_norm_fwd (spc_layer_norm_bwd): x is what was normed
+    (the forward's total with a residual), ``dtotal`` the gradient that reaches
+    it past the norm.  Returns ``(dx, dgamma, dbeta)``, the last two fp32 [C] or
+    None; dx is the gradient of x and residual alike and may be dout or dtotal."""
+    _rows_checks(x)
+    dev, (n, C) = x.device, x.shape
+    if gamma is not None:
+        _need_like(gamma, "gamma", torch.float32, dev, (C,))
+    _need_like(dout, "dout", x.dtype, dev, x.shape)
+    _need_like(stats, "stats", torch.float32, dev, (n, 2))
+    if dtotal is not None:
+        _need_like(dtotal, "dtotal", x.dtype, dev, x.shape)
+    if dx is None:
+        dx = torch.empty_like(x)
+    else:
+        _need_like(dx, "dx", x.dtype, dev, x.shape)
+    dgamma = dbeta = None
+    if want_affine:
+        dgamma, dbeta = x.new_empty((C,), dtype=torch.float32), x.new_empty((C,), dtype=torch.float32)
+    workspace = _scratch(workspace, layer_norm_workspace(n, C) if want_affine else 0, x)
+    st = lib().spc_layer_norm_bwd(_DTYPES[x.dtype], _ptr(dout), _ptr(x), n, C, _ptr(gamma), _ptr(stats), _ptr(dtotal), _ptr(dx),
+                                  _ptr(dgamma), _ptr(dbeta), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                  _stream(dev))
+    _check(st, "spc_layer_norm_bwd")
+    return dx, dgamma, dbeta
+
+
+def _heads(t, name, dtype=None, dev=None, shape=None):
+    """Checks a [N, H, D] view whose heads lie side by side within a row (a
+    column slice of a wider tensor is one) and returns its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N, heads, head_dim]")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    n, H, D = t.shape
+    ln, lh, ld = t.stride()
+    if (D > 1 and ld != 1) or (H > 1 and lh != D):
+        raise ValueError(f"the heads of {name} must lie side by side in a row")
+    return ln if n > 1 else H * D
+
+
+@functools.lru_cache(maxsize=256)
+def _axis_pairs(pairs: tuple):
+    return (ctypes.c_int32 * len(pairs))(*pairs)
+
+
+def rotary(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, pairs: Sequence[int], inverse: bool = False,
+           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotary positions of several axes (spc_rotary): x [N, heads, head_dim],
+    or a column slice of a wider tensor; pos int32 [N, axes], which may be
+    columns of the voxels' coordinates; freq fp32, one for each rotated pair;
+    pairs: the pairs of each axis.  ``inverse`` rotates back, which is the
+    gradient; ``out`` may be x."""
+    ldx = _heads(x, "input")
+    dev, (n, H, D) = x.device, x.shape
+    pairs = tuple(int(v) for v in pairs)
+    if not isinstance(pos, torch.Tensor) or not pos.is_cuda:
+        raise TypeError("pos must be a CUDA (HIP) tensor")
+    if pos.dtype != torch.int32:
+        raise TypeError(f"pos must be {torch.int32}, got {pos.dtype}")
+    if pos.device != dev:
+        raise ValueError(f"pos is on {pos.device}, expected {dev}")
+    if pos.dim() != 2 or pos.shape != (n, len(pairs)) or (pos.shape[1] > 1 and pos.stride(1) != 1):
+        raise ValueError(f"pos must be [N, {len(pairs)}] with its axes side by side")
+    _need(freq, "freq", torch.float32, dev)
+    if freq.shape != (sum(pairs),):
+        raise ValueError(f"freq must be [{sum(pairs)}], got {tuple(freq.shape)}")
+    if out is None:
+        out = x.new_empty((n, H, D))
+    elif out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+        raise ValueError("out may be x itself, not another view of it")
+    ldo = _heads(out, "out", x.dtype, dev, x.shape)
+    st = lib().spc_rotary(_DTYPES[x.dtype], _ptr(x), ldx, n, H, D, _ptr(pos), pos.stride(0) if n > 1 else len(pairs),
+                          len(pairs), _axis_pairs(pairs), _ptr(freq), 1 if inverse else 0, _ptr(out), ldo, _stream(dev))
+    _check(st, "spc_rotary")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def attention_workspace(dtype: torch.dtype, n_q: int, n_kv: int, n_seg: int, heads: int, kv_heads: int, head_dim: int) -> tuple:
+    """(workspace bytes of attention_fwd, of attention_bwd)."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    a = _AttnArg(n_q, n_kv, n_seg, heads, kv_heads, head_dim, 0, 1.0)
+    _check(lib().spc_attention_workspace(_DTYPES[dtype], ctypes.byref(a), ctypes.byref(f), ctypes.byref(b)),
+           "spc_attention_workspace")
+    return f.value, b.value
+
+
+def _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale):
+    """(descriptor, row strides of q, k, v, workspace bytes)."""
+    ldq = _heads(q, "q")
+    dev, (n, H, D) = q.device, q.shape
+    ldk = _heads(k, "k", q.dtype, dev)
+    m, Hk, _ = k.shape
+    ldv = _heads(v, "v", q.dtype, dev, k.shape)
+    if k.shape[2] != D:
+        raise ValueError(f"q has head_dim {D}, k {k.shape[2]}")
+    n_seg = _n_seg(seg_ptr, dev)
+    if kv_ptr is None and kv_order is None and seg_ptr is not None or order is not None and kv_ptr is None and kv_order is None:
+        if n != m:
+            raise ValueError(f"{n} queries and {m} keys: kv_ptr or kv_order must say how the keys are laid out")
+    if kv_ptr is None and kv_order is None:          # the rows attend to themselves
+        kv_ptr, kv_order = seg_ptr, order
+    else:
+        if kv_ptr is None and seg_ptr is not None:
+            raise ValueError("kv_order without kv_ptr: give both")
+        if kv_ptr is not None and _n_seg(kv_ptr, dev) != n_seg:
+            raise ValueError(f"seg_ptr has {n_seg} samples, kv_ptr {_n_seg(kv_ptr, dev)}")
+    if order is not None:
+        _need_like(order, "order", torch.int32, dev, (n,))
+    if kv_order is not None:
+        _need_like(kv_order, "kv_order", torch.int32, dev, (m,))
+    a = _AttnArg(n, m, n_seg, H, Hk, D, 1 if causal else 0, D ** -0.5 if scale is None else scale, _ptr(seg_ptr), _ptr(kv_ptr),
+                 _ptr(order), _ptr(kv_order))
+    return a, (ldq, ldk, ldv), attention_workspace(q.dtype, n, m, n_seg, H, Hk, D)
+
+
+def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg_ptr: Optional[torch.Tensor] = None,
+                  order: Optional[torch.Tensor] = None, kv_ptr: Optional[torch.Tensor] = None,
+                  kv_order: Optional[torch.Tensor] = None, causal: bool = False, scale: Optional[float] = None,
+                  want_stats: bool = False, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Attention of each sample's queries to its keys (spc_attention_fwd): q
+    [Nq, heads, D], k and v [Nkv, kv_heads, D], each of which may be a column
+    slice of one product.  seg_ptr and order lay out the queries and, where
+    neither kv_ptr nor kv_order is given, the keys; scale defaults to D^-1/2.
+    Returns ``(out [Nq, heads, D], stats fp32 [heads, Nq, 2] or None)``; stats
+    are for attention_bwd."""
+    a, (ldq, ldk, ldv), (need, _) = _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale)
+    dev, (n, H, D) = q.device, q.shape
+    if out is None:
+        out = q.new_empty((n, H, D))
+    ldo = _heads(out, "out", q.dtype, dev, q.shape)
+    stats = q.new_empty((H, n, 2), dtype=torch.float32) if want_stats else None
+    workspace = _scratch(workspace, need, q)
+    st = lib().spc_attention_fwd(_DTYPES[q.dtype], ctypes.byref(a), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(out), ldo,
+                                 _ptr(stats), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev))
+    _check(st, "spc_attention_fwd")
+    return out, stats
+
+
+def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                  stats: torch.Tensor, seg_ptr: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None,
+                  kv_ptr: Optional[torch.Tensor] = None, kv_order: Optional[torch.Tensor] = None, causal: bool = False,
+                  scale: Optional[float] = None, dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                  dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of attention_fwd (spc_attention_bwd) from its arguments, out
+    and stats: ``(dq, dk, dv)``, which may be given as column slices of one
+    tensor."""
+    a, (ldq, ldk, ldv), (_, need) = _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale)
+    dev, (n, H, D) = q.device, q.shape
+    lddo, ldo = _heads(dout, "dout", q.dtype, dev, q.shape), _heads(out, "out", q.dtype, dev, q.shape)
+    _need_like(stats, "stats", torch.float32, dev, (H, n, 2))
+    dq = q.new_empty(q.shape) if dq is None else dq
+    dk = k.new_empty(k.shape) if dk is None else dk
+    dv = v.new_empty(v.shape) if dv is None else dv
+    lddq, lddk, lddv = (_heads(t, nm, q.dtype, dev, like.shape) for t, nm, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
+    workspace = _scratch(workspace, need, q)
+    st = lib().spc_attention_bwd(_DTYPES[q.dtype], ctypes.byref(a), _ptr(dout), lddo, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
+                                 _ptr(out), ldo, _ptr(stats), _ptr(dq), lddq, _ptr(dk), lddk, _ptr(dv), lddv, _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), _stream(dev))
+    _check(st, "spc_attention_bwd")
+    return dq, dk, dv
 
 
 def calibrate_mfma(shape: int, blocks: int, iters: int, sink: torch.Tensor) -> float:

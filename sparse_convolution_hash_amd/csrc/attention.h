@@ -1,0 +1,972 @@
+// Attention over ragged samples: the kernels, compiled per dtype in
+// attention_{f32,f16,bf16}.hip; entry points and launch rules in attention.hip.
+//
+//   forward    s_ij = scale q_i . k_j,  p = softmax_j s,  o_i = sum_j p_ij v_j
+//   backward   p_ij = 2^(c q_i . k_j - m_i) / l_i from the forward's m and l,
+//              ds_ij = p_ij (do_i . v_j - do_i . o_i),
+//              dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
+//              dv_j = sum_i p_ij do_i
+//
+// Scores never leave the registers.  A wave owns 32 columns (queries, or keys
+// in k_attn_dkv) and walks the other side in tiles that its workgroup stages
+// in LDS.  v_mfma_f32_32x32 gives a tile of scores with its column in lane % 32
+// and 16 rows in registers, so a column's maximum and sum cost one exchange
+// between the wave's halves, its rescaling no exchange at all, and the tile is
+// at once the right operand of the second product: the contraction may run
+// over the rows in the order in which the registers hold them, as long as the
+// left operand comes in the same one, and the transposing LDS read
+// (ds_read_b64_tr_b16) gives it so from rows as they were stored.
+#pragma once
+
+#include "rows.h"
+
+namespace spc {
+namespace attn {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+
+struct Args {
+    const char *q, *k, *v, *o, *dout;       // o: the forward's output, read by the backward
+    char *out, *dq, *dk, *dv;
+    int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;   // bytes between rows
+    const int32_t *q_order, *kv_order;
+    Segs qs, ks;
+    int32_t g, hk, D, causal;               // query heads to a key head, key heads, head dimension
+    float c, scale;                         // c = scale log2(e)
+    float2* stats;                          // [heads, n_q] (m, l)
+    float* delta;                           // [heads, n_q] do . o
+    float* part;                            // partial results of the splits
+    int32_t splits, slots;
+    unsigned chunk, total;                  // workgroups of one XCD, of all
+};
+
+__device__ __forceinline__ f32x16_t zero16() {
+    f32x16_t z;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) z[r] = 0.f;
+    return z;
+}
+
+// One 32x32 tile step over 32 bytes of contraction: lane l supplies row
+// (column) l % 32 and the 16 bytes of half l / 32.
+template <typename TT>
+__device__ __forceinline__ f32x16_t mfma32(const u32x4& a, const u32x4& b, f32x16_t c);
+template <>
+__device__ __forceinline__ f32x16_t mfma32<BF16>(const u32x4& a, const u32x4& b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16_t mfma32<F16>(const u32x4& a, const u32x4& b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16_t mfma32<F32>(const u32x4& a, const u32x4& b, f32x16_t c) {
+    const float fa[4] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w)};
+    const float fb[4] = {__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i], fb[i], c, 0, 0, 0);
+    return c;
+}
+
+// The value of the wave's other half, next to this one's.
+__device__ __forceinline__ float2 halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return float2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ float sum_halves(float v) {
+    const float2 t = halves(v);
+    return t.x + t.y;
+}
+
+__device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// Row of a tile register: register r of a lane in half h holds row
+// 8 (r / 4) + 4 h + r % 4; bit_of(r) is the row of h = 0.
+constexpr int bit_of(int r) { return 8 * (r / 4) + r % 4; }
+
+// Tile of `rows` rows of DP elements in LDS, in 16-byte chunks.  The chunk
+// number is XORed with bits of the row so that both reads are free of bank
+// conflicts: 8 consecutive rows of one chunk (row reads), and two chunks of 4
+// consecutive rows (transposing reads).  M chunks a row: rows repeat their
+// banks every 1, 2 or 4 rows when M is a multiple of 8, 4 or 2.
+template <typename TT, int DP>
+struct Tile {
+    static constexpr int ES = sizeof(typename TT::storage);
+    static constexpr int PITCH = DP * ES, M = PITCH / 16;
+    static constexpr int NS = PITCH / 32;                 // steps of a product over DP
+    static constexpr int NB = (DP + 31) / 32;             // 32-row blocks of a result over DP
+    static __device__ __forceinline__ int swz(int row) {
+        if constexpr (M % 8 == 0) return ((row & 3) << 1) | ((row >> 2) & 1);
+        else if constexpr (M % 4 == 0) return (row & 2) | ((row >> 2) & 1);
+        else return (row >> 2) & 1;
+    }
+    static __device__ __forceinline__ int at(int row, int chunk) { return row * PITCH + ((chunk ^ swz(row)) << 4); }
+    static __device__ __forceinline__ u32x4 row16(const char* t, int row, int chunk) { return ld16(t + at(row, chunk)); }
+};
+
+// ------------------------------------------------- second kind of product
+
+// acc[db][rows d, cols] += sum over the tile's 32 rows j of X[j][d] w[j][col],
+// X a tile in LDS, w in the registers as a score tile is.
+template <typename TT, int DP>
+struct Second {
+    using T = Tile<TT, DP>;
+    static constexpr int STEPS = TT::E == 8 ? 2 : 16;     // contraction steps of a 32-row tile
+    static constexpr int PER = 16 / STEPS;                // registers (rows of each half) to a step
+
+    // Left operand of step t, block db: PER elements of this lane's d.
+    static __device__ __forceinline__ u32x4 left(const char* x, int row0, int t, int db, int lane) {
+        u32x4 f = zero4();
+        const bool narrow_block = DP % 32 != 0 && db == T::NB - 1;     // 16 of 32 rows exist; the others repeat them
+        if constexpr (TT::E == 8) {
+            const int i = lane & 15, h = lane >> 5, odd = narrow_block ? 0 : (lane >> 4) & 1;
+            const int row = row0 + 16 * t + 4 * h + (i >> 2);
+            const int chunk = 4 * db + 2 * odd + ((i >> 1) & 1);
+            const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(x + T::at(row, chunk) + 8 * (i & 1)));
+            const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(x + T::at(row + 8, chunk) + 8 * (i & 1)));
+            const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
+            f = u32x4{ua.x, ua.y, ub.x, ub.y};
+        } else {
+            const int h = lane >> 5, d = 32 * db + (narrow_block ? lane & 15 : lane & 31);
+            f.x = *reinterpret_cast<const uint32_t*>(x + T::at(row0 + bit_of(t) + 4 * h, d >> 2) + 4 * (d & 3));
+        }
+        return f;
+    }
+
+    static __device__ __forceinline__ u32x4 pack(const float* w) {
+        u32x4 f = zero4();
+        if constexpr (TT::E == 8) {
+            f32x8_t v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = w[e];
+            f = narrow<TT>(v).v[0];
+        } else {
+            f.x = __float_as_uint(w[0]);
+        }
+        return f;
+    }
+
+    static __device__ __forceinline__ f32x16_t step(const u32x4& a, const u32x4& b, f32x16_t c) {
+        if constexpr (TT::E == 8) return mfma32<TT>(a, b, c);
+        else return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    }
+
+    static __device__ __forceinline__ void add(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w, int lane) {
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t) {
+            float wt[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) wt[e] = w[t * PER + e];
+            const u32x4 b = pack(wt);
+#pragma unroll
+            for (int db = 0; db < T::NB; ++db) acc[db] = step(left(x, row0, t, db, lane), b, acc[db]);
+        }
+    }
+
+    // Elements of a left operand by class, as 1 and 0 of the type (clean: the
+    // finite ones themselves).
+    enum Class { CLEAN, POS, NEG, NOT_A_NUMBER, INFINITE };
+    static __device__ __forceinline__ uint32_t pick16(uint32_t u, Class k) {
+        constexpr uint32_t INF = TT::id == SPC_BF16 ? 0x7f80u : 0x7c00u, ONE = TT::id == SPC_BF16 ? 0x3f80u : 0x3c00u;
+        const uint32_t m = u & 0x7fffu;
+        switch (k) {
+            case CLEAN: return m < INF ? u : 0u;
+            case POS: return u == INF ? ONE : 0u;
+            case NEG: return u == (INF | 0x8000u) ? ONE : 0u;
+            case INFINITE: return m == INF ? ONE : 0u;
+            default: return m > INF ? ONE : 0u;
+        }
+    }
+    static __device__ __forceinline__ uint32_t pick32(uint32_t u, Class k) {
+        constexpr uint32_t INF = 0x7f800000u, ONE = 0x3f800000u;
+        const uint32_t m = u & 0x7fffffffu;
+        switch (k) {
+            case CLEAN: return m < INF ? u : 0u;
+            case POS: return u == INF ? ONE : 0u;
+            case NEG: return u == (INF | 0x80000000u) ? ONE : 0u;
+            case INFINITE: return m == INF ? ONE : 0u;
+            default: return m > INF ? ONE : 0u;
+        }
+    }
+    static __device__ __forceinline__ u32x4 pick(const u32x4& a, Class k) {
+        uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < (TT::E == 8 ? 4 : 1); ++i)
+            w[i] = TT::E == 8 ? pick16(w[i] & 0xffffu, k) | pick16(w[i] >> 16, k) << 16 : pick32(w[i], k);
+        return u32x4{w[0], w[1], w[2], w[3]};
+    }
+
+    // The same where w is 0 for pairs that a mask hides (bit bit_of(r) of vis is
+    // 0): hidden pairs are not in the sum, so an infinite or NaN X[j][d] must
+    // not reach the columns that do not see row j, as 0 * inf would.  Where
+    // X holds such values, the finite ones are summed and what the others
+    // make of each sum is counted apart.
+    static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w,
+                                                      uint32_t vis, int lane) {
+        bool odd = false;
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+            for (int db = 0; db < T::NB; ++db) {
+                const u32x4 a = left(x, row0, t, db, lane), f = pick(a, CLEAN);
+                odd |= a.x != f.x || a.y != f.y || a.z != f.z || a.w != f.w;
+            }
+        if (!__any(odd)) return add(acc, x, row0, w, lane);
+#pragma unroll
+        for (int db = 0; db < T::NB; ++db) {
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) {
+                float wt[PER];
+#pragma unroll
+                for (int e = 0; e < PER; ++e) wt[e] = w[t * PER + e];
+                acc[db] = step(pick(left(x, row0, t, db, lane), CLEAN), pack(wt), acc[db]);
+            }
+#pragma unroll 1
+            for (int kind = 0; kind < 3; ++kind) {        // infinite, minus infinite, neither
+                f32x16_t n = zero16();
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t) {
+                    const u32x4 a = left(x, row0, t, db, lane);
+                    float b1[PER], b2[PER];
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                        const float u = w[t * PER + e];
+                        const bool see = (vis >> bit_of(t * PER + e)) & 1u;
+                        const bool gt = see && u > 0.f, lt = see && u < 0.f;
+                        b1[e] = (kind == 0 ? gt : kind == 1 ? lt : see && !gt && !lt) ? 1.f : 0.f;
+                        b2[e] = (kind == 0 ? lt : kind == 1 ? gt : see) ? 1.f : 0.f;
+                    }
+                    n = step(kind < 2 ? pick(a, POS) : pick(a, INFINITE), pack(b1), n);
+                    n = step(kind < 2 ? pick(a, NEG) : pick(a, NOT_A_NUMBER), pack(b2), n);
+                }
+                const float v = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[db][r] += n[r] > 0.f ? v : 0.f;
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------ jobs
+
+// A workgroup's part: rows [r0, r0 + BM) of one sample, counted over the
+// positions and, for queries, the heads that share keys (row = position * mult
+// + head).  Sample s owns the slots from floor(at(s) mult / BM) + s on, at
+// least as many as it has tiles, so no table of tiles is needed; the slots left
+// over end at once.  Workgroups go round the 8 XCDs in launch order: each XCD
+// takes a contiguous part of (split, slot, head), so that workgroups which
+// read the same keys share an L2.
+struct Job {
+    int s, head, split, r0, a, len;    // sample, key head, split, first row, first position of the sample, its positions
+};
+
+template <int BM>
+__device__ __forceinline__ bool job_of(const Args& p, const Segs& segs, int mult, bool reverse, Job& j) {
+    const unsigned x = blockIdx.x & 7u, i = blockIdx.x >> 3;
+    unsigned l = x * p.chunk + i;
+    if (i >= p.chunk || l >= p.total) return false;
+    j.head = int(l % unsigned(p.hk));
+    l /= unsigned(p.hk);
+    int slot = int(l % unsigned(p.slots));
+    j.split = int(l / unsigned(p.slots));
+    if (reverse) slot = p.slots - 1 - slot;
+    const int lane = int(threadIdx.x) & (WAVE - 1);
+    auto first = [&](int s) { return int(unsigned(segs.at(s)) * unsigned(mult) / unsigned(BM)) + s; };
+    int lo = 0, hi = segs.n_seg;       // the count of samples that begin at or before the slot is in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + WAVE - 1) / WAVE;
+        const int t = lo + lane * step;
+        const int k = __popcll(__ballot(t < hi && first(t < hi ? t : lo) <= slot));
+        if (k == 0) break;
+        if (step == 1) {
+            lo += k;
+            break;
+        }
+        const int nlo = lo + (k - 1) * step + 1, nhi = lo + k * step;
+        lo = nlo;
+        hi = nhi < hi ? nhi : hi;
+    }
+    j.s = lo > 0 ? lo - 1 : 0;
+    j.s = __builtin_amdgcn_readfirstlane(j.s);
+    j.a = __builtin_amdgcn_readfirstlane(segs.at(j.s));
+    const int b = __builtin_amdgcn_readfirstlane(segs.at(j.s + 1));
+    j.len = b > j.a ? b - j.a : 0;
+    const int t = slot - (int(unsigned(j.a) * unsigned(mult) / unsigned(BM)) + j.s);
+    if (t < 0 || int64_t(t) * BM >= int64_t(j.len) * mult) return false;
+    j.r0 = t * BM;
+    return true;
+}
+
+// Position pos of a sample that begins at a: its row, or -1 where an order
+// names none.
+__device__ __forceinline__ int row_of(const int32_t* order, int a, int pos, int n) {
+    const int r = order ? order[a + pos] : a + pos;
+    return r >= 0 && r < n ? r : -1;
+}
+
+// A query of the walk: row index rq counts (position, head within its group).
+struct Query {
+    int pos, head, row;      // row -1: there is none
+};
+__device__ __forceinline__ Query query_of(const Args& p, const Job& j, int qa, int rq, int rows) {
+    Query q;
+    q.pos = p.g == 1 ? rq : rq / p.g;
+    q.head = j.head * p.g + (p.g == 1 ? 0 : rq - q.pos * p.g);
+    q.row = rq < rows ? row_of(p.q_order, qa, q.pos, p.qs.n) : -1;
+    return q;
+}
+
+// Fragments of one row of DP elements (zeros past D, or for no row), as the
+// column operand of the first product.
+template <typename TT, int DP>
+__device__ __forceinline__ void load_frags(u32x4* f, const char* row, bool there, int D, int h) {
+    using T = Tile<TT, DP>;
+#pragma unroll
+    for (int s = 0; s < T::NS; ++s) f[s] = there && (2 * s + h) * 16 < D * T::ES ? ld16(row + (2 * s + h) * 16) : zero4();
+}
+
+// Staging of tiles of BN rows from two tensors: what a thread moves.
+template <typename TT, int DP, int BN, int NT>
+struct Stage {
+    using T = Tile<TT, DP>;
+    static constexpr int CH = BN * T::M, PT = (CH + NT - 1) / NT;
+    static __device__ __forceinline__ bool mine(int i) { return CH % NT == 0 || int(threadIdx.x) + i * NT < CH; }
+    static __device__ __forceinline__ int row(int i) { return (int(threadIdx.x) + i * NT) / T::M; }
+    static __device__ __forceinline__ int chunk(int i) { return (int(threadIdx.x) + i * NT) % T::M; }
+    static __device__ __forceinline__ void put(char* tile, const u32x4 (&v)[PT]) {
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+            if (mine(i)) st16(tile + T::at(row(i), chunk(i)), v[i]);
+    }
+};
+
+// Bits of the first cnt of 64 rows.
+__device__ __forceinline__ uint64_t first_bits(int cnt) { return cnt >= 64 ? ~0ull : cnt <= 0 ? 0ull : (1ull << cnt) - 1; }
+
+// Keys of a tile [p0, p0 + BN) that are there, as bits.
+template <int BN>
+__device__ __forceinline__ uint64_t live_keys(const Args& p, int ka, int lk, int p0) {
+    if (!p.kv_order) return first_bits(lk - p0 < BN ? lk - p0 : BN);
+    const int t = p0 + (int(threadIdx.x) & (WAVE - 1));
+    return __ballot(t < p0 + BN && t < lk && row_of(p.kv_order, ka, t < lk ? t : lk - 1, p.ks.n) >= 0);
+}
+
+// ----------------------------------------------------------- forward
+
+// Keys below 32 rows to a tile step: 64 keys for the wide workgroups of 16-bit
+// types, 32 else (LDS and registers of the staging).
+template <typename TT, int NW>
+constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
+
+constexpr float LAZY = 8.f;   // a column's sums are rescaled once its maximum grew by 2^8
+
+template <typename TT, int DP, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attn_fwd(const Args p) {
+    constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
+    using T = Tile<TT, DP>;
+    using S = Stage<TT, DP, BN, NT>;
+    __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
+    Job j;
+    if (!job_of<BM>(p, p.qs, p.g, p.causal != 0, j)) return;
+    const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
+    const int ka = __builtin_amdgcn_readfirstlane(p.ks.at(j.s)), kb = __builtin_amdgcn_readfirstlane(p.ks.at(j.s + 1));
+    const int lk = kb > ka ? kb - ka : 0, rows = j.len * p.g, off = lk - j.len;
+    const int rw = j.r0 + 32 * wave;                       // the wave's first row
+    const Query q = query_of(p, j, j.a, rw + col, rows);
+    u32x4 qf[T::NS];
+    load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + int64_t(q.head) * p.D * T::ES, q.row >= 0, p.D, h);
+    // keys that the workgroup's last row, the wave's first and its last see
+    auto limit = [&](int r) { return !p.causal ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
+    const int nk = limit(j.r0 + BM - 1), seen_first = rw < rows ? limit(rw) : 0, seen_last = rw < rows ? limit(rw + 31) : 0;
+    const int mine = p.causal ? q.pos + 1 + off : lk;      // keys [0, mine) of this lane's query
+    const int tiles = (nk + BN - 1) / BN, per = (tiles + p.splits - 1) / p.splits;
+    const int t0 = j.split * per, t1 = min(tiles, t0 + per);
+
+    u32x4 rk[S::PT], rv[S::PT];
+    int at[S::PT];
+    auto find = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < S::PT; ++i) {
+            const int pos = t * BN + S::row(i);
+            at[i] = S::mine(i) && pos < lk ? row_of(p.kv_order, ka, pos, p.ks.n) : -1;
+        }
+    };
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::PT; ++i) {
+            const bool there = at[i] >= 0 && S::chunk(i) * 16 < p.D * T::ES;
+            const int64_t o = int64_t(j.head) * p.D * T::ES + S::chunk(i) * 16;
+            rk[i] = there ? ld16(p.k + int64_t(at[i]) * p.ldk + o) : zero4();
+            rv[i] = there ? ld16(p.v + int64_t(at[i]) * p.ldv + o) : zero4();
+        }
+    };
+
+    f32x16_t acc[T::NB];
+#pragma unroll
+    for (int db = 0; db < T::NB; ++db) acc[db] = zero16();
+    float m = -INFINITY, l = 0.f;      // m in units of log2: p = 2^(c s - m)
+    uint32_t seen = 0;
+
+    if (t0 < t1) {
+        find(t0);
+        fetch();
+        if (t0 + 1 < t1) find(t0 + 1);
+        S::put(lds[0][0], rk);
+        S::put(lds[0][1], rv);
+    }
+    lds_barrier();
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1, p0 = t * BN;
+        const bool more = t + 1 < t1;
+        if (more) {
+            fetch();
+            if (t + 2 < t1) find(t + 2);
+        }
+        if (p0 < seen_last) {          // else none of the wave's rows sees the tile
+            const uint64_t live = live_keys<BN>(p, ka, lk, p0);
+            const char *kt = lds[buf][0], *vt = lds[buf][1];
+            f32x16_t s[KT];
+            uint32_t vis[KT];
+            bool masked = false;
+#pragma unroll
+            for (int u = 0; u < KT; ++u) {
+                s[u] = zero16();
+#pragma unroll
+                for (int st = 0; st < T::NS; ++st) s[u] = mfma32<TT>(T::row16(kt, 32 * u + col, 2 * st + h), qf[st], s[u]);
+            }
+            const bool edge = live != first_bits(BN) || p0 + BN > seen_first;
+            if (edge) {
+#pragma unroll
+                for (int u = 0; u < KT; ++u) {
+                    const int n = mine - (p0 + 32 * u);
+                    vis[u] = (uint32_t(live >> (32 * u)) & uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
+                    seen |= vis[u] & 0x0f0f0f0fu;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[u][r] = (vis[u] >> bit_of(r)) & 1u ? s[u][r] : -INFINITY;
+                }
+                masked = p.causal != 0;
+            } else {
+                seen = 1;
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int u = 0; u < KT; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
+            const float2 both = halves(top);
+            top = fmaxf(both.x, both.y) * p.c;
+            const bool grew = top > m + LAZY;
+            if (__any(grew)) {         // the other columns keep their sums to the bit
+                const float a = grew ? exp2_(m - top) : 1.f;
+                l *= a;
+#pragma unroll
+                for (int db = 0; db < T::NB; ++db)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[db][r] *= a;
+                m = grew ? top : m;
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int u = 0; u < KT; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    s[u][r] = exp2_(fmaf(s[u][r], p.c, -base));
+                    l += s[u][r];
+                }
+#pragma unroll
+            for (int u = 0; u < KT; ++u) {
+                if (masked) Second<TT, DP>::add_masked(acc, vt, 32 * u, s[u], vis[u], lane);
+                else Second<TT, DP>::add(acc, vt, 32 * u, s[u], lane);
+            }
+        }
+        if (more) {
+            S::put(lds[buf ^ 1][0], rk);
+            S::put(lds[buf ^ 1][1], rv);
+        }
+        lds_barrier();
+    }
+    l = sum_halves(l);
+    seen |= uint32_t(__shfl_xor(int(seen), 32));
+    if (seen && l == 0.f) l = NAN;     // keys are seen, and every score is minus infinity
+    if (q.row < 0) return;
+    const int64_t id = int64_t(q.head) * p.qs.n + q.row;
+    if (p.splits > 1) {
+        float* part = p.part + (int64_t(j.split) * p.qs.n * (int64_t(p.g) * p.hk) + id) * (p.D + 4);
+#pragma unroll
+        for (int db = 0; db < T::NB; ++db)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int d = 32 * db + 8 * b + 4 * h;
+                if (d < p.D) *reinterpret_cast<f32x4_t*>(part + d) = f32x4_t{acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]};
+            }
+        if (h == 0) *reinterpret_cast<float2*>(part + p.D) = float2{m, l};
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    char* out = p.out + int64_t(q.row) * p.ldo + int64_t(q.head) * p.D * T::ES;
+#pragma unroll
+    for (int db = 0; db < T::NB; ++db)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int d = 32 * db + 8 * b + 4 * h;
+            if (d < p.D) store4<TT>(out + d * T::ES, f32x4_t{acc[db][4 * b] * inv, acc[db][4 * b + 1] * inv, acc[db][4 * b + 2] * inv, acc[db][4 * b + 3] * inv});
+        }
+    if (p.stats && h == 0) p.stats[id] = float2{m, l};
+}
+
+// Joins the splits of the forward: one thread takes four elements of a row.
+template <typename TT>
+__global__ __launch_bounds__(256) void k_attn_join(const Args p) {
+    constexpr int BM = 32, ES = sizeof(typename TT::storage);
+    Job j;
+    if (!job_of<BM>(p, p.qs, p.g, false, j)) return;
+    const int rows = min(j.len * p.g, j.r0 + BM), quads = p.D / 4;
+    const int64_t step = int64_t(p.qs.n) * (int64_t(p.g) * p.hk) * (p.D + 4);
+    for (int e = int(threadIdx.x); e < (rows - j.r0) * quads; e += 256) {
+        const int rq = j.r0 + e / quads, d = (e % quads) * 4;
+        const Query q = query_of(p, j, j.a, rq, rows);
+        if (q.row < 0) continue;
+        const int64_t id = int64_t(q.head) * p.qs.n + q.row;
+        const float* part = p.part + id * (p.D + 4);
+        float m = -INFINITY;
+        for (int s = 0; s < p.splits; ++s) m = fmaxf(m, part[s * step + p.D]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < p.splits; ++s) {
+            const float2 ml = *reinterpret_cast<const float2*>(part + s * step + p.D);
+            const float w = exp2_(ml.x - base);
+            l += ml.y * w;
+            if (ml.x != -INFINITY) o += *reinterpret_cast<const f32x4_t*>(part + s * step + d) * w;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        store4<TT>(p.out + int64_t(q.row) * p.ldo + (int64_t(q.head) * p.D + d) * ES, o * inv);
+        if (p.stats && d == 0) p.stats[id] = float2{m, l};
+    }
+}
+
+// ---------------------------------------------------------- backward
+
+// What a row's probabilities are computed from: p = 2^(c s - m) * f.
+// 16-bit types fold the sum into m (m + log2 l is off by up to 2^-24 of its
+// size, far below the rounding of p that follows); fp32 multiplies by 1 / l,
+// so that a large m costs no precision.
+template <typename TT>
+__device__ __forceinline__ float2 from_stats(float2 ml) {
+    if (ml.y == 0.f) return float2{INFINITY, 0.f};         // a row that sees no key: 2^-inf
+    if constexpr (TT::E == 8) return float2{ml.x + __log2f(ml.y), 1.f};
+    else return float2{ml.x, 1.f / ml.y};
+}
+
+// dq and delta: as the forward, a wave of 32 queries walks the keys.
+template <typename TT, int DP, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
+    constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
+    using T = Tile<TT, DP>;
+    using S = Stage<TT, DP, BN, NT>;
+    __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
+    Job j;
+    if (!job_of<BM>(p, p.qs, p.g, p.causal != 0, j)) return;
+    const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
+    const int ka = __builtin_amdgcn_readfirstlane(p.ks.at(j.s)), kb = __builtin_amdgcn_readfirstlane(p.ks.at(j.s + 1));
+    const int lk = kb > ka ? kb - ka : 0, rows = j.len * p.g, off = lk - j.len;
+    const int rw = j.r0 + 32 * wave;
+    const Query q = query_of(p, j, j.a, rw + col, rows);
+    const int64_t id = int64_t(q.head) * p.qs.n + q.row, in = int64_t(q.head) * p.D * T::ES;
+    u32x4 qf[T::NS], gf[T::NS];
+    load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + in, q.row >= 0, p.D, h);
+    load_frags<TT, DP>(gf, p.dout + int64_t(q.row) * p.lddo + in, q.row >= 0, p.D, h);
+    float delta = 0.f;
+    {
+        u32x4 of[T::NS];
+        load_frags<TT, DP>(of, p.o + int64_t(q.row) * p.ldo + in, q.row >= 0, p.D, h);
+#pragma unroll
+        for (int s = 0; s < T::NS; ++s) {
+            if constexpr (TT::E == 8) {
+                Raw8<TT> x, y;
+                x.v[0] = of[s], y.v[0] = gf[s];
+                const f32x8_t a = widen<TT>(x), b = widen<TT>(y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
+            } else {
+                delta = fmaf(__uint_as_float(of[s].x), __uint_as_float(gf[s].x), delta);
+                delta = fmaf(__uint_as_float(of[s].y), __uint_as_float(gf[s].y), delta);
+                delta = fmaf(__uint_as_float(of[s].z), __uint_as_float(gf[s].z), delta);
+                delta = fmaf(__uint_as_float(of[s].w), __uint_as_float(gf[s].w), delta);
+            }
+        }
+        delta = sum_halves(delta);
+    }
+    if (q.row >= 0 && h == 0 && j.split == 0) p.delta[id] = delta;
+    const float2 mf = from_stats<TT>(q.row >= 0 ? p.stats[id] : float2{0.f, 0.f});
+    auto limit = [&](int r) { return !p.causal ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
+    const int nk = limit(j.r0 + BM - 1), seen_first = rw < rows ? limit(rw) : 0, seen_last = rw < rows ? limit(rw + 31) : 0;
+    const int mine = p.causal ? q.pos + 1 + off : lk;
+    const int tiles = (nk + BN - 1) / BN, per = (tiles + p.splits - 1) / p.splits;
+    const int t0 = j.split * per, t1 = min(tiles, t0 + per);
+
+    u32x4 rk[S::PT], rv[S::PT];
+    int at[S::PT];
+    auto find = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < S::PT; ++i) {
+            const int pos = t * BN + S::row(i);
+            at[i] = S::mine(i) && pos < lk ? row_of(p.kv_order, ka, pos, p.ks.n) : -1;
+        }
+    };
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::PT; ++i) {
+            const bool there = at[i] >= 0 && S::chunk(i) * 16 < p.D * T::ES;
+            const int64_t o = int64_t(j.head) * p.D * T::ES + S::chunk(i) * 16;
+            rk[i] = there ? ld16(p.k + int64_t(at[i]) * p.ldk + o) : zero4();
+            rv[i] = there ? ld16(p.v + int64_t(at[i]) * p.ldv + o) : zero4();
+        }
+    };
+
+    f32x16_t acc[T::NB];
+#pragma unroll
+    for (int db = 0; db < T::NB; ++db) acc[db] = zero16();
+    if (t0 < t1) {
+        find(t0);
+        fetch();
+        if (t0 + 1 < t1) find(t0 + 1);
+        S::put(lds[0][0], rk);
+        S::put(lds[0][1], rv);
+    }
+    lds_barrier();
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1, p0 = t * BN;
+        const bool more = t + 1 < t1;
+        if (more) {
+            fetch();
+            if (t + 2 < t1) find(t + 2);
+        }
+        if (p0 < seen_last) {
+            const uint64_t live = live_keys<BN>(p, ka, lk, p0);
+            const char *kt = lds[buf][0], *vt = lds[buf][1];
+            const bool edge = live != first_bits(BN) || p0 + BN > seen_first;
+#pragma unroll
+            for (int u = 0; u < KT; ++u) {
+                f32x16_t s = zero16(), d = zero16();
+#pragma unroll
+                for (int st = 0; st < T::NS; ++st) s = mfma32<TT>(T::row16(kt, 32 * u + col, 2 * st + h), qf[st], s);
+#pragma unroll
+                for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(vt, 32 * u + col, 2 * st + h), gf[st], d);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float w = exp2_(fmaf(s[r], p.c, -mf.x));
+                    if constexpr (TT::E == 4) w *= mf.y;
+                    s[r] = w * (d[r] - delta);
+                }
+                if (edge) {
+                    const int n = mine - (p0 + 32 * u);
+                    const uint32_t vis = (uint32_t(live >> (32 * u)) & uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = (vis >> bit_of(r)) & 1u ? s[r] : 0.f;
+                    if (p.causal) Second<TT, DP>::add_masked(acc, kt, 32 * u, s, vis, lane);
+                    else Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
+                } else {
+                    Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
+                }
+            }
+        }
+        if (more) {
+            S::put(lds[buf ^ 1][0], rk);
+            S::put(lds[buf ^ 1][1], rv);
+        }
+        lds_barrier();
+    }
+    if (q.row < 0) return;
+    if (p.splits > 1) {
+        float* part = p.part + (int64_t(j.split) * p.qs.n * (int64_t(p.g) * p.hk) + id) * p.D;
+#pragma unroll
+        for (int db = 0; db < T::NB; ++db)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int d = 32 * db + 8 * b + 4 * h;
+                if (d < p.D) *reinterpret_cast<f32x4_t*>(part + d) = f32x4_t{acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]};
+            }
+        return;
+    }
+    char* out = p.dq + int64_t(q.row) * p.lddq + in;
+#pragma unroll
+    for (int db = 0; db < T::NB; ++db)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int d = 32 * db + 8 * b + 4 * h;
+            if (d < p.D)
+                store4<TT>(out + d * T::ES, f32x4_t{acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]} * p.scale);
+        }
+}
+
+// dk and dv: a wave of 32 keys walks the queries of all heads that share them,
+// which sums their gradients without an atomic.
+template <typename TT, int DP, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
+    constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
+    using T = Tile<TT, DP>;
+    using S = Stage<TT, DP, BN, NT>;
+    __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
+    __shared__ __attribute__((aligned(16))) float row_m[2][BN], row_f[2][BN], row_d[2][BN];
+    Job j;
+    if (!job_of<BM>(p, p.ks, 1, false, j)) return;
+    const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
+    const int qa = __builtin_amdgcn_readfirstlane(p.qs.at(j.s)), qb = __builtin_amdgcn_readfirstlane(p.qs.at(j.s + 1));
+    const int lq = qb > qa ? qb - qa : 0, rows = lq * p.g, off = j.len - lq;
+    const int kw = j.r0 + 32 * wave, key = kw + col;       // the wave's first key, this lane's
+    const int krow = key < j.len ? row_of(p.kv_order, j.a, key, p.ks.n) : -1;
+    const int64_t in = int64_t(j.head) * p.D * T::ES;
+    u32x4 kf[T::NS], vf[T::NS];
+    load_frags<TT, DP>(kf, p.k + int64_t(krow) * p.ldk + in, krow >= 0, p.D, h);
+    load_frags<TT, DP>(vf, p.v + int64_t(krow) * p.ldv + in, krow >= 0, p.D, h);
+    // the first row that sees a key: of the workgroup's first, the wave's first and last, this lane's
+    auto begin = [&](int k) { return !p.causal ? 0 : min(rows, max(0, k - off) * p.g); };
+    const int first = begin(j.r0), first_lo = begin(kw), first_hi = begin(kw + 31), mine = begin(key);
+    const int tb = first / BN, tiles = (rows + BN - 1) / BN - tb, per = (tiles + p.splits - 1) / p.splits;
+    const int t0 = tb + j.split * per, t1 = min(tb + tiles, t0 + per);
+
+    u32x4 rq[S::PT], rg[S::PT];
+    int at[S::PT], hd[S::PT], own = -1, own_head = 0;
+    float2 own_ml = {0.f, 0.f};
+    float own_d = 0.f;
+    auto find = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < S::PT; ++i) {
+            const Query q = query_of(p, j, qa, t * BN + S::row(i), S::mine(i) ? rows : 0);
+            at[i] = q.row, hd[i] = q.head;
+        }
+        const Query q = query_of(p, j, qa, t * BN + int(threadIdx.x), int(threadIdx.x) < BN ? rows : 0);
+        own = q.row, own_head = q.head;
+    };
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::PT; ++i) {
+            const bool there = at[i] >= 0 && S::chunk(i) * 16 < p.D * T::ES;
+            const int64_t o = int64_t(hd[i]) * p.D * T::ES + S::chunk(i) * 16;
+            rq[i] = there ? ld16(p.q + int64_t(at[i]) * p.ldq + o) : zero4();
+            rg[i] = there ? ld16(p.dout + int64_t(at[i]) * p.lddo + o) : zero4();
+        }
+        const int64_t id = int64_t(own_head) * p.qs.n + own;
+        own_ml = own >= 0 ? p.stats[id] : float2{0.f, 0.f};
+        own_d = own >= 0 ? p.delta[id] : 0.f;
+    };
+    auto put = [&](int buf) {
+        S::put(lds[buf][0], rq);
+        S::put(lds[buf][1], rg);
+        if (int(threadIdx.x) < BN) {
+            const float2 mf = from_stats<TT>(own_ml);
+            row_m[buf][threadIdx.x] = mf.x;
+            if constexpr (TT::E == 4) row_f[buf][threadIdx.x] = mf.y;
+            row_d[buf][threadIdx.x] = own_d;
+        }
+    };
+
+    f32x16_t dk[T::NB], dv[T::NB];
+#pragma unroll
+    for (int db = 0; db < T::NB; ++db) dk[db] = zero16(), dv[db] = zero16();
+    if (t0 < t1) {
+        find(t0);
+        fetch();
+        put(0);
+        if (t0 + 1 < t1) find(t0 + 1);
+    }
+    lds_barrier();
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1, p0 = t * BN;
+        const bool more = t + 1 < t1;
+        uint64_t live;
+        if (!p.q_order) {
+            live = first_bits(rows - p0 < BN ? rows - p0 : BN);
+        } else {
+            const int r = p0 + lane;
+            live = __ballot(lane < BN && query_of(p, j, qa, r, rows).row >= 0);
+        }
+        if (more) {
+            fetch();
+            if (t + 2 < t1) find(t + 2);
+        }
+        if (p0 + BN > first_lo && kw < j.len) {
+            const char *qt = lds[buf][0], *gt = lds[buf][1];
+            const bool edge = live != first_bits(BN) || p0 < first_hi;
+#pragma unroll
+            for (int u = 0; u < KT; ++u) {
+                f32x16_t s = zero16(), d = zero16();
+#pragma unroll
+                for (int st = 0; st < T::NS; ++st) s = mfma32<TT>(T::row16(qt, 32 * u + col, 2 * st + h), kf[st], s);
+#pragma unroll
+                for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(gt, 32 * u + col, 2 * st + h), vf[st], d);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int r0 = 32 * u + 8 * b + 4 * h;
+                    const f32x4_t m4 = *reinterpret_cast<const f32x4_t*>(&row_m[buf][r0]);
+                    const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(&row_d[buf][r0]);
+                    f32x4_t f4 = {1.f, 1.f, 1.f, 1.f};
+                    if constexpr (TT::E == 4) f4 = *reinterpret_cast<const f32x4_t*>(&row_f[buf][r0]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 4 * b + e;
+                        float w = exp2_(fmaf(s[r], p.c, -m4[e]));
+                        if constexpr (TT::E == 4) w *= f4[e];
+                        s[r] = w;
+                        d[r] = w * (d[r] - d4[e]);
+                    }
+                }
+                if (edge) {
+                    const int n = mine - (p0 + 32 * u);    // rows before this lane's first are hidden
+                    const uint32_t vis = (uint32_t(live >> (32 * u)) & ~uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const bool see = (vis >> bit_of(r)) & 1u;
+                        s[r] = see ? s[r] : 0.f, d[r] = see ? d[r] : 0.f;
+                    }
+                    if (p.causal) {
+                        Second<TT, DP>::add_masked(dv, gt, 32 * u, s, vis, lane);
+                        Second<TT, DP>::add_masked(dk, qt, 32 * u, d, vis, lane);
+                        continue;
+                    }
+                }
+                Second<TT, DP>::add(dv, gt, 32 * u, s, lane);
+                Second<TT, DP>::add(dk, qt, 32 * u, d, lane);
+            }
+        }
+        if (more) put(buf ^ 1);
+        lds_barrier();
+    }
+    if (krow < 0) return;
+    if (p.splits > 1) {
+        float* part = p.part + (int64_t(j.split) * p.ks.n * p.hk + int64_t(j.head) * p.ks.n + krow) * (2 * p.D);
+#pragma unroll
+        for (int db = 0; db < T::NB; ++db)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int d = 32 * db + 8 * b + 4 * h;
+                if (d >= p.D) continue;
+                *reinterpret_cast<f32x4_t*>(part + d) = f32x4_t{dk[db][4 * b], dk[db][4 * b + 1], dk[db][4 * b + 2], dk[db][4 * b + 3]};
+                *reinterpret_cast<f32x4_t*>(part + p.D + d) = f32x4_t{dv[db][4 * b], dv[db][4 * b + 1], dv[db][4 * b + 2], dv[db][4 * b + 3]};
+            }
+        return;
+    }
+    char *ok = p.dk + int64_t(krow) * p.lddk + in, *ov = p.dv + int64_t(krow) * p.lddv + in;
+#pragma unroll
+    for (int db = 0; db < T::NB; ++db)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int d = 32 * db + 8 * b + 4 * h;
+            if (d >= p.D) continue;
+            store4<TT>(ok + d * T::ES, f32x4_t{dk[db][4 * b], dk[db][4 * b + 1], dk[db][4 * b + 2], dk[db][4 * b + 3]} * p.scale);
+            store4<TT>(ov + d * T::ES, f32x4_t{dv[db][4 * b], dv[db][4 * b + 1], dv[db][4 * b + 2], dv[db][4 * b + 3]});
+        }
+}
+
+// Sums the splits of a gradient, in their order: of dq (KEYS false), or of dk
+// and dv.
+template <typename TT, bool KEYS>
+__global__ __launch_bounds__(256) void k_attn_sum(const Args p) {
+    constexpr int BM = 32, ES = sizeof(typename TT::storage);
+    Job j;
+    const int mult = KEYS ? 1 : p.g;
+    if (!job_of<BM>(p, KEYS ? p.ks : p.qs, mult, false, j)) return;
+    const int rows = min(j.len * mult, j.r0 + BM), width = KEYS ? 2 * p.D : p.D, quads = width / 4;
+    for (int e = int(threadIdx.x); e < (rows - j.r0) * quads; e += 256) {
+        const int r = j.r0 + e / quads, d = (e % quads) * 4;
+        int row, head;
+        if constexpr (KEYS) {
+            row = row_of(p.kv_order, j.a, r, p.ks.n), head = j.head;
+        } else {
+            const Query q = query_of(p, j, j.a, r, rows);
+            row = q.row, head = q.head;
+        }
+        if (row < 0) continue;
+        const int64_t n = KEYS ? p.ks.n : p.qs.n, heads = KEYS ? int64_t(p.hk) : int64_t(p.g) * p.hk;
+        const float* part = p.part + (int64_t(head) * n + row) * width + d;
+        f32x4_t t = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < p.splits; ++s) t += *reinterpret_cast<const f32x4_t*>(part + s * (n * heads * width));
+        if constexpr (KEYS) {
+            if (d < p.D) store4<TT>(p.dk + int64_t(row) * p.lddk + (int64_t(head) * p.D + d) * ES, t * p.scale);
+            else store4<TT>(p.dv + int64_t(row) * p.lddv + (int64_t(head) * p.D + d - p.D) * ES, t);
+        } else {
+            store4<TT>(p.dq + int64_t(row) * p.lddq + (int64_t(head) * p.D + d) * ES, t * p.scale);
+        }
+    }
+}
+
+// ------------------------------------------------------------- launches
+
+// How a walk is cut: waves to a workgroup, splits of the other side.
+struct Cut {
+    int32_t nw, splits;
+    int64_t slots, blocks;     // of BM = 32 nw rows; workgroups of all splits and heads
+};
+
+spc_status launch_fwd_f32(const Args& p, const Cut& c, hipStream_t stream);
+spc_status launch_fwd_f16(const Args& p, const Cut& c, hipStream_t stream);
+spc_status launch_fwd_bf16(const Args& p, const Cut& c, hipStream_t stream);
+spc_status launch_bwd_f32(const Args& p, const Cut& q, const Cut& k, hipStream_t stream);
+spc_status launch_bwd_f16(const Args& p, const Cut& q, const Cut& k, hipStream_t stream);
+spc_status launch_bwd_bf16(const Args& p, const Cut& q, const Cut& k, hipStream_t stream);
+
+inline int64_t slots_of(int64_t rows, int64_t n_seg, int bm) { return rows / bm + n_seg + 1; }
+
+inline unsigned set_grid(Args& p, int64_t slots, int splits) {
+    p.slots = int32_t(slots), p.splits = splits;
+    p.total = unsigned(slots * splits * p.hk);
+    p.chunk = unsigned(ceil_div(int64_t(p.total), 8));
+    return p.chunk * 8;
+}
+
+#define ATTN_WIDTHS(name, nw, grid, p)                                                                                        \
+    do {                                                                                                                      \
+        if (p.D <= 16) hipLaunchKernelGGL((name<TT, 16, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                       \
+        else if (p.D <= 32) hipLaunchKernelGGL((name<TT, 32, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                  \
+        else if (p.D <= 64) hipLaunchKernelGGL((name<TT, 64, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                  \
+        else hipLaunchKernelGGL((name<TT, 128, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                                \
+        SPC_LAUNCHED(#name);                                                                                                  \
+    } while (0)
+
+template <typename TT>
+spc_status launch_fwd(Args p, const Cut& c, hipStream_t stream) {
+    const unsigned grid = set_grid(p, c.slots, c.splits);
+    if (c.nw == 4) ATTN_WIDTHS(k_attn_fwd, 4, grid, p);
+    else ATTN_WIDTHS(k_attn_fwd, 1, grid, p);
+    if (c.splits > 1) {
+        const int splits = p.splits;
+        const unsigned rows = set_grid(p, slots_of(int64_t(p.qs.n) * p.g, p.qs.n_seg, 32), 1);
+        p.splits = splits;
+        hipLaunchKernelGGL(k_attn_join<TT>, dim3(rows), dim3(256), 0, stream, p);
+        SPC_LAUNCHED("k_attn_join");
+    }
+    return SPC_OK;
+}
+
+template <typename TT>
+spc_status launch_bwd(Args p, const Cut& cq, const Cut& ck, hipStream_t stream) {
+    if (p.qs.n) {
+        unsigned grid = set_grid(p, cq.slots, cq.splits);
+        if (cq.nw == 4) ATTN_WIDTHS(k_attn_dq, 4, grid, p);
+        else ATTN_WIDTHS(k_attn_dq, 1, grid, p);
+        if (cq.splits > 1) {
+            grid = set_grid(p, slots_of(int64_t(p.qs.n) * p.g, p.qs.n_seg, 32), 1);
+            p.splits = cq.splits;
+            hipLaunchKernelGGL((k_attn_sum<TT, false>), dim3(grid), dim3(256), 0, stream, p);
+            SPC_LAUNCHED("k_attn_sum");
+        }
+    }
+    if (p.ks.n) {
+        unsigned grid = set_grid(p, ck.slots, ck.splits);
+        if (ck.nw == 4) ATTN_WIDTHS(k_attn_dkv, 4, grid, p);
+        else ATTN_WIDTHS(k_attn_dkv, 1, grid, p);
+        if (ck.splits > 1) {
+            grid = set_grid(p, slots_of(p.ks.n, p.ks.n_seg, 32), 1);
+            p.splits = ck.splits;
+            hipLaunchKernelGGL((k_attn_sum<TT, true>), dim3(grid), dim3(256), 0, stream, p);
+            SPC_LAUNCHED("k_attn_sum");
+        }
+    }
+    return SPC_OK;
+}
+
+}  // namespace attn
+}  // namespace spc

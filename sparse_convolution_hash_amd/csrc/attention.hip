@@ -1,0 +1,167 @@
+// Entry points of the attention calls: host checks, the cut of a call into
+// workgroups, workspaces.  The kernels are in attention.h.
+#include "attention.h"
+
+namespace spc {
+namespace attn {
+namespace {
+
+constexpr int D_MAX = 128;
+
+// Rows of one side that work is cut over (positions times the heads that share
+// them), the other side's positions, and what a split must at least be worth.
+Cut cut_of(int64_t rows, int64_t other, int64_t n_seg, int heads) {
+    Cut c;
+    // Four waves share the staged tiles where samples have rows for them and
+    // the call fills the chip; else single waves, which leave fewer lanes idle.
+    c.nw = rows >= 64 * n_seg && slots_of(rows, n_seg, 128) * heads >= 512 ? 4 : 1;
+    c.slots = slots_of(rows, n_seg, 32 * c.nw);
+    // Few workgroups: the other side is split too, in parts of at least 256
+    // rows on average, and the parts are joined by a second launch.
+    const int64_t want = 2048 / c.nw, have = (rows / (32 * c.nw) + n_seg) * heads, most = other / n_seg / 256;
+    c.splits = int32_t(have * 2 > want || most < 2 ? 1 : (want / have < most ? want / have : most));
+    c.blocks = c.slots * c.splits * heads;
+    return c;
+}
+
+struct Plan {
+    Cut q, k;
+    size_t fwd, bwd;    // workspace bytes
+};
+
+spc_status check_sizes(spc_dtype dtype, const spc_attention* a, Plan& w) {
+    if (dtype != SPC_F32 && dtype != SPC_F16 && dtype != SPC_BF16) return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+    if (!a) return fail(SPC_ERR_ARG, "the attention descriptor is NULL");
+    if (a->n_q < 0 || a->n_q >= ROWS_END) return fail(SPC_ERR_ARG, "n_q=%lld is out of range", (long long)a->n_q);
+    if (a->n_kv < 0 || a->n_kv >= ROWS_END) return fail(SPC_ERR_ARG, "n_kv=%lld is out of range", (long long)a->n_kv);
+    if (a->n_seg < 1 || a->n_seg >= ROWS_END) return fail(SPC_ERR_ARG, "n_seg=%lld is out of range", (long long)a->n_seg);
+    if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads)
+        return fail(SPC_ERR_ARG, "heads=%d is not a positive multiple of kv_heads=%d", a->heads, a->kv_heads);
+    if (a->head_dim < 1 || a->head_dim % 16 || a->head_dim > D_MAX)
+        return fail(SPC_ERR_UNSUPPORTED, "head_dim=%d: a multiple of 16 up to %d", a->head_dim, D_MAX);
+    if (int64_t(a->heads) * a->head_dim > C_MAX) return fail(SPC_ERR_UNSUPPORTED, "%d heads of %d are too many", a->heads, a->head_dim);
+    if (a->n_q * a->heads >= ROWS_END || a->n_kv * a->kv_heads >= ROWS_END)
+        return fail(SPC_ERR_UNSUPPORTED, "rows x heads exceed 31 bits");
+    if (!(a->scale > 0.f && a->scale <= 3.402823466e38f)) return fail(SPC_ERR_ARG, "scale=%g must be positive and finite", double(a->scale));
+    const int64_t rows = a->n_q * (a->heads / a->kv_heads);
+    w.q = cut_of(rows, a->n_kv, a->n_seg, a->kv_heads);
+    w.k = cut_of(a->n_kv, rows, a->n_seg, a->kv_heads);
+    // (a call that is split has few workgroups, so its join has too)
+    if (!launchable(w.q.blocks + 8, 64 * w.q.nw) || !launchable(w.k.blocks + 8, 64 * w.k.nw))
+        return fail(SPC_ERR_UNSUPPORTED, "%lld samples of %lld and %lld rows exceed one launch", (long long)a->n_seg, (long long)a->n_q,
+                    (long long)a->n_kv);
+    const size_t hq = size_t(a->n_q) * size_t(a->heads), hk = size_t(a->n_kv) * size_t(a->kv_heads), D = size_t(a->head_dim);
+    w.fwd = w.q.splits > 1 ? size_t(w.q.splits) * hq * (D + 4) * 4 : 0;
+    const size_t pq = w.q.splits > 1 ? size_t(w.q.splits) * hq * D * 4 : 0, pk = w.k.splits > 1 ? size_t(w.k.splits) * hk * 2 * D * 4 : 0;
+    w.bwd = align_up(hq * 4, 256) + (pq > pk ? pq : pk);
+    return SPC_OK;
+}
+
+struct Side {
+    const void* p;
+    int64_t ld;
+    int32_t heads;
+    const char* name;
+};
+
+spc_status check_call(spc_dtype dtype, const spc_attention* a, const void* ws, size_t need, size_t ws_bytes, Args& p) {
+    if ((!a->q_ptr || !a->kv_ptr) && a->n_seg != 1) return fail(SPC_ERR_ARG, "q_ptr or kv_ptr is NULL with n_seg=%lld", (long long)a->n_seg);
+    for (const void* q : {(const void*)a->q_ptr, (const void*)a->kv_ptr, (const void*)a->q_order, (const void*)a->kv_order, ws})
+        if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    if (!ws && need) return fail(SPC_ERR_ARG, "ws is NULL");
+    if (ws_bytes < need) return fail(SPC_ERR_WORKSPACE, "ws_bytes=%zu, need %zu", ws_bytes, need);
+    p = Args{};
+    p.qs = Segs{a->q_ptr, int32_t(a->n_seg), int32_t(a->n_q)};
+    p.ks = Segs{a->kv_ptr, int32_t(a->n_seg), int32_t(a->n_kv)};
+    p.q_order = a->q_order, p.kv_order = a->kv_order;
+    p.hk = a->kv_heads, p.g = a->heads / a->kv_heads, p.D = a->head_dim, p.causal = a->causal != 0;
+    p.scale = a->scale, p.c = float(double(a->scale) * 1.4426950408889634);
+    return SPC_OK;
+}
+
+spc_status check_rows(spc_dtype dtype, const spc_attention* a, const Side& s, int64_t n) {
+    if (s.ld < int64_t(s.heads) * a->head_dim || s.ld * dtype_size(dtype) % 16 || s.ld >= (int64_t(1) << 31))
+        return fail(SPC_ERR_ARG, "row stride %lld of %s: at least heads x head_dim, a multiple of 16 bytes, below 2^31", (long long)s.ld, s.name);
+    if (n > 0 && !s.p) return fail(SPC_ERR_ARG, "%s is NULL", s.name);
+    if (s.p && !aligned16(s.p)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    return SPC_OK;
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace spc
+
+using namespace spc;
+using namespace spc::attn;
+
+extern "C" spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size_t* fwd, size_t* bwd) {
+    clear_error();
+    if (!fwd || !bwd) return fail(SPC_ERR_ARG, "fwd or bwd is NULL");
+    Plan w;
+    const spc_status st = check_sizes(dtype, a, w);
+    if (st == SPC_OK) *fwd = w.fwd, *bwd = w.bwd;
+    return st;
+}
+
+extern "C" spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a, const void* q, int64_t ldq, const void* k,
+                                        int64_t ldk, const void* v, int64_t ldv, void* out, int64_t ldo, float* stats, void* ws,
+                                        size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    Plan w;
+    Args p;
+    spc_status st = check_sizes(dtype, a, w);
+    if (st == SPC_OK) st = check_call(dtype, a, ws, w.fwd, ws_bytes, p);
+    if (st != SPC_OK) return st;
+    for (const Side& s : {Side{q, ldq, a->heads, "q"}, Side{out, ldo, a->heads, "out"}})
+        if ((st = check_rows(dtype, a, s, a->n_q)) != SPC_OK) return st;
+    for (const Side& s : {Side{k, ldk, a->kv_heads, "k"}, Side{v, ldv, a->kv_heads, "v"}})
+        if ((st = check_rows(dtype, a, s, a->n_kv)) != SPC_OK) return st;
+    if (stats && !aligned16(stats)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    if (a->n_q == 0) return SPC_OK;
+    const int64_t e = dtype_size(dtype);
+    p.q = static_cast<const char*>(q), p.k = static_cast<const char*>(k), p.v = static_cast<const char*>(v), p.out = static_cast<char*>(out);
+    p.ldq = ldq * e, p.ldk = ldk * e, p.ldv = ldv * e, p.ldo = ldo * e;
+    p.stats = reinterpret_cast<float2*>(stats);
+    p.part = static_cast<float*>(ws);
+    switch (dtype) {
+        case SPC_F32: return launch_fwd_f32(p, w.q, stream);
+        case SPC_F16: return launch_fwd_f16(p, w.q, stream);
+        case SPC_BF16: return launch_fwd_bf16(p, w.q, stream);
+    }
+    return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+}
+
+extern "C" spc_status spc_attention_bwd(spc_dtype dtype, const spc_attention* a, const void* dout, int64_t lddo, const void* q,
+                                        int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, const void* out,
+                                        int64_t ldo, const float* stats, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv,
+                                        int64_t lddv, void* ws, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    Plan w;
+    Args p;
+    spc_status st = check_sizes(dtype, a, w);
+    if (st == SPC_OK) st = check_call(dtype, a, ws, w.bwd, ws_bytes, p);
+    if (st != SPC_OK) return st;
+    for (const Side& s : {Side{dout, lddo, a->heads, "dout"}, Side{q, ldq, a->heads, "q"}, Side{out, ldo, a->heads, "out"},
+                          Side{dq, lddq, a->heads, "dq"}})
+        if ((st = check_rows(dtype, a, s, a->n_q)) != SPC_OK) return st;
+    for (const Side& s : {Side{k, ldk, a->kv_heads, "k"}, Side{v, ldv, a->kv_heads, "v"}, Side{dk, lddk, a->kv_heads, "dk"},
+                          Side{dv, lddv, a->kv_heads, "dv"}})
+        if ((st = check_rows(dtype, a, s, a->n_kv)) != SPC_OK) return st;
+    if (a->n_q > 0 && !stats) return fail(SPC_ERR_ARG, "stats is NULL");
+    if (stats && !aligned16(stats)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    const int64_t e = dtype_size(dtype);
+    p.q = static_cast<const char*>(q), p.k = static_cast<const char*>(k), p.v = static_cast<const char*>(v);
+    p.o = static_cast<const char*>(out), p.dout = static_cast<const char*>(dout);
+    p.dq = static_cast<char*>(dq), p.dk = static_cast<char*>(dk), p.dv = static_cast<char*>(dv);
+    p.ldq = ldq * e, p.ldk = ldk * e, p.ldv = ldv * e, p.ldo = ldo * e, p.lddo = lddo * e;
+    p.lddq = lddq * e, p.lddk = lddk * e, p.lddv = lddv * e;
+    p.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
+    p.delta = static_cast<float*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(size_t(a->n_q) * size_t(a->heads) * 4, 256));
+    switch (dtype) {
+        case SPC_F32: return launch_bwd_f32(p, w.q, w.k, stream);
+        case SPC_F16: return launch_bwd_f16(p, w.q, w.k, stream);
+        case SPC_BF16: return launch_bwd_bf16(p, w.q, w.k, stream);
+    }
+    return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+}

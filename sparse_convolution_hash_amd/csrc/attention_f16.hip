@@ -1,0 +1,11 @@
+// The attention kernels for f16.
+#include "attention.h"
+
+namespace spc {
+namespace attn {
+
+spc_status launch_fwd_f16(const Args& p, const Cut& c, hipStream_t stream) { return launch_fwd<F16>(p, c, stream); }
+spc_status launch_bwd_f16(const Args& p, const Cut& q, const Cut& k, hipStream_t stream) { return launch_bwd<F16>(p, q, k, stream); }
+
+}  // namespace attn
+}  // namespace spc

@@ -1,0 +1,328 @@
+// Layer norm over the channels of each row, with the residual join before it:
+//   u = x + residual,  y = gamma (u - mean) rstd + beta,
+//   backward: h = (u - mean) rstd, w = gamma dy,
+//   du = rstd (w - mean(w) - h mean(w h)) (+ dtotal),
+//   dgamma = sum dy h, dbeta = sum dy over the rows.
+// A row lies in the registers of 2 to 64 lanes, eight channels a lane and
+// step, so every tensor is read once; what bounds it is memory.
+//
+// Differences are taken from the rounded mean and their own mean, near 0, is
+// taken out again: a row far from 0 next to its spread keeps the precision
+// that its values have.  The backward does the same from the saved mean.
+#include "rows.h"
+
+namespace spc {
+namespace {
+
+constexpr int LT = 256;          // threads per workgroup
+constexpr int LN_C_MAX = 4096;   // channels that one wave holds: 8 steps of 512
+
+// Sums of K values over the lanes of a row (lanes a power of two, aligned).
+template <int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], int lanes) {
+    for (int m = 1; m < lanes; m <<= 1) {
+        float t[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) t[k] = __shfl_xor(v[k], m);
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += t[k];
+    }
+}
+
+__device__ __forceinline__ float sum8(const f32x8_t& v) { return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])); }
+
+__device__ __forceinline__ f32x8_t ldf8(const float* p) { return widen<F32>(ld8<F32>(p)); }
+
+// V steps of 512 channels (lanes = 64), or one step of `lanes` lanes; R rows of
+// a thread in flight.
+template <typename TT, int V, int R, bool RES>
+__global__ __launch_bounds__(LT) void k_ln_fwd(const void* x_, const void* res_, int64_t n, int C, int lanes, float inv_c,
+                                               const float* gamma, const float* beta, float eps, void* y_, void* total_,
+                                               float2* stats) {
+    using S = typename TT::storage;
+    const S *x = static_cast<const S*>(x_), *res = static_cast<const S*>(res_);
+    S *y = static_cast<S*>(y_), *total = static_cast<S*>(total_);
+    const int rl = int(threadIdx.x) / lanes, c0 = (int(threadIdx.x) % lanes) * 8, per = LT / lanes;
+    const int64_t row0 = int64_t(blockIdx.x) * (per * R) + rl;
+    f32x8_t u[R][V];
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t r = row0 + k * per;
+            const int c = c0 + 512 * v;
+            if (r < n && c < C) {
+                u[k][v] = widen<TT>(ld8<TT>(x + r * C + c));
+                if constexpr (RES) {
+                    const Raw8<TT> t = narrow<TT>(u[k][v] + widen<TT>(ld8<TT>(res + r * C + c)));
+                    st8<TT>(total + r * C + c, t);
+                    u[k][v] = widen<TT>(t);      // the sum as it is stored, so that the backward sees the same
+                }
+            } else {
+                u[k][v] = 0.f;
+            }
+        }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int64_t r = row0 + k * per;
+        float s[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[0] += sum8(u[k][v]);
+        row_sums(s, lanes);
+        const float mean = s[0] * inv_c;
+        float q[2] = {0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (c0 + 512 * v < C) u[k][v] -= mean;
+            q[0] += sum8(u[k][v]);
+            q[1] += sum8(u[k][v] * u[k][v]);
+        }
+        row_sums(q, lanes);
+        const float md = q[0] * inv_c, rstd = rsqrtf(fmaxf(fmaf(-md, md, q[1] * inv_c), 0.f) + eps);
+        if (r >= n) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = c0 + 512 * v;
+            if (c >= C) continue;
+            f32x8_t h = (u[k][v] - md) * rstd;
+            if (gamma) h *= ldf8(gamma + c);
+            if (beta) h += ldf8(beta + c);
+            st8<TT>(y + r * C + c, narrow<TT>(h));
+        }
+        if (c0 == 0) stats[r] = float2{mean + md, rstd};
+    }
+}
+
+// A workgroup takes `iters` (at most 16) rows of each of its row groups, keeps
+// its channels' two sums in fp32 over them, and adds up the groups in double:
+// part[workgroup][C] (dgamma, dbeta), or the results where there is one.
+template <typename TT, int V, bool AFFINE>
+__global__ __launch_bounds__(LT) void k_ln_bwd(const void* dy_, const void* x_, int64_t n, int C, int lanes, int iters, float inv_c,
+                                               const float* gamma, const float2* stats, const void* dtotal_, void* dx_,
+                                               float2* part, float* dgamma, float* dbeta) {
+    using S = typename TT::storage;
+    const S *dy = static_cast<const S*>(dy_), *x = static_cast<const S*>(x_), *dtotal = static_cast<const S*>(dtotal_);
+    S* dx = static_cast<S*>(dx_);
+    __shared__ float2 lds[AFFINE ? LT * 8 : 1];
+    const int rl = int(threadIdx.x) / lanes, c0 = (int(threadIdx.x) % lanes) * 8, per = LT / lanes;
+    f32x8_t sg[V], sb[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sg[v] = 0.f, sb[v] = 0.f;
+    for (int it = 0; it < iters; ++it) {
+        const int64_t r = (int64_t(blockIdx.x) * iters + it) * per + rl;
+        const bool in = r < n;
+        const float2 st = in ? stats[r] : float2{0.f, 0.f};
+        f32x8_t d[V], g[V];
+        float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = c0 + 512 * v;
+            if (in && c < C) {
+                d[v] = widen<TT>(ld8<TT>(x + r * C + c)) - st.x;
+                g[v] = widen<TT>(ld8<TT>(dy + r * C + c));
+            } else {
+                d[v] = 0.f, g[v] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            f32x8_t w = g[v];
+            if (gamma && c0 + 512 * v < C) w *= ldf8(gamma + c0 + 512 * v);
+            s[0] += sum8(d[v]);
+            s[1] += sum8(w);
+            s[2] += sum8(w * d[v]);
+        }
+        row_sums(s, lanes);
+        const float md = s[0] * inv_c, m1 = s[1] * inv_c, m2 = st.y * fmaf(-md, s[1], s[2]) * inv_c;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = c0 + 512 * v;
+            if (!in || c >= C) continue;
+            const f32x8_t h = (d[v] - md) * st.y;
+            f32x8_t w = g[v];
+            if (gamma) w *= ldf8(gamma + c);
+            w = (w - m1 - h * m2) * st.y;
+            if (dtotal) w += widen<TT>(ld8<TT>(dtotal + r * C + c));
+            st8<TT>(dx + r * C + c, narrow<TT>(w));
+            if constexpr (AFFINE) sg[v] += g[v] * h, sb[v] += g[v];
+        }
+    }
+    if constexpr (AFFINE) {
+        const int cw = lanes * 8;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) lds[rl * cw + c0 + e] = float2{sg[v][e], sb[v][e]};
+            __syncthreads();
+            for (int i = int(threadIdx.x); i < cw; i += LT) {
+                const int c = i + 512 * v;
+                if (c >= C) continue;
+                double a = 0.0, b = 0.0;
+                for (int k = 0; k < per; ++k) a += lds[k * cw + i].x, b += lds[k * cw + i].y;
+                if (part) {
+                    part[int64_t(blockIdx.x) * C + c] = float2{float(a), float(b)};
+                } else {
+                    if (dgamma) dgamma[c] = float(a);
+                    if (dbeta) dbeta[c] = float(b);
+                }
+            }
+        }
+    }
+}
+
+// Sums of the workgroups' parts in double, four channels to a workgroup.
+__global__ __launch_bounds__(LT) void k_ln_sums(const float2* part, int64_t parts, int C, float* dgamma, float* dbeta) {
+    __shared__ double2 lds[LT];
+    const int e = int(threadIdx.x) & 3, c = int(blockIdx.x) * 4 + e;
+    double a = 0.0, b = 0.0;
+    for (int64_t k = threadIdx.x >> 2; k < parts; k += LT / 4) {
+        const float2 t = part[k * C + c];
+        a += t.x, b += t.y;
+    }
+    lds[threadIdx.x] = double2{a, b};
+    for (int m = LT / 2; m >= 4; m >>= 1) {
+        __syncthreads();
+        if (int(threadIdx.x) < m) lds[threadIdx.x].x += lds[threadIdx.x + m].x, lds[threadIdx.x].y += lds[threadIdx.x + m].y;
+    }
+    if (threadIdx.x < 4) {
+        if (dgamma) dgamma[c] = float(lds[e].x);
+        if (dbeta) dbeta[c] = float(lds[e].y);
+    }
+}
+
+struct LnCut {
+    int lanes, per;          // lanes of a row, rows of a workgroup at a time
+    int iters;               // the backward's rounds
+    int64_t parts;           // its workgroups
+    size_t bytes;
+};
+
+spc_status check_sizes(int64_t n, int32_t C, LnCut& k) {
+    if (n < 0 || n >= ROWS_END) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
+    if (C <= 0 || C % 16) return fail(SPC_ERR_UNSUPPORTED, "C=%d: channels must be a positive multiple of 16", C);
+    if (C > LN_C_MAX) return fail(SPC_ERR_UNSUPPORTED, "C=%d: at most %d channels", C, LN_C_MAX);
+    k.lanes = 2;
+    while (k.lanes < 64 && k.lanes * 8 < C) k.lanes *= 2;
+    k.per = LT / k.lanes;
+    const int64_t want = ceil_div(n, int64_t(k.per) * 512);
+    k.iters = int(want < 1 ? 1 : want > 16 ? 16 : want);
+    k.parts = ceil_div(n, int64_t(k.per) * k.iters);
+    k.bytes = k.parts > 1 ? size_t(k.parts) * size_t(C) * 8 : 0;
+    if (!launchable(k.parts, LT) || !launchable(ceil_div(n, k.per), LT))
+        return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d channels exceed one launch", (long long)n, C);
+    return SPC_OK;
+}
+
+template <typename TT, int V, int R>
+spc_status launch_fwd(const void* x, const void* res, int64_t n, int C, const LnCut& k, const float* gamma, const float* beta,
+                      float eps, void* y, void* total, float2* stats, hipStream_t stream) {
+    const dim3 grid(unsigned(ceil_div(n, int64_t(k.per) * R)));
+    const float inv = 1.f / float(C);
+    if (res) hipLaunchKernelGGL((k_ln_fwd<TT, V, R, true>), grid, dim3(LT), 0, stream, x, res, n, C, k.lanes, inv, gamma, beta, eps, y, total, stats);
+    else hipLaunchKernelGGL((k_ln_fwd<TT, V, R, false>), grid, dim3(LT), 0, stream, x, res, n, C, k.lanes, inv, gamma, beta, eps, y, total, stats);
+    SPC_LAUNCHED("k_ln_fwd");
+    return SPC_OK;
+}
+
+template <typename TT>
+spc_status dispatch_fwd(const void* x, const void* res, int64_t n, int C, const LnCut& k, const float* gamma, const float* beta,
+                        float eps, void* y, void* total, float2* stats, hipStream_t stream) {
+    if (C <= 512) return launch_fwd<TT, 1, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+    if (C <= 1024) return launch_fwd<TT, 2, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+    if (C <= 2048) return launch_fwd<TT, 4, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+    return launch_fwd<TT, 8, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+}
+
+template <typename TT, int V>
+spc_status launch_bwd(const void* dy, const void* x, int64_t n, int C, const LnCut& k, const float* gamma, const float2* stats,
+                      const void* dtotal, void* dx, float* dgamma, float* dbeta, float2* part, hipStream_t stream) {
+    const dim3 grid(unsigned(k.parts));
+    const float inv = 1.f / float(C);
+    if (k.parts <= 1) part = nullptr;
+    if (!dgamma && !dbeta) {
+        hipLaunchKernelGGL((k_ln_bwd<TT, V, false>), grid, dim3(LT), 0, stream, dy, x, n, C, k.lanes, k.iters, inv, gamma, stats, dtotal, dx, part, dgamma, dbeta);
+        SPC_LAUNCHED("k_ln_bwd");
+        return SPC_OK;
+    }
+    if (k.parts) {
+        hipLaunchKernelGGL((k_ln_bwd<TT, V, true>), grid, dim3(LT), 0, stream, dy, x, n, C, k.lanes, k.iters, inv, gamma, stats, dtotal, dx, part, dgamma, dbeta);
+        SPC_LAUNCHED("k_ln_bwd");
+    }
+    if (k.parts != 1) {
+        hipLaunchKernelGGL(k_ln_sums, dim3(unsigned(C / 4)), dim3(LT), 0, stream, part, k.parts, C, dgamma, dbeta);
+        SPC_LAUNCHED("k_ln_sums");
+    }
+    return SPC_OK;
+}
+
+template <typename TT>
+spc_status dispatch_bwd(const void* dy, const void* x, int64_t n, int C, const LnCut& k, const float* gamma, const float2* stats,
+                        const void* dtotal, void* dx, float* dgamma, float* dbeta, float2* part, hipStream_t stream) {
+    if (n == 0 && !dgamma && !dbeta) return SPC_OK;
+    if (C <= 512) return launch_bwd<TT, 1>(dy, x, n, C, k, gamma, stats, dtotal, dx, dgamma, dbeta, part, stream);
+    if (C <= 1024) return launch_bwd<TT, 2>(dy, x, n, C, k, gamma, stats, dtotal, dx, dgamma, dbeta, part, stream);
+    if (C <= 2048) return launch_bwd<TT, 4>(dy, x, n, C, k, gamma, stats, dtotal, dx, dgamma, dbeta, part, stream);
+    return launch_bwd<TT, 8>(dy, x, n, C, k, gamma, stats, dtotal, dx, dgamma, dbeta, part, stream);
+}
+
+}  // namespace
+}  // namespace spc
+
+using namespace spc;
+
+extern "C" spc_status spc_layer_norm_workspace(int64_t n, int32_t C, size_t* bytes) {
+    clear_error();
+    if (!bytes) return fail(SPC_ERR_ARG, "bytes is NULL");
+    LnCut k;
+    const spc_status st = check_sizes(n, C, k);
+    if (st == SPC_OK) *bytes = k.bytes;
+    return st;
+}
+
+extern "C" spc_status spc_layer_norm_fwd(spc_dtype dtype, const void* x, const void* residual, int64_t n, int32_t C,
+                                         const float* gamma, const float* beta, float eps, void* y, void* total, float* stats,
+                                         hipStream_t stream) {
+    clear_error();
+    LnCut k;
+    if (dtype != SPC_F32 && dtype != SPC_F16 && dtype != SPC_BF16) return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+    const spc_status st = check_sizes(n, C, k);
+    if (st != SPC_OK) return st;
+    if (!(eps > 0.f)) return fail(SPC_ERR_ARG, "eps=%g must be positive", double(eps));
+    if (!residual != !total) return fail(SPC_ERR_ARG, "residual and total: give both or neither");
+    for (const void* q : {x, residual, (const void*)gamma, (const void*)beta, (const void*)y, (const void*)total, (const void*)stats})
+        if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    if (n == 0) return SPC_OK;
+    if (!x || !y || !stats) return fail(SPC_ERR_ARG, "x, y or stats is NULL");
+    float2* so = reinterpret_cast<float2*>(stats);
+    switch (dtype) {
+        case SPC_F32: return dispatch_fwd<F32>(x, residual, n, C, k, gamma, beta, eps, y, total, so, stream);
+        case SPC_F16: return dispatch_fwd<F16>(x, residual, n, C, k, gamma, beta, eps, y, total, so, stream);
+        case SPC_BF16: return dispatch_fwd<BF16>(x, residual, n, C, k, gamma, beta, eps, y, total, so, stream);
+    }
+    return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+}
+
+extern "C" spc_status spc_layer_norm_bwd(spc_dtype dtype, const void* dout, const void* x, int64_t n, int32_t C, const float* gamma,
+                                         const float* stats, const void* dtotal, void* dx, float* dgamma, float* dbeta, void* ws,
+                                         size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    LnCut k;
+    if (dtype != SPC_F32 && dtype != SPC_F16 && dtype != SPC_BF16) return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+    const spc_status st = check_sizes(n, C, k);
+    if (st != SPC_OK) return st;
+    for (const void* q : {dout, x, (const void*)gamma, (const void*)stats, dtotal, (const void*)dx, (const void*)dgamma, (const void*)dbeta, (const void*)ws})
+        if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    if (n > 0 && (!dout || !x || !stats || !dx)) return fail(SPC_ERR_ARG, "dout, x, stats or dx is NULL");
+    const size_t need = dgamma || dbeta ? k.bytes : 0;
+    if (need && !ws) return fail(SPC_ERR_ARG, "ws is NULL");
+    if (ws_bytes < need) return fail(SPC_ERR_WORKSPACE, "ws_bytes=%zu, need %zu", ws_bytes, need);
+    const float2* si = reinterpret_cast<const float2*>(stats);
+    float2* part = static_cast<float2*>(ws);
+    switch (dtype) {
+        case SPC_F32: return dispatch_bwd<F32>(dout, x, n, C, k, gamma, si, dtotal, dx, dgamma, dbeta, part, stream);
+        case SPC_F16: return dispatch_bwd<F16>(dout, x, n, C, k, gamma, si, dtotal, dx, dgamma, dbeta, part, stream);
+        case SPC_BF16: return dispatch_bwd<BF16>(dout, x, n, C, k, gamma, si, dtotal, dx, dgamma, dbeta, part, stream);
+    }
+    return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+}

@@ -1,0 +1,125 @@
+// Rotary positions of several axes: pair j of a head, elements 2j and 2j + 1,
+// belongs to one axis of the row's position and is rotated by the angle
+// position * freq[j]; pairs past the axes' stay as they are.
+//
+// A workgroup computes the sines and cosines of its rows once into LDS, for
+// all heads, and then walks the rows' chunks of 8 elements in memory order,
+// reading and writing every line once.  Angles: the product of the int32
+// position and the fp32 frequency is taken in double, in quarter turns, so a
+// position of 2^31 loses nothing; what is left of it, at most an eighth of a
+// turn, goes to fp32.
+#include "rows.h"
+
+namespace spc {
+namespace {
+
+constexpr int RT = 256;           // threads per workgroup
+constexpr int TABLE = 2048;       // pairs a workgroup has room for (16 KB)
+constexpr int AXES = 8;
+constexpr int ROT_D_MAX = 2 * TABLE;
+
+struct RotArgs {
+    const char* x;
+    char* out;
+    int64_t ldx, ldo;             // bytes between rows
+    const int32_t* pos;
+    int64_t ldp;                  // elements between positions
+    const float* freq;
+    int64_t n;
+    int heads, D, rows;           // rows of a workgroup
+    int axes, pairs;              // rotated pairs of a head
+    int end[AXES];                // pairs of the axes up to and with each
+    float sign;                   // -1: the rotation back
+};
+
+template <typename TT>
+__global__ __launch_bounds__(RT) void k_rotary(const RotArgs p) {
+    __shared__ __attribute__((aligned(16))) float2 table[TABLE];
+    constexpr int ES = sizeof(typename TT::storage);
+    const int64_t row0 = int64_t(blockIdx.x) * p.rows;
+    const int rows = int(p.n - row0 < p.rows ? p.n - row0 : p.rows), half = p.D / 2;
+    for (int e = int(threadIdx.x); e < rows * half; e += RT) {
+        const int r = e / half, j = e - r * half;
+        float2 cs = {1.f, 0.f};
+        if (j < p.pairs) {
+            int axis = 0;
+            while (j >= p.end[axis]) ++axis;
+            const double quarters = double(p.pos[(row0 + r) * p.ldp + axis]) * double(p.freq[j]) * 0.63661977236758134308;
+            const double whole = rint(quarters);
+            float s, c;
+            sincospif(float(quarters - whole) * 0.5f, &s, &c);
+            const int k = int(int64_t(whole) & 3);
+            cs.x = k == 0 ? c : k == 1 ? -s : k == 2 ? -c : s;
+            cs.y = (k == 0 ? s : k == 1 ? c : k == 2 ? -s : -c) * p.sign;
+        }
+        table[e] = cs;
+    }
+    __syncthreads();
+    const int width = p.heads * (p.D / 8), chunks = rows * width;
+    for (int e = int(threadIdx.x); e < chunks; e += RT) {
+        const int r = e / width, c = e - r * width, i = c % (p.D / 8);
+        f32x8_t v = widen<TT>(ld8<TT>(p.x + (row0 + r) * p.ldx + int64_t(c) * 8 * ES));
+        const float2* t = table + r * half + i * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 cs = t[k];
+            const float a = v[2 * k], b = v[2 * k + 1];
+            v[2 * k] = fmaf(a, cs.x, -(b * cs.y));
+            v[2 * k + 1] = fmaf(a, cs.y, b * cs.x);
+        }
+        st8<TT>(p.out + (row0 + r) * p.ldo + int64_t(c) * 8 * ES, narrow<TT>(v));
+    }
+}
+
+}  // namespace
+}  // namespace spc
+
+using namespace spc;
+
+extern "C" spc_status spc_rotary(spc_dtype dtype, const void* x, int64_t ldx, int64_t n, int32_t heads, int32_t head_dim,
+                                 const int32_t* pos, int64_t ldp, int32_t n_axes, const int32_t* pairs, const float* freq,
+                                 int32_t inverse, void* out, int64_t ldo, hipStream_t stream) {
+    clear_error();
+    if (dtype != SPC_F32 && dtype != SPC_F16 && dtype != SPC_BF16) return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
+    if (n < 0 || n >= ROWS_END) return fail(SPC_ERR_ARG, "n=%lld is out of range", (long long)n);
+    if (heads < 1) return fail(SPC_ERR_ARG, "heads=%d must be positive", heads);
+    if (head_dim < 1 || head_dim % 16 || head_dim > ROT_D_MAX)
+        return fail(SPC_ERR_UNSUPPORTED, "head_dim=%d: a multiple of 16 up to %d", head_dim, ROT_D_MAX);
+    if (int64_t(heads) * head_dim > C_MAX) return fail(SPC_ERR_UNSUPPORTED, "%d heads of %d are too many", heads, head_dim);
+    if (n_axes < 1 || n_axes > AXES || !pairs) return fail(SPC_ERR_ARG, "n_axes=%d: 1 to %d, with their pairs", n_axes, AXES);
+    const int64_t e = dtype_size(dtype), width = int64_t(heads) * head_dim;
+    for (const int64_t ld : {ldx, ldo})
+        if (ld < width || ld * e % 16 || ld >= (int64_t(1) << 31))
+            return fail(SPC_ERR_ARG, "row stride %lld: at least heads x head_dim, a multiple of 16 bytes, below 2^31", (long long)ld);
+    if (ldp < n_axes || ldp >= (int64_t(1) << 31)) return fail(SPC_ERR_ARG, "ldp=%lld is not between n_axes=%d and 2^31", (long long)ldp, n_axes);
+    RotArgs p{};
+    int64_t sum = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        if (pairs[a] < 0) return fail(SPC_ERR_ARG, "pairs[%d]=%d is negative", a, pairs[a]);
+        sum += pairs[a];
+        if (sum > head_dim / 2) return fail(SPC_ERR_ARG, "%lld pairs exceed half of head_dim=%d", (long long)sum, head_dim);
+        p.end[a] = int(sum);
+    }
+    if (n == 0) return SPC_OK;
+    if (!x || !out || !pos || (sum && !freq)) return fail(SPC_ERR_ARG, "x, out, pos or freq is NULL");
+    for (const void* q : {x, (const void*)out})
+        if (!aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    // positions may be columns of the coordinates: aligned as their type
+    for (const void* q : {(const void*)pos, (const void*)freq})
+        if (reinterpret_cast<uintptr_t>(q) & 3u) return fail(SPC_ERR_ARG, "pos and freq must be aligned to 4 bytes");
+    p.x = static_cast<const char*>(x), p.out = static_cast<char*>(out);
+    p.ldx = ldx * e, p.ldo = ldo * e, p.ldp = ldp, p.pos = pos, p.freq = freq;
+    p.n = n, p.heads = heads, p.D = head_dim, p.axes = n_axes, p.pairs = int(sum), p.sign = inverse ? -1.f : 1.f;
+    // as many rows as the table holds, fewer where that leaves compute units without work
+    const int64_t room = TABLE / (head_dim / 2), fill = ceil_div(n, 1024);
+    p.rows = int(fill < room ? fill : room);
+    const int64_t blocks = ceil_div(n, p.rows);
+    if (!launchable(blocks, RT)) return fail(SPC_ERR_UNSUPPORTED, "%lld rows of %d elements exceed one launch", (long long)n, head_dim);
+    switch (dtype) {
+        case SPC_F32: hipLaunchKernelGGL(k_rotary<F32>, dim3(unsigned(blocks)), dim3(RT), 0, stream, p); break;
+        case SPC_F16: hipLaunchKernelGGL(k_rotary<F16>, dim3(unsigned(blocks)), dim3(RT), 0, stream, p); break;
+        case SPC_BF16: hipLaunchKernelGGL(k_rotary<BF16>, dim3(unsigned(blocks)), dim3(RT), 0, stream, p); break;
+    }
+    SPC_LAUNCHED("k_rotary");
+    return SPC_OK;
+}
