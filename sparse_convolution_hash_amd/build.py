@@ -35,9 +35,16 @@ FLAGS = [
 
 # Per-source additions.  The MFMA rate probe keeps its accumulators in VGPRs:
 # in AGPRs the compiler moves its independent accumulator chains between
-# registers every round, and the probe would time those moves.
+# registers every round, and the probe would time those moves.  So do the
+# 16-bit attention kernels, whose vector instructions read and write every
+# accumulator: 266,426 x 4 x 32 bf16 in windows of 1,024 has 108 registers
+# instead of 95 + 48 in the forward, 4 waves to a SIMD instead of 3
+# (fp32's spend their time in the matrix unit; the moves do not show).
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 SOURCE_FLAGS = {
-    "calibrate.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "calibrate.hip": _VGPR_FORM,
+    "attention_f16.hip": _VGPR_FORM,
+    "attention_bf16.hip": _VGPR_FORM,
 }
 
 

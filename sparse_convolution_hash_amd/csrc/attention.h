@@ -165,87 +165,74 @@ struct Second {
         }
     }
 
-    // Elements of a left operand by class, as 1 and 0 of the type (clean: the
-    // finite ones themselves).
-    enum Class { CLEAN, POS, NEG, NOT_A_NUMBER, INFINITE };
-    static __device__ __forceinline__ uint32_t pick16(uint32_t u, Class k) {
-        constexpr uint32_t INF = TT::id == SPC_BF16 ? 0x7f80u : 0x7c00u, ONE = TT::id == SPC_BF16 ? 0x3f80u : 0x3c00u;
-        const uint32_t m = u & 0x7fffu;
-        switch (k) {
-            case CLEAN: return m < INF ? u : 0u;
-            case POS: return u == INF ? ONE : 0u;
-            case NEG: return u == (INF | 0x8000u) ? ONE : 0u;
-            case INFINITE: return m == INF ? ONE : 0u;
-            default: return m > INF ? ONE : 0u;
-        }
-    }
-    static __device__ __forceinline__ uint32_t pick32(uint32_t u, Class k) {
-        constexpr uint32_t INF = 0x7f800000u, ONE = 0x3f800000u;
-        const uint32_t m = u & 0x7fffffffu;
-        switch (k) {
-            case CLEAN: return m < INF ? u : 0u;
-            case POS: return u == INF ? ONE : 0u;
-            case NEG: return u == (INF | 0x80000000u) ? ONE : 0u;
-            case INFINITE: return m == INF ? ONE : 0u;
-            default: return m > INF ? ONE : 0u;
-        }
-    }
-    static __device__ __forceinline__ u32x4 pick(const u32x4& a, Class k) {
+    // The finite elements of a left operand, the others 0.
+    static __device__ __forceinline__ u32x4 finite(const u32x4& a) {
         uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        if constexpr (TT::E == 4) {
+            w[0] = (w[0] & 0x7f800000u) == 0x7f800000u ? 0u : w[0];
+        } else {
+            constexpr uint32_t INF = TT::id == SPC_BF16 ? 0x7f80u : 0x7c00u;
 #pragma unroll
-        for (int i = 0; i < (TT::E == 8 ? 4 : 1); ++i)
-            w[i] = TT::E == 8 ? pick16(w[i] & 0xffffu, k) | pick16(w[i] >> 16, k) << 16 : pick32(w[i], k);
+            for (int i = 0; i < 4; ++i) w[i] &= ((w[i] & INF) == INF ? 0u : 0xffffu) | ((w[i] >> 16 & INF) == INF ? 0u : 0xffff0000u);
+        }
         return u32x4{w[0], w[1], w[2], w[3]};
     }
+    static __device__ __forceinline__ u32x4 minus(const u32x4& a, const u32x4& b) {
+        return u32x4{a.x ^ b.x, a.y ^ b.y, a.z ^ b.z, a.w ^ b.w};     // b is a or 0 in each element
+    }
 
-    // The same where w is 0 for pairs that a mask hides (bit bit_of(r) of vis is
-    // 0): hidden pairs are not in the sum, so an infinite or NaN X[j][d] must
-    // not reach the columns that do not see row j, as 0 * inf would.  Where
-    // X holds such values, the finite ones are summed and what the others
-    // make of each sum is counted apart.
+    // The same where a mask hides pairs (bit bit_of(r) of vis is 0, and w is 0).
+    // Hidden pairs are not in the sum, so an infinite or NaN X[j][d] must not
+    // reach the columns that do not see row j, as 0 * inf would: where X holds
+    // such values, the finite ones are summed as ever, and the others row by
+    // row, each added to the columns that see it.
     static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w,
                                                       uint32_t vis, int lane) {
-        bool odd = false;
+        bool any = false;
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t)
+        for (int t = 0; t < STEPS; ++t) {
+            float wt[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) wt[e] = w[t * PER + e];
+            const u32x4 b = pack(wt);
 #pragma unroll
             for (int db = 0; db < T::NB; ++db) {
-                const u32x4 a = left(x, row0, t, db, lane), f = pick(a, CLEAN);
-                odd |= a.x != f.x || a.y != f.y || a.z != f.z || a.w != f.w;
-            }
-        if (!__any(odd)) return add(acc, x, row0, w, lane);
-#pragma unroll
-        for (int db = 0; db < T::NB; ++db) {
-#pragma unroll
-            for (int t = 0; t < STEPS; ++t) {
-                float wt[PER];
-#pragma unroll
-                for (int e = 0; e < PER; ++e) wt[e] = w[t * PER + e];
-                acc[db] = step(pick(left(x, row0, t, db, lane), CLEAN), pack(wt), acc[db]);
-            }
-#pragma unroll 1
-            for (int kind = 0; kind < 3; ++kind) {        // infinite, minus infinite, neither
-                f32x16_t n = zero16();
-#pragma unroll
-                for (int t = 0; t < STEPS; ++t) {
-                    const u32x4 a = left(x, row0, t, db, lane);
-                    float b1[PER], b2[PER];
-#pragma unroll
-                    for (int e = 0; e < PER; ++e) {
-                        const float u = w[t * PER + e];
-                        const bool see = (vis >> bit_of(t * PER + e)) & 1u;
-                        const bool gt = see && u > 0.f, lt = see && u < 0.f;
-                        b1[e] = (kind == 0 ? gt : kind == 1 ? lt : see && !gt && !lt) ? 1.f : 0.f;
-                        b2[e] = (kind == 0 ? lt : kind == 1 ? gt : see) ? 1.f : 0.f;
-                    }
-                    n = step(kind < 2 ? pick(a, POS) : pick(a, INFINITE), pack(b1), n);
-                    n = step(kind < 2 ? pick(a, NEG) : pick(a, NOT_A_NUMBER), pack(b2), n);
-                }
-                const float v = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[db][r] += n[r] > 0.f ? v : 0.f;
+                const u32x4 a = left(x, row0, t, db, lane), f = finite(a), m = minus(a, f);
+                any |= (m.x | m.y | m.z | m.w) != 0u;
+                acc[db] = step(f, b, acc[db]);
             }
         }
+        if (!__any(any)) return;
+        const int h = lane >> 5;
+        const uint32_t all = vis << (4 * h) | uint32_t(__shfl_xor(int(vis << (4 * h)), 32));   // of both halves' rows
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t)
+#pragma unroll 1
+            for (int i = 0; i < 2 * PER; ++i) {
+                const int e = i & (PER - 1), half = i / PER;           // element e of one half is row j of the tile
+                const int j = bit_of(t * PER) + (e & 3) + 8 * (e >> 2) + 4 * half;
+                const bool see = (all >> j) & 1u;
+                float wt[PER];
+#pragma unroll
+                for (int k = 0; k < PER; ++k) wt[k] = k == e && h == half ? w[t * PER + k] : 0.f;
+                const u32x4 b = pack(wt);
+#pragma unroll
+                for (int db = 0; db < T::NB; ++db) {
+                    const u32x4 a = left(x, row0, t, db, lane);
+                    u32x4 f = minus(a, finite(a));
+                    if constexpr (TT::E == 8) {
+                        uint32_t v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = h == half && k == e >> 1 ? v[k] & (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+                        f = u32x4{v[0], v[1], v[2], v[3]};
+                    } else {
+                        f.x = h == half ? f.x : 0u;
+                    }
+                    const f32x16_t one = step(f, b, zero16());
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[db][r] += see ? one[r] : 0.f;
+                }
+            }
     }
 };
 
@@ -362,14 +349,14 @@ constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
 
 constexpr float LAZY = 8.f;   // a column's sums are rescaled once its maximum grew by 2^8
 
-template <typename TT, int DP, int NW>
+template <typename TT, int DP, int NW, bool CAUSAL>
 __global__ __launch_bounds__(64 * NW) void k_attn_fwd(const Args p) {
     constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
     using T = Tile<TT, DP>;
     using S = Stage<TT, DP, BN, NT>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
     Job j;
-    if (!job_of<BM>(p, p.qs, p.g, p.causal != 0, j)) return;
+    if (!job_of<BM>(p, p.qs, p.g, CAUSAL, j)) return;
     const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
     const int ka = __builtin_amdgcn_readfirstlane(p.ks.at(j.s)), kb = __builtin_amdgcn_readfirstlane(p.ks.at(j.s + 1));
     const int lk = kb > ka ? kb - ka : 0, rows = j.len * p.g, off = lk - j.len;
@@ -378,9 +365,9 @@ __global__ __launch_bounds__(64 * NW) void k_attn_fwd(const Args p) {
     u32x4 qf[T::NS];
     load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + int64_t(q.head) * p.D * T::ES, q.row >= 0, p.D, h);
     // keys that the workgroup's last row, the wave's first and its last see
-    auto limit = [&](int r) { return !p.causal ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
+    auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
     const int nk = limit(j.r0 + BM - 1), seen_first = rw < rows ? limit(rw) : 0, seen_last = rw < rows ? limit(rw + 31) : 0;
-    const int mine = p.causal ? q.pos + 1 + off : lk;      // keys [0, mine) of this lane's query
+    const int mine = CAUSAL ? q.pos + 1 + off : lk;      // keys [0, mine) of this lane's query
     const int tiles = (nk + BN - 1) / BN, per = (tiles + p.splits - 1) / p.splits;
     const int t0 = j.split * per, t1 = min(tiles, t0 + per);
 
@@ -446,7 +433,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_fwd(const Args p) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[u][r] = (vis[u] >> bit_of(r)) & 1u ? s[u][r] : -INFINITY;
                 }
-                masked = p.causal != 0;
+                masked = CAUSAL;
             } else {
                 seen = 1;
             }
@@ -477,7 +464,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_fwd(const Args p) {
                 }
 #pragma unroll
             for (int u = 0; u < KT; ++u) {
-                if (masked) Second<TT, DP>::add_masked(acc, vt, 32 * u, s[u], vis[u], lane);
+                if (CAUSAL && masked) Second<TT, DP>::add_masked(acc, vt, 32 * u, s[u], vis[u], lane);
                 else Second<TT, DP>::add(acc, vt, 32 * u, s[u], lane);
             }
         }
@@ -561,14 +548,14 @@ __device__ __forceinline__ float2 from_stats(float2 ml) {
 }
 
 // dq and delta: as the forward, a wave of 32 queries walks the keys.
-template <typename TT, int DP, int NW>
+template <typename TT, int DP, int NW, bool CAUSAL>
 __global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
     constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
     using T = Tile<TT, DP>;
     using S = Stage<TT, DP, BN, NT>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
     Job j;
-    if (!job_of<BM>(p, p.qs, p.g, p.causal != 0, j)) return;
+    if (!job_of<BM>(p, p.qs, p.g, CAUSAL, j)) return;
     const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
     const int ka = __builtin_amdgcn_readfirstlane(p.ks.at(j.s)), kb = __builtin_amdgcn_readfirstlane(p.ks.at(j.s + 1));
     const int lk = kb > ka ? kb - ka : 0, rows = j.len * p.g, off = lk - j.len;
@@ -601,9 +588,9 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
     }
     if (q.row >= 0 && h == 0 && j.split == 0) p.delta[id] = delta;
     const float2 mf = from_stats<TT>(q.row >= 0 ? p.stats[id] : float2{0.f, 0.f});
-    auto limit = [&](int r) { return !p.causal ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
+    auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
     const int nk = limit(j.r0 + BM - 1), seen_first = rw < rows ? limit(rw) : 0, seen_last = rw < rows ? limit(rw + 31) : 0;
-    const int mine = p.causal ? q.pos + 1 + off : lk;
+    const int mine = CAUSAL ? q.pos + 1 + off : lk;
     const int tiles = (nk + BN - 1) / BN, per = (tiles + p.splits - 1) / p.splits;
     const int t0 = j.split * per, t1 = min(tiles, t0 + per);
 
@@ -666,7 +653,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
                     const uint32_t vis = (uint32_t(live >> (32 * u)) & uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = (vis >> bit_of(r)) & 1u ? s[r] : 0.f;
-                    if (p.causal) Second<TT, DP>::add_masked(acc, kt, 32 * u, s, vis, lane);
+                    if constexpr (CAUSAL) Second<TT, DP>::add_masked(acc, kt, 32 * u, s, vis, lane);
                     else Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
                 } else {
                     Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
@@ -704,7 +691,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
 
 // dk and dv: a wave of 32 keys walks the queries of all heads that share them,
 // which sums their gradients without an atomic.
-template <typename TT, int DP, int NW>
+template <typename TT, int DP, int NW, bool CAUSAL>
 __global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
     constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
     using T = Tile<TT, DP>;
@@ -723,7 +710,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
     load_frags<TT, DP>(kf, p.k + int64_t(krow) * p.ldk + in, krow >= 0, p.D, h);
     load_frags<TT, DP>(vf, p.v + int64_t(krow) * p.ldv + in, krow >= 0, p.D, h);
     // the first row that sees a key: of the workgroup's first, the wave's first and last, this lane's
-    auto begin = [&](int k) { return !p.causal ? 0 : min(rows, max(0, k - off) * p.g); };
+    auto begin = [&](int k) { return !CAUSAL ? 0 : min(rows, max(0, k - off) * p.g); };
     const int first = begin(j.r0), first_lo = begin(kw), first_hi = begin(kw + 31), mine = begin(key);
     const int tb = first / BN, tiles = (rows + BN - 1) / BN - tb, per = (tiles + p.splits - 1) / p.splits;
     const int t0 = tb + j.split * per, t1 = min(tb + tiles, t0 + per);
@@ -822,7 +809,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
                         const bool see = (vis >> bit_of(r)) & 1u;
                         s[r] = see ? s[r] : 0.f, d[r] = see ? d[r] : 0.f;
                     }
-                    if (p.causal) {
+                    if constexpr (CAUSAL) {
                         Second<TT, DP>::add_masked(dv, gt, 32 * u, s, vis, lane);
                         Second<TT, DP>::add_masked(dk, qt, 32 * u, d, vis, lane);
                         continue;
@@ -917,12 +904,18 @@ inline unsigned set_grid(Args& p, int64_t slots, int splits) {
     return p.chunk * 8;
 }
 
+#define ATTN_WIDTH(name, dp, nw, grid, p)                                                                                     \
+    do {                                                                                                                      \
+        if (p.causal) hipLaunchKernelGGL((name<TT, dp, nw, true>), dim3(grid), dim3(64 * nw), 0, stream, p);                  \
+        else hipLaunchKernelGGL((name<TT, dp, nw, false>), dim3(grid), dim3(64 * nw), 0, stream, p);                          \
+    } while (0)
+
 #define ATTN_WIDTHS(name, nw, grid, p)                                                                                        \
     do {                                                                                                                      \
-        if (p.D <= 16) hipLaunchKernelGGL((name<TT, 16, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                       \
-        else if (p.D <= 32) hipLaunchKernelGGL((name<TT, 32, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                  \
-        else if (p.D <= 64) hipLaunchKernelGGL((name<TT, 64, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                  \
-        else hipLaunchKernelGGL((name<TT, 128, nw>), dim3(grid), dim3(64 * nw), 0, stream, p);                                \
+        if (p.D <= 16) ATTN_WIDTH(name, 16, nw, grid, p);                                                                     \
+        else if (p.D <= 32) ATTN_WIDTH(name, 32, nw, grid, p);                                                                \
+        else if (p.D <= 64) ATTN_WIDTH(name, 64, nw, grid, p);                                                                \
+        else ATTN_WIDTH(name, 128, nw, grid, p);                                                                              \
         SPC_LAUNCHED(#name);                                                                                                  \
     } while (0)
 
