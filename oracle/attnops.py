@@ -102,11 +102,14 @@ def _samples(nq, nk, q_ptr, kv_ptr, q_order, kv_order, causal):
         yield rq[okq], rk[okk], see[okq][:, okk]
 
 
-def attention(q, k, v, q_ptr, kv_ptr, scale, causal=False, q_order=None, kv_order=None, dout=None, step=0.0, floor=0.0):
+def attention(q, k, v, q_ptr, kv_ptr, scale, causal=False, q_order=None, kv_order=None, dout=None, step=0.0, floor=0.0,
+              split=(0.0, 0.0)):
     """dict of out, (m + log l) and, with dout, dq, dk, dv, each with its
     envelope under "e_" + name, and "rows"/"keys": which rows are in a sample.
     step: the relative rounding of p and ds (0: none); floor: what p and ds are
-    off by at least (their type's smallest numbers)."""
+    off by at least (their type's smallest numbers).  split: how far the factor
+    scale log2(e) times an element of q or k, kept as two numbers of the type,
+    may be off, relative and absolute."""
     q, k, v = f64(q), f64(k), f64(v)
     nq, H, D = q.shape
     nk, Hk, _ = k.shape
@@ -126,6 +129,7 @@ def attention(q, k, v, q_ptr, kv_ptr, scale, causal=False, q_order=None, kv_orde
             with np.errstate(invalid="ignore", over="ignore"):
                 s = np.where(see, Q @ K.T * scale, -np.inf)
             es = (D + 6) * EPS * scale * (np.abs(Q) @ np.abs(K).T)
+            es = es + split[0] * scale * (np.abs(Q) @ np.abs(K).T) + split[1] * (np.abs(Q).sum(1)[:, None] + np.abs(K).sum(1)[None, :])
             es = np.where(see, es, 0.0)
             top = s.max(1, keepdims=True)
             top = np.where(np.isneginf(top), 0.0, top)

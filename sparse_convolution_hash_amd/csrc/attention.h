@@ -34,20 +34,22 @@ struct Args {
     const int32_t *q_order, *kv_order;
     Segs qs, ks;
     int32_t g, hk, D, causal;               // query heads to a key head, key heads, head dimension
+    uint32_t inv_g;                         // 2^32 / g, rounded up (g > 1)
     float c, scale;                         // c = scale log2(e)
     float2* stats;                          // [heads, n_q] (m, l)
     float* delta;                           // [heads, n_q] do . o
     float* part;                            // partial results of the splits
     int32_t splits, slots;
-    unsigned chunk, total;                  // workgroups of one XCD, of all
+    unsigned group, total;                  // workgroups that an XCD takes in a row, of all
 };
 
-__device__ __forceinline__ f32x16_t zero16() {
+__device__ __forceinline__ f32x16_t all16(float v) {
     f32x16_t z;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) z[r] = 0.f;
+    for (int r = 0; r < 16; ++r) z[r] = v;
     return z;
 }
+__device__ __forceinline__ f32x16_t zero16() { return all16(0.f); }
 
 // One 32x32 tile step over 32 bytes of contraction: lane l supplies row
 // (column) l % 32 and the 16 bytes of half l / 32.
@@ -81,6 +83,20 @@ __device__ __forceinline__ float sum_halves(float v) {
 }
 
 __device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// Four results of one row, rounded once and stored.
+template <typename TT>
+__device__ __forceinline__ void put4(char* p, f32x4_t v) {
+    if constexpr (TT::id == SPC_BF16) {
+        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, __builtin_convertvector(v, b4));
+    } else if constexpr (TT::id == SPC_F16) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, __builtin_convertvector(v, h4));
+    } else {
+        *reinterpret_cast<f32x4_t*>(p) = v;
+    }
+}
 
 // Row of a tile register: register r of a lane in half h holds row
 // 8 (r / 4) + 4 h + r % 4; bit_of(r) is the row of h = 0.
@@ -177,18 +193,29 @@ struct Second {
         }
         return u32x4{w[0], w[1], w[2], w[3]};
     }
-    static __device__ __forceinline__ u32x4 minus(const u32x4& a, const u32x4& b) {
-        return u32x4{a.x ^ b.x, a.y ^ b.y, a.z ^ b.z, a.w ^ b.w};     // b is a or 0 in each element
+    // Elements that are infinity (kind 0), minus infinity (1) or NaN (2), as 1.
+    static __device__ __forceinline__ u32x4 only(const u32x4& a, int kind) {
+        uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        constexpr bool W = TT::E == 4;
+        constexpr uint32_t INF = W ? 0x7f800000u : TT::id == SPC_BF16 ? 0x7f80u : 0x7c00u;
+        constexpr uint32_t ONE = W ? 0x3f800000u : TT::id == SPC_BF16 ? 0x3f80u : 0x3c00u;
+        constexpr uint32_t SIGN = W ? 0x80000000u : 0x8000u;
+        auto one = [&](uint32_t u) { return (kind == 2 ? (u & (SIGN - 1)) > INF : u == (kind ? INF | SIGN : INF)) ? ONE : 0u; };
+#pragma unroll
+        for (int i = 0; i < (W ? 1 : 4); ++i) w[i] = W ? one(w[i]) : one(w[i] & 0xffffu) | one(w[i] >> 16) << 16;
+        return u32x4{w[0], w[1], w[2], w[3]};
     }
 
     // The same where a mask hides pairs (bit bit_of(r) of vis is 0, and w is 0).
     // Hidden pairs are not in the sum, so an infinite or NaN X[j][d] must not
-    // reach the columns that do not see row j, as 0 * inf would: where X holds
-    // such values, the finite ones are summed as ever, and the others row by
-    // row, each added to the columns that see it.
+    // reach the columns that do not see row j, as 0 * inf would: the finite
+    // values are summed.  With OTHERS (w are probabilities, positive), an
+    // infinite or NaN value reaches the columns that see its row: counted
+    // apart.  Without, it has made w itself NaN in those columns.
+    template <bool OTHERS>
     static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w,
                                                       uint32_t vis, int lane) {
-        bool any = false;
+        bool odd = false;
 #pragma unroll
         for (int t = 0; t < STEPS; ++t) {
             float wt[PER];
@@ -197,42 +224,31 @@ struct Second {
             const u32x4 b = pack(wt);
 #pragma unroll
             for (int db = 0; db < T::NB; ++db) {
-                const u32x4 a = left(x, row0, t, db, lane), f = finite(a), m = minus(a, f);
-                any |= (m.x | m.y | m.z | m.w) != 0u;
+                const u32x4 a = left(x, row0, t, db, lane), f = finite(a);
+                if constexpr (OTHERS) odd |= a.x != f.x || a.y != f.y || a.z != f.z || a.w != f.w;
                 acc[db] = step(f, b, acc[db]);
             }
         }
-        if (!__any(any)) return;
-        const int h = lane >> 5;
-        const uint32_t all = vis << (4 * h) | uint32_t(__shfl_xor(int(vis << (4 * h)), 32));   // of both halves' rows
+        if constexpr (OTHERS) {
+            if (!__any(odd)) return;
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t)
+            for (int db = 0; db < T::NB; ++db)
 #pragma unroll 1
-            for (int i = 0; i < 2 * PER; ++i) {
-                const int e = i & (PER - 1), half = i / PER;           // element e of one half is row j of the tile
-                const int j = bit_of(t * PER) + (e & 3) + 8 * (e >> 2) + 4 * half;
-                const bool see = (all >> j) & 1u;
-                float wt[PER];
+                for (int kind = 0; kind < 3; ++kind) {
+                    asm volatile("" : "+v"(lane), "+v"(vis));      // nothing of this part is computed ahead of it
+                    f32x16_t n = zero16();
 #pragma unroll
-                for (int k = 0; k < PER; ++k) wt[k] = k == e && h == half ? w[t * PER + k] : 0.f;
-                const u32x4 b = pack(wt);
+                    for (int t = 0; t < STEPS; ++t) {
+                        float see[PER];
 #pragma unroll
-                for (int db = 0; db < T::NB; ++db) {
-                    const u32x4 a = left(x, row0, t, db, lane);
-                    u32x4 f = minus(a, finite(a));
-                    if constexpr (TT::E == 8) {
-                        uint32_t v[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = h == half && k == e >> 1 ? v[k] & (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
-                        f = u32x4{v[0], v[1], v[2], v[3]};
-                    } else {
-                        f.x = h == half ? f.x : 0u;
+                        for (int e = 0; e < PER; ++e) see[e] = (vis >> bit_of(t * PER + e)) & 1u ? 1.f : 0.f;
+                        n = step(only(left(x, row0, t, db, lane), kind), pack(see), n);
                     }
-                    const f32x16_t one = step(f, b, zero16());
+                    const float v = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[db][r] += see ? one[r] : 0.f;
+                    for (int r = 0; r < 16; ++r) acc[db][r] += n[r] > 0.f ? v : 0.f;
                 }
-            }
+        }
     }
 };
 
@@ -242,9 +258,10 @@ struct Second {
 // positions and, for queries, the heads that share keys (row = position * mult
 // + head).  Sample s owns the slots from floor(at(s) mult / BM) + s on, at
 // least as many as it has tiles, so no table of tiles is needed; the slots left
-// over end at once.  Workgroups go round the 8 XCDs in launch order: each XCD
-// takes a contiguous part of (split, slot, head), so that workgroups which
-// read the same keys share an L2.
+// over end at once.  Workgroups go round the 8 XCDs in launch order: an XCD
+// takes groups of neighbours in (split, slot, head), which read the same keys
+// through its L2, and the groups go round the XCDs, so that long samples, and
+// the late rows of a causal one, spread over all of them.
 struct Job {
     int s, head, split, r0, a, len;    // sample, key head, split, first row, first position of the sample, its positions
 };
@@ -252,8 +269,8 @@ struct Job {
 template <int BM>
 __device__ __forceinline__ bool job_of(const Args& p, const Segs& segs, int mult, bool reverse, Job& j) {
     const unsigned x = blockIdx.x & 7u, i = blockIdx.x >> 3;
-    unsigned l = x * p.chunk + i;
-    if (i >= p.chunk || l >= p.total) return false;
+    unsigned l = (i / p.group * 8u + x) * p.group + i % p.group;
+    if (l >= p.total) return false;
     j.head = int(l % unsigned(p.hk));
     l /= unsigned(p.hk);
     int slot = int(l % unsigned(p.slots));
@@ -297,13 +314,24 @@ __device__ __forceinline__ int row_of(const int32_t* order, int a, int pos, int 
 struct Query {
     int pos, head, row;      // row -1: there is none
 };
-__device__ __forceinline__ Query query_of(const Args& p, const Job& j, int qa, int rq, int rows) {
-    Query q;
-    q.pos = p.g == 1 ? rq : rq / p.g;
-    q.head = j.head * p.g + (p.g == 1 ? 0 : rq - q.pos * p.g);
-    q.row = rq < rows ? row_of(p.q_order, qa, q.pos, p.qs.n) : -1;
+__device__ __forceinline__ Query place_of(const Args& p, const Job& j, int rq) {
+    Query q{rq, j.head, -1};
+    if (p.g > 1) {
+        // rq times the rounded-up 2^32 / g: the quotient, or one more
+        q.pos = int(__umulhi(unsigned(rq), p.inv_g));
+        q.pos -= q.pos * p.g > rq;
+        q.head = j.head * p.g + (rq - q.pos * p.g);
+    }
     return q;
 }
+__device__ __forceinline__ Query query_of(const Args& p, const Job& j, int qa, int rq, int rows) {
+    Query q = place_of(p, j, rq);
+    if (rq < rows) q.row = row_of(p.q_order, qa, q.pos, p.qs.n);
+    return q;
+}
+
+// Bits of the first cnt of 64 rows.
+__device__ __forceinline__ uint64_t first_bits(int cnt) { return cnt >= 64 ? ~0ull : cnt <= 0 ? 0ull : (1ull << cnt) - 1; }
 
 // Fragments of one row of DP elements (zeros past D, or for no row), as the
 // column operand of the first product.
@@ -314,6 +342,32 @@ __device__ __forceinline__ void load_frags(u32x4* f, const char* row, bool there
     for (int s = 0; s < T::NS; ++s) f[s] = there && (2 * s + h) * 16 < D * T::ES ? ld16(row + (2 * s + h) * 16) : zero4();
 }
 
+// Narrow heads of 16-bit types spend their time in the vector unit, a score's
+// multiplication by c and subtraction of m among it, and leave the matrix unit
+// idle.  There the column operand is multiplied by c once, kept as the sum of
+// two numbers of the type (off by 2^-18 of itself for bf16, 2^-22 for fp16), and
+// the product starts from -m, so that the matrix unit hands over the exponent
+// itself.  Wider heads would pay more in the matrix unit (a second product
+// over DP) than they save: 64 cycles for DP / 16 products of 32 on each tile.
+template <typename TT, int DP>
+constexpr bool SPLIT = TT::E == 8 && DP <= 32;
+
+// f times c as f + lo (lo has entries where the product is split).
+template <typename TT, int DP>
+__device__ __forceinline__ void split_frags(u32x4* f, u32x4* lo, float c) {
+    if constexpr (SPLIT<TT, DP>) {
+#pragma unroll
+        for (int s = 0; s < Tile<TT, DP>::NS; ++s) {
+            Raw8<TT> x;
+            x.v[0] = f[s];
+            const f32x8_t t = widen<TT>(x) * c;
+            x = narrow<TT>(t);
+            f[s] = x.v[0];
+            lo[s] = narrow<TT>(t - widen<TT>(x)).v[0];
+        }
+    }
+}
+
 // Staging of tiles of BN rows from two tensors: what a thread moves.
 template <typename TT, int DP, int BN, int NT>
 struct Stage {
@@ -322,23 +376,101 @@ struct Stage {
     static __device__ __forceinline__ bool mine(int i) { return CH % NT == 0 || int(threadIdx.x) + i * NT < CH; }
     static __device__ __forceinline__ int row(int i) { return (int(threadIdx.x) + i * NT) / T::M; }
     static __device__ __forceinline__ int chunk(int i) { return (int(threadIdx.x) + i * NT) % T::M; }
-    static __device__ __forceinline__ void put(char* tile, const u32x4 (&v)[PT]) {
+
+    u32x4 ra[PT], rb[PT];
+    bool whole;          // every element of the tile is there (the same for all threads)
+    uint32_t there;      // bit i: this thread's part i is
+
+    // Rows that lie ld bytes apart from `a` and `b` on, the first cnt > 0 of
+    // them there, `width` bytes of each.  Loads are unconditional, so that
+    // nothing waits for them before put(): absent parts load a part that is
+    // there, and put() writes zeros for them.
+    __device__ __forceinline__ void load(const char* a, int64_t lda, const char* b, int64_t ldb, int cnt, int width) {
+        whole = cnt >= BN && width == T::PITCH;
+        there = ~0u;
+        int64_t oa[PT], ob[PT];
+#pragma unroll
+        for (int i = 0; i < PT; ++i) oa[i] = row(i) * lda + chunk(i) * 16, ob[i] = row(i) * ldb + chunk(i) * 16;
+        if (!whole) {
+            there = 0;
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const int r = row(i) < cnt ? row(i) : cnt - 1, c = chunk(i) * 16 < width ? chunk(i) * 16 : 0;
+                there |= uint32_t(row(i) < cnt && chunk(i) * 16 < width) << i;
+                oa[i] = r * lda + c, ob[i] = r * ldb + c;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < PT; ++i)
-            if (mine(i)) st16(tile + T::at(row(i), chunk(i)), v[i]);
+            if (mine(i)) ra[i] = ld16(a + oa[i]), rb[i] = ld16(b + ob[i]);
+    }
+    // Part i of this thread from the row at `a` and `b` plus the offsets; call
+    // begin_parts() first.
+    __device__ __forceinline__ void begin_parts() { whole = false, there = 0; }
+    __device__ __forceinline__ void load_part(int i, bool is, const char* a, const char* b, int width) {
+        const bool in = chunk(i) * 16 < width;
+        there |= uint32_t(is && in) << i;
+        const int c = in ? chunk(i) * 16 : 0;
+        if (mine(i)) ra[i] = ld16(a + c), rb[i] = ld16(b + c);
+    }
+    __device__ __forceinline__ void put(char* ta, char* tb) {
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < PT; ++i)
+                if (!((there >> i) & 1u)) ra[i] = zero4(), rb[i] = zero4();
+        }
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+            if (mine(i)) {
+                st16(ta + T::at(row(i), chunk(i)), ra[i]);
+                st16(tb + T::at(row(i), chunk(i)), rb[i]);
+            }
     }
 };
 
-// Bits of the first cnt of 64 rows.
-__device__ __forceinline__ uint64_t first_bits(int cnt) { return cnt >= 64 ? ~0ull : cnt <= 0 ? 0ull : (1ull << cnt) - 1; }
+// Keys of a sample, tile by tile: rows in place come from one base; entries of
+// an order are read one tile ahead of the rows that they name, and looked at
+// when those are fetched.
+template <typename TT, int DP, int BN, int NT>
+struct KeyStage : Stage<TT, DP, BN, NT> {
+    using S = Stage<TT, DP, BN, NT>;
+    const char *k, *v;
+    int ka, lk, width;
+    int at[S::PT], mark;
+    uint64_t live;           // keys of the fetched tile that are there, as bits
 
-// Keys of a tile [p0, p0 + BN) that are there, as bits.
-template <int BN>
-__device__ __forceinline__ uint64_t live_keys(const Args& p, int ka, int lk, int p0) {
-    if (!p.kv_order) return first_bits(lk - p0 < BN ? lk - p0 : BN);
-    const int t = p0 + (int(threadIdx.x) & (WAVE - 1));
-    return __ballot(t < p0 + BN && t < lk && row_of(p.kv_order, ka, t < lk ? t : lk - 1, p.ks.n) >= 0);
-}
+    __device__ __forceinline__ void begin(const Args& p, const Job& j, int a, int len) {
+        width = p.D * S::T::ES;
+        const int64_t in = int64_t(j.head) * width;
+        k = p.k + in, v = p.v + in;
+        ka = a, lk = len;
+    }
+    __device__ __forceinline__ void find(const Args& p, int t) {
+        if (!p.kv_order) return;
+        const int32_t* o = p.kv_order + ka;
+        mark = o[min(t * BN + (int(threadIdx.x) & (WAVE - 1)), lk - 1)];
+#pragma unroll
+        for (int i = 0; i < S::PT; ++i) at[i] = o[min(t * BN + S::row(i), lk - 1)];
+    }
+    __device__ __forceinline__ void fetch(const Args& p, int t) {
+        const int cnt = lk - t * BN;
+        if (!p.kv_order) {
+            const int64_t row = ka + t * BN;
+            live = first_bits(cnt < BN ? cnt : BN);
+            S::load(k + row * p.ldk, p.ldk, v + row * p.ldv, p.ldv, cnt, width);
+        } else {
+            const int l = int(threadIdx.x) & (WAVE - 1);
+            live = __ballot(l < BN && l < cnt && unsigned(mark) < unsigned(p.ks.n));
+            S::begin_parts();
+#pragma unroll
+            for (int i = 0; i < S::PT; ++i) {
+                const bool is = S::row(i) < cnt && unsigned(at[i]) < unsigned(p.ks.n);
+                const int64_t r = is ? at[i] : 0;
+                S::load_part(i, is, k + r * p.ldk, v + r * p.ldv, width);
+            }
+        }
+    }
+};
 
 // ----------------------------------------------------------- forward
 
@@ -347,131 +479,149 @@ __device__ __forceinline__ uint64_t live_keys(const Args& p, int ka, int lk, int
 template <typename TT, int NW>
 constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
 
-constexpr float LAZY = 8.f;   // a column's sums are rescaled once its maximum grew by 2^8
+// Waves that a SIMD is to hold at least, which bounds the registers: the most
+// that costs no spills in the loops.
+template <typename TT, int DP, bool CAUSAL>
+constexpr int FWD_WAVES = TT::E == 4 ? 1 : DP <= 32 ? 4 - CAUSAL : DP <= 64 ? 3 - CAUSAL : 2;
+template <typename TT, int DP>
+constexpr int BWD_WAVES = TT::E == 4 ? 1 : DP <= 32 ? 3 : DP <= 64 ? 2 : 1;
+
+constexpr float LAZY = 1024.f;   // far below fp16's largest number, which a single p may not pass
 
 template <typename TT, int DP, int NW, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW) void k_attn_fwd(const Args p) {
+__global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_fwd(const Args p) {
     constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
+    constexpr bool SP = SPLIT<TT, DP>;
     using T = Tile<TT, DP>;
-    using S = Stage<TT, DP, BN, NT>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
     Job j;
     if (!job_of<BM>(p, p.qs, p.g, CAUSAL, j)) return;
     const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
     const int ka = __builtin_amdgcn_readfirstlane(p.ks.at(j.s)), kb = __builtin_amdgcn_readfirstlane(p.ks.at(j.s + 1));
     const int lk = kb > ka ? kb - ka : 0, rows = j.len * p.g, off = lk - j.len;
-    const int rw = j.r0 + 32 * wave;                       // the wave's first row
+    const int rw = __builtin_amdgcn_readfirstlane(j.r0 + 32 * wave);          // the wave's first row
     const Query q = query_of(p, j, j.a, rw + col, rows);
-    u32x4 qf[T::NS];
+    u32x4 qf[T::NS], ql[SP ? T::NS : 1];
     load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + int64_t(q.head) * p.D * T::ES, q.row >= 0, p.D, h);
+    split_frags<TT, DP>(qf, ql, p.c);
     // keys that the workgroup's last row, the wave's first and its last see
     auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
     const int nk = limit(j.r0 + BM - 1), seen_first = rw < rows ? limit(rw) : 0, seen_last = rw < rows ? limit(rw + 31) : 0;
-    const int mine = CAUSAL ? q.pos + 1 + off : lk;      // keys [0, mine) of this lane's query
+    const int mine = CAUSAL ? q.pos + 1 + off : lk;        // keys [0, mine) of this lane's query
     const int tiles = (nk + BN - 1) / BN, per = (tiles + p.splits - 1) / p.splits;
     const int t0 = j.split * per, t1 = min(tiles, t0 + per);
 
-    u32x4 rk[S::PT], rv[S::PT];
-    int at[S::PT];
-    auto find = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < S::PT; ++i) {
-            const int pos = t * BN + S::row(i);
-            at[i] = S::mine(i) && pos < lk ? row_of(p.kv_order, ka, pos, p.ks.n) : -1;
-        }
-    };
-    auto fetch = [&]() {
-#pragma unroll
-        for (int i = 0; i < S::PT; ++i) {
-            const bool there = at[i] >= 0 && S::chunk(i) * 16 < p.D * T::ES;
-            const int64_t o = int64_t(j.head) * p.D * T::ES + S::chunk(i) * 16;
-            rk[i] = there ? ld16(p.k + int64_t(at[i]) * p.ldk + o) : zero4();
-            rv[i] = there ? ld16(p.v + int64_t(at[i]) * p.ldv + o) : zero4();
-        }
-    };
-
-    f32x16_t acc[T::NB];
+    KeyStage<TT, DP, BN, NT> stage;
+    stage.begin(p, j, ka, lk);
+    f32x16_t acc[T::NB], from = zero16();                  // from: -m for the split product
 #pragma unroll
     for (int db = 0; db < T::NB; ++db) acc[db] = zero16();
-    float m = -INFINITY, l = 0.f;      // m in units of log2: p = 2^(c s - m)
+    float m = -INFINITY, l = 0.f;                          // m in units of log2: p = 2^(c s - m)
     uint32_t seen = 0;
 
     if (t0 < t1) {
-        find(t0);
-        fetch();
-        if (t0 + 1 < t1) find(t0 + 1);
-        S::put(lds[0][0], rk);
-        S::put(lds[0][1], rv);
+        stage.find(p, t0);
+        stage.fetch(p, t0);
+        if (t0 + 1 < t1) stage.find(p, t0 + 1);
+        stage.put(lds[0][0], lds[0][1]);
     }
     lds_barrier();
     for (int t = t0; t < t1; ++t) {
         const int buf = (t - t0) & 1, p0 = t * BN;
         const bool more = t + 1 < t1;
+        const uint64_t live = stage.live;
         if (more) {
-            fetch();
-            if (t + 2 < t1) find(t + 2);
+            stage.fetch(p, t + 1);
+            if (t + 2 < t1) stage.find(p, t + 2);
         }
         if (p0 < seen_last) {          // else none of the wave's rows sees the tile
-            const uint64_t live = live_keys<BN>(p, ka, lk, p0);
             const char *kt = lds[buf][0], *vt = lds[buf][1];
-            f32x16_t s[KT];
+            const bool edge = p0 + BN > seen_first || live != first_bits(BN);
             uint32_t vis[KT];
-            bool masked = false;
-#pragma unroll
-            for (int u = 0; u < KT; ++u) {
-                s[u] = zero16();
-#pragma unroll
-                for (int st = 0; st < T::NS; ++st) s[u] = mfma32<TT>(T::row16(kt, 32 * u + col, 2 * st + h), qf[st], s[u]);
-            }
-            const bool edge = live != first_bits(BN) || p0 + BN > seen_first;
             if (edge) {
 #pragma unroll
                 for (int u = 0; u < KT; ++u) {
                     const int n = mine - (p0 + 32 * u);
                     vis[u] = (uint32_t(live >> (32 * u)) & uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
                     seen |= vis[u] & 0x0f0f0f0fu;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[u][r] = (vis[u] >> bit_of(r)) & 1u ? s[u][r] : -INFINITY;
                 }
-                masked = CAUSAL;
             } else {
                 seen = 1;
             }
-            float top = s[0][0];
+            // Scores are exponentiated against the maximum so far.  Their sum
+            // tells whether it still serves: where a column's part of the tile
+            // sums to more than LAZY, and at the first tile, the scores are
+            // computed once more (the tile is still there) for a new maximum.
+            f32x16_t s[KT];
+            float sum = 0.f;
+            for (bool fresh = t == t0;;) {
+                int c = col;
+                asm volatile("" : "+v"(c));    // the second round reads the tile again: nothing is kept for it
 #pragma unroll
-            for (int u = 0; u < KT; ++u)
+                for (int u = 0; u < KT; ++u) {
+                    s[u] = SP ? from : zero16();
 #pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
-            const float2 both = halves(top);
-            top = fmaxf(both.x, both.y) * p.c;
-            const bool grew = top > m + LAZY;
-            if (__any(grew)) {         // the other columns keep their sums to the bit
-                const float a = grew ? exp2_(m - top) : 1.f;
-                l *= a;
-#pragma unroll
-                for (int db = 0; db < T::NB; ++db)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[db][r] *= a;
-                m = grew ? top : m;
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int u = 0; u < KT; ++u)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[u][r] = exp2_(fmaf(s[u][r], p.c, -base));
-                    l += s[u][r];
+                    for (int st = 0; st < T::NS; ++st) {
+                        const u32x4 a = T::row16(kt, 32 * u + c, 2 * st + h);
+                        s[u] = mfma32<TT>(a, qf[st], s[u]);
+                        if constexpr (SP) s[u] = mfma32<TT>(a, ql[st], s[u]);
+                    }
                 }
+                if (edge) {
+#pragma unroll
+                    for (int u = 0; u < KT; ++u) {
+                        asm volatile("" : "+v"(vis[u]));
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[u][r] = (vis[u] >> bit_of(r)) & 1u ? s[u][r] : -INFINITY;
+                    }
+                }
+                if (fresh) {
+                    float top = s[0][0];
+#pragma unroll
+                    for (int u = 0; u < KT; ++u)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
+                    const float2 both = halves(top), sums = halves(sum);
+                    top = fmaxf(both.x, both.y);
+                    // the other columns keep their sums to the bit
+                    const bool none = m == -INFINITY, grew = top > -INFINITY && (none || sums.x > LAZY || sums.y > LAZY);
+                    float a = 1.f;
+                    if constexpr (SP) {    // s is c s - m already
+                        const float d = grew ? top : 0.f;
+                        a = !grew ? 1.f : none ? 0.f : exp2_(-top);
+#pragma unroll
+                        for (int u = 0; u < KT; ++u) s[u] -= d;
+                        m = !grew ? m : none ? top : m + top;
+                        from = all16(m == -INFINITY ? 0.f : -m);
+                    } else if (grew) {
+                        a = none ? 0.f : exp2_(m - top * p.c);
+                        m = top * p.c;
+                    }
+                    l *= a;
+#pragma unroll
+                    for (int db = 0; db < T::NB; ++db) acc[db] *= a;
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < KT; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        s[u][r] = exp2_(SP ? s[u][r] : fmaf(s[u][r], p.c, -base));
+                        part[r & 3] += s[u][r];
+                    }
+                sum = (part[0] + part[1]) + (part[2] + part[3]);
+                if (fresh || !__any(sum > LAZY)) break;
+                fresh = true;
+            }
+            l += sum;
 #pragma unroll
             for (int u = 0; u < KT; ++u) {
-                if (CAUSAL && masked) Second<TT, DP>::add_masked(acc, vt, 32 * u, s[u], vis[u], lane);
+                if (CAUSAL && edge) Second<TT, DP>::template add_masked<true>(acc, vt, 32 * u, s[u], vis[u], lane);
                 else Second<TT, DP>::add(acc, vt, 32 * u, s[u], lane);
             }
         }
-        if (more) {
-            S::put(lds[buf ^ 1][0], rk);
-            S::put(lds[buf ^ 1][1], rv);
-        }
+        if (more) stage.put(lds[buf ^ 1][0], lds[buf ^ 1][1]);
         lds_barrier();
     }
     l = sum_halves(l);
@@ -498,7 +648,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_fwd(const Args p) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int d = 32 * db + 8 * b + 4 * h;
-            if (d < p.D) store4<TT>(out + d * T::ES, f32x4_t{acc[db][4 * b] * inv, acc[db][4 * b + 1] * inv, acc[db][4 * b + 2] * inv, acc[db][4 * b + 3] * inv});
+            if (d < p.D) put4<TT>(out + d * T::ES, f32x4_t{acc[db][4 * b] * inv, acc[db][4 * b + 1] * inv, acc[db][4 * b + 2] * inv, acc[db][4 * b + 3] * inv});
         }
     if (p.stats && h == 0) p.stats[id] = float2{m, l};
 }
@@ -529,41 +679,40 @@ __global__ __launch_bounds__(256) void k_attn_join(const Args p) {
             if (ml.x != -INFINITY) o += *reinterpret_cast<const f32x4_t*>(part + s * step + d) * w;
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        store4<TT>(p.out + int64_t(q.row) * p.ldo + (int64_t(q.head) * p.D + d) * ES, o * inv);
+        put4<TT>(p.out + int64_t(q.row) * p.ldo + (int64_t(q.head) * p.D + d) * ES, o * inv);
         if (p.stats && d == 0) p.stats[id] = float2{m, l};
     }
 }
 
 // ---------------------------------------------------------- backward
 
-// What a row's probabilities are computed from: p = 2^(c s - m) * f.
-// 16-bit types fold the sum into m (m + log2 l is off by up to 2^-24 of its
+// What a row's probabilities are computed from: p = 2^(c s + x) * y.
+// 16-bit types fold the sum into x (m + log2 l is off by up to 2^-24 of its
 // size, far below the rounding of p that follows); fp32 multiplies by 1 / l,
 // so that a large m costs no precision.
 template <typename TT>
 __device__ __forceinline__ float2 from_stats(float2 ml) {
-    if (ml.y == 0.f) return float2{INFINITY, 0.f};         // a row that sees no key: 2^-inf
-    if constexpr (TT::E == 8) return float2{ml.x + __log2f(ml.y), 1.f};
-    else return float2{ml.x, 1.f / ml.y};
+    if (ml.y == 0.f) return float2{-INFINITY, 0.f};        // a row that sees no key: 2^-inf
+    if constexpr (TT::E == 8) return float2{-(ml.x + __log2f(ml.y)), 1.f};
+    else return float2{-ml.x, 1.f / ml.y};
 }
 
 // dq and delta: as the forward, a wave of 32 queries walks the keys.
 template <typename TT, int DP, int NW, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
+__global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const Args p) {
     constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
+    constexpr bool SP = SPLIT<TT, DP>;
     using T = Tile<TT, DP>;
-    using S = Stage<TT, DP, BN, NT>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
     Job j;
     if (!job_of<BM>(p, p.qs, p.g, CAUSAL, j)) return;
     const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
     const int ka = __builtin_amdgcn_readfirstlane(p.ks.at(j.s)), kb = __builtin_amdgcn_readfirstlane(p.ks.at(j.s + 1));
     const int lk = kb > ka ? kb - ka : 0, rows = j.len * p.g, off = lk - j.len;
-    const int rw = j.r0 + 32 * wave;
+    const int rw = __builtin_amdgcn_readfirstlane(j.r0 + 32 * wave);
     const Query q = query_of(p, j, j.a, rw + col, rows);
     const int64_t id = int64_t(q.head) * p.qs.n + q.row, in = int64_t(q.head) * p.D * T::ES;
-    u32x4 qf[T::NS], gf[T::NS];
-    load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + in, q.row >= 0, p.D, h);
+    u32x4 qf[T::NS], ql[SP ? T::NS : 1], gf[T::NS];
     load_frags<TT, DP>(gf, p.dout + int64_t(q.row) * p.lddo + in, q.row >= 0, p.D, h);
     float delta = 0.f;
     {
@@ -586,6 +735,8 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
         }
         delta = sum_halves(delta);
     }
+    load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + in, q.row >= 0, p.D, h);
+    split_frags<TT, DP>(qf, ql, p.c);
     if (q.row >= 0 && h == 0 && j.split == 0) p.delta[id] = delta;
     const float2 mf = from_stats<TT>(q.row >= 0 ? p.stats[id] : float2{0.f, 0.f});
     auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
@@ -594,76 +745,61 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
     const int tiles = (nk + BN - 1) / BN, per = (tiles + p.splits - 1) / p.splits;
     const int t0 = j.split * per, t1 = min(tiles, t0 + per);
 
-    u32x4 rk[S::PT], rv[S::PT];
-    int at[S::PT];
-    auto find = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < S::PT; ++i) {
-            const int pos = t * BN + S::row(i);
-            at[i] = S::mine(i) && pos < lk ? row_of(p.kv_order, ka, pos, p.ks.n) : -1;
-        }
-    };
-    auto fetch = [&]() {
-#pragma unroll
-        for (int i = 0; i < S::PT; ++i) {
-            const bool there = at[i] >= 0 && S::chunk(i) * 16 < p.D * T::ES;
-            const int64_t o = int64_t(j.head) * p.D * T::ES + S::chunk(i) * 16;
-            rk[i] = there ? ld16(p.k + int64_t(at[i]) * p.ldk + o) : zero4();
-            rv[i] = there ? ld16(p.v + int64_t(at[i]) * p.ldv + o) : zero4();
-        }
-    };
-
+    KeyStage<TT, DP, BN, NT> stage;
+    stage.begin(p, j, ka, lk);
+    const f32x16_t from_s = SP ? all16(mf.x) : zero16(), from_d = all16(-delta);   // what the products start from
     f32x16_t acc[T::NB];
 #pragma unroll
     for (int db = 0; db < T::NB; ++db) acc[db] = zero16();
     if (t0 < t1) {
-        find(t0);
-        fetch();
-        if (t0 + 1 < t1) find(t0 + 1);
-        S::put(lds[0][0], rk);
-        S::put(lds[0][1], rv);
+        stage.find(p, t0);
+        stage.fetch(p, t0);
+        if (t0 + 1 < t1) stage.find(p, t0 + 1);
+        stage.put(lds[0][0], lds[0][1]);
     }
     lds_barrier();
     for (int t = t0; t < t1; ++t) {
         const int buf = (t - t0) & 1, p0 = t * BN;
         const bool more = t + 1 < t1;
+        const uint64_t live = stage.live;
         if (more) {
-            fetch();
-            if (t + 2 < t1) find(t + 2);
+            stage.fetch(p, t + 1);
+            if (t + 2 < t1) stage.find(p, t + 2);
         }
         if (p0 < seen_last) {
-            const uint64_t live = live_keys<BN>(p, ka, lk, p0);
             const char *kt = lds[buf][0], *vt = lds[buf][1];
-            const bool edge = live != first_bits(BN) || p0 + BN > seen_first;
+            const bool edge = p0 + BN > seen_first || live != first_bits(BN);
 #pragma unroll
             for (int u = 0; u < KT; ++u) {
-                f32x16_t s = zero16(), d = zero16();
+                f32x16_t s = from_s, d = from_d;
 #pragma unroll
-                for (int st = 0; st < T::NS; ++st) s = mfma32<TT>(T::row16(kt, 32 * u + col, 2 * st + h), qf[st], s);
+                for (int st = 0; st < T::NS; ++st) {
+                    const u32x4 a = T::row16(kt, 32 * u + col, 2 * st + h);
+                    s = mfma32<TT>(a, qf[st], s);
+                    if constexpr (SP) s = mfma32<TT>(a, ql[st], s);
+                }
 #pragma unroll
                 for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(vt, 32 * u + col, 2 * st + h), gf[st], d);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    float w = exp2_(fmaf(s[r], p.c, -mf.x));
+                    float w = exp2_(SP ? s[r] : fmaf(s[r], p.c, mf.x));
                     if constexpr (TT::E == 4) w *= mf.y;
-                    s[r] = w * (d[r] - delta);
+                    s[r] = w * d[r];
                 }
                 if (edge) {
                     const int n = mine - (p0 + 32 * u);
                     const uint32_t vis = (uint32_t(live >> (32 * u)) & uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = (vis >> bit_of(r)) & 1u ? s[r] : 0.f;
-                    if constexpr (CAUSAL) Second<TT, DP>::add_masked(acc, kt, 32 * u, s, vis, lane);
-                    else Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
-                } else {
-                    Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
+                    if constexpr (CAUSAL) {
+                        Second<TT, DP>::template add_masked<false>(acc, kt, 32 * u, s, vis, lane);
+                        continue;
+                    }
                 }
+                Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
             }
         }
-        if (more) {
-            S::put(lds[buf ^ 1][0], rk);
-            S::put(lds[buf ^ 1][1], rv);
-        }
+        if (more) stage.put(lds[buf ^ 1][0], lds[buf ^ 1][1]);
         lds_barrier();
     }
     if (q.row < 0) return;
@@ -685,15 +821,16 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dq(const Args p) {
         for (int b = 0; b < 4; ++b) {
             const int d = 32 * db + 8 * b + 4 * h;
             if (d < p.D)
-                store4<TT>(out + d * T::ES, f32x4_t{acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]} * p.scale);
+                put4<TT>(out + d * T::ES, f32x4_t{acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]} * p.scale);
         }
 }
 
 // dk and dv: a wave of 32 keys walks the queries of all heads that share them,
 // which sums their gradients without an atomic.
 template <typename TT, int DP, int NW, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
-    constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
+__global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const Args p) {
+    constexpr int BM = 32 * NW, KT = DP <= 64 ? KT_OF<TT, NW> : 1, BN = 32 * KT, NT = 64 * NW;
+    constexpr bool SP = SPLIT<TT, DP>;
     using T = Tile<TT, DP>;
     using S = Stage<TT, DP, BN, NT>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
@@ -703,51 +840,65 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
     const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, h = lane >> 5, col = lane & 31;
     const int qa = __builtin_amdgcn_readfirstlane(p.qs.at(j.s)), qb = __builtin_amdgcn_readfirstlane(p.qs.at(j.s + 1));
     const int lq = qb > qa ? qb - qa : 0, rows = lq * p.g, off = j.len - lq;
-    const int kw = j.r0 + 32 * wave, key = kw + col;       // the wave's first key, this lane's
+    const int kw = __builtin_amdgcn_readfirstlane(j.r0 + 32 * wave), key = kw + col;   // the wave's first key, this lane's
     const int krow = key < j.len ? row_of(p.kv_order, j.a, key, p.ks.n) : -1;
     const int64_t in = int64_t(j.head) * p.D * T::ES;
-    u32x4 kf[T::NS], vf[T::NS];
+    u32x4 kf[T::NS], kl[SP ? T::NS : 1], vf[T::NS];
     load_frags<TT, DP>(kf, p.k + int64_t(krow) * p.ldk + in, krow >= 0, p.D, h);
     load_frags<TT, DP>(vf, p.v + int64_t(krow) * p.ldv + in, krow >= 0, p.D, h);
+    split_frags<TT, DP>(kf, kl, p.c);
     // the first row that sees a key: of the workgroup's first, the wave's first and last, this lane's
     auto begin = [&](int k) { return !CAUSAL ? 0 : min(rows, max(0, k - off) * p.g); };
     const int first = begin(j.r0), first_lo = begin(kw), first_hi = begin(kw + 31), mine = begin(key);
     const int tb = first / BN, tiles = (rows + BN - 1) / BN - tb, per = (tiles + p.splits - 1) / p.splits;
     const int t0 = tb + j.split * per, t1 = min(tb + tiles, t0 + per);
 
-    u32x4 rq[S::PT], rg[S::PT];
-    int at[S::PT], hd[S::PT], own = -1, own_head = 0;
+    const bool in_place = p.g == 1 && !p.q_order;
+    S stage;
+    int at[S::PT], mark = 0;
+    uint64_t live = 0;
     float2 own_ml = {0.f, 0.f};
     float own_d = 0.f;
+    bool own = false;
     auto find = [&](int t) {
+        if (!p.q_order) return;
+        const int32_t* o = p.q_order + qa;
+        mark = o[min(place_of(p, j, t * BN + lane).pos, lq - 1)];
 #pragma unroll
-        for (int i = 0; i < S::PT; ++i) {
-            const Query q = query_of(p, j, qa, t * BN + S::row(i), S::mine(i) ? rows : 0);
-            at[i] = q.row, hd[i] = q.head;
-        }
-        const Query q = query_of(p, j, qa, t * BN + int(threadIdx.x), int(threadIdx.x) < BN ? rows : 0);
-        own = q.row, own_head = q.head;
+        for (int i = 0; i < S::PT; ++i) at[i] = o[min(place_of(p, j, t * BN + S::row(i)).pos, lq - 1)];
     };
-    auto fetch = [&]() {
+    auto fetch = [&](int t) {
+        const int cnt = rows - t * BN;
+        if (in_place) {
+            const int64_t row = qa + t * BN;
+            stage.load(p.q + row * p.ldq + in, p.ldq, p.dout + row * p.lddo + in, p.lddo, cnt, p.D * T::ES);
+        } else {
+            stage.begin_parts();
 #pragma unroll
-        for (int i = 0; i < S::PT; ++i) {
-            const bool there = at[i] >= 0 && S::chunk(i) * 16 < p.D * T::ES;
-            const int64_t o = int64_t(hd[i]) * p.D * T::ES + S::chunk(i) * 16;
-            rq[i] = there ? ld16(p.q + int64_t(at[i]) * p.ldq + o) : zero4();
-            rg[i] = there ? ld16(p.dout + int64_t(at[i]) * p.lddo + o) : zero4();
+            for (int i = 0; i < S::PT; ++i) {
+                const Query q = place_of(p, j, t * BN + S::row(i));
+                const int w = p.q_order ? at[i] : qa + q.pos;
+                const bool is = S::row(i) < cnt && unsigned(w) < unsigned(p.qs.n);
+                const int64_t r = is ? w : 0, o = is ? int64_t(q.head) * p.D * T::ES : 0;
+                stage.load_part(i, is, p.q + r * p.ldq + o, p.dout + r * p.lddo + o, p.D * T::ES);
+            }
         }
-        const int64_t id = int64_t(own_head) * p.qs.n + own;
-        own_ml = own >= 0 ? p.stats[id] : float2{0.f, 0.f};
-        own_d = own >= 0 ? p.delta[id] : 0.f;
+        const Query q = place_of(p, j, t * BN + lane);
+        const int w = p.q_order ? mark : qa + q.pos;
+        own = lane < BN && lane < cnt && unsigned(w) < unsigned(p.qs.n);
+        live = __ballot(own);
+        if (wave == 0) {
+            const int64_t id = own ? int64_t(q.head) * p.qs.n + w : 0;
+            own_ml = p.stats[id], own_d = p.delta[id];
+        }
     };
     auto put = [&](int buf) {
-        S::put(lds[buf][0], rq);
-        S::put(lds[buf][1], rg);
+        stage.put(lds[buf][0], lds[buf][1]);
         if (int(threadIdx.x) < BN) {
-            const float2 mf = from_stats<TT>(own_ml);
+            const float2 mf = from_stats<TT>(own ? own_ml : float2{0.f, 0.f});
             row_m[buf][threadIdx.x] = mf.x;
             if constexpr (TT::E == 4) row_f[buf][threadIdx.x] = mf.y;
-            row_d[buf][threadIdx.x] = own_d;
+            row_d[buf][threadIdx.x] = own ? -own_d : 0.f;
         }
     };
 
@@ -756,7 +907,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
     for (int db = 0; db < T::NB; ++db) dk[db] = zero16(), dv[db] = zero16();
     if (t0 < t1) {
         find(t0);
-        fetch();
+        fetch(t0);
         put(0);
         if (t0 + 1 < t1) find(t0 + 1);
     }
@@ -764,54 +915,64 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
     for (int t = t0; t < t1; ++t) {
         const int buf = (t - t0) & 1, p0 = t * BN;
         const bool more = t + 1 < t1;
-        uint64_t live;
-        if (!p.q_order) {
-            live = first_bits(rows - p0 < BN ? rows - p0 : BN);
-        } else {
-            const int r = p0 + lane;
-            live = __ballot(lane < BN && query_of(p, j, qa, r, rows).row >= 0);
-        }
+        const uint64_t here = live;
         if (more) {
-            fetch();
+            fetch(t + 1);
             if (t + 2 < t1) find(t + 2);
         }
         if (p0 + BN > first_lo && kw < j.len) {
             const char *qt = lds[buf][0], *gt = lds[buf][1];
-            const bool edge = live != first_bits(BN) || p0 < first_hi;
+            const bool edge = here != first_bits(BN) || p0 < first_hi;
 #pragma unroll
             for (int u = 0; u < KT; ++u) {
-                f32x16_t s = zero16(), d = zero16();
+                // the products start from the rows' -m and -delta
+                f32x16_t s = zero16(), d;
 #pragma unroll
-                for (int st = 0; st < T::NS; ++st) s = mfma32<TT>(T::row16(qt, 32 * u + col, 2 * st + h), kf[st], s);
+                for (int b = 0; b < 4; ++b) {
+                    const int r0 = 32 * u + 8 * b + 4 * h;
+                    const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(&row_d[buf][r0]);
+                    f32x4_t m4;
+                    if constexpr (SP) m4 = *reinterpret_cast<const f32x4_t*>(&row_m[buf][r0]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        d[4 * b + e] = d4[e];
+                        if constexpr (SP) s[4 * b + e] = m4[e];
+                    }
+                }
+#pragma unroll
+                for (int st = 0; st < T::NS; ++st) {
+                    const u32x4 a = T::row16(qt, 32 * u + col, 2 * st + h);
+                    s = mfma32<TT>(a, kf[st], s);
+                    if constexpr (SP) s = mfma32<TT>(a, kl[st], s);
+                }
 #pragma unroll
                 for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(gt, 32 * u + col, 2 * st + h), vf[st], d);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const int r0 = 32 * u + 8 * b + 4 * h;
-                    const f32x4_t m4 = *reinterpret_cast<const f32x4_t*>(&row_m[buf][r0]);
-                    const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(&row_d[buf][r0]);
-                    f32x4_t f4 = {1.f, 1.f, 1.f, 1.f};
+                    f32x4_t m4, f4;
+                    if constexpr (!SP) m4 = *reinterpret_cast<const f32x4_t*>(&row_m[buf][r0]);
                     if constexpr (TT::E == 4) f4 = *reinterpret_cast<const f32x4_t*>(&row_f[buf][r0]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int r = 4 * b + e;
-                        float w = exp2_(fmaf(s[r], p.c, -m4[e]));
+                        float w = exp2_(SP ? s[r] : fmaf(s[r], p.c, m4[e]));
                         if constexpr (TT::E == 4) w *= f4[e];
                         s[r] = w;
-                        d[r] = w * (d[r] - d4[e]);
+                        d[r] *= w;
                     }
                 }
                 if (edge) {
                     const int n = mine - (p0 + 32 * u);    // rows before this lane's first are hidden
-                    const uint32_t vis = (uint32_t(live >> (32 * u)) & ~uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
+                    const uint32_t vis = (uint32_t(here >> (32 * u)) & ~uint32_t(first_bits(n < 32 ? n : 32))) >> (4 * h);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const bool see = (vis >> bit_of(r)) & 1u;
                         s[r] = see ? s[r] : 0.f, d[r] = see ? d[r] : 0.f;
                     }
                     if constexpr (CAUSAL) {
-                        Second<TT, DP>::add_masked(dv, gt, 32 * u, s, vis, lane);
-                        Second<TT, DP>::add_masked(dk, qt, 32 * u, d, vis, lane);
+                        Second<TT, DP>::template add_masked<true>(dv, gt, 32 * u, s, vis, lane);
+                        Second<TT, DP>::template add_masked<false>(dk, qt, 32 * u, d, vis, lane);
                         continue;
                     }
                 }
@@ -843,8 +1004,8 @@ __global__ __launch_bounds__(64 * NW) void k_attn_dkv(const Args p) {
         for (int b = 0; b < 4; ++b) {
             const int d = 32 * db + 8 * b + 4 * h;
             if (d >= p.D) continue;
-            store4<TT>(ok + d * T::ES, f32x4_t{dk[db][4 * b], dk[db][4 * b + 1], dk[db][4 * b + 2], dk[db][4 * b + 3]} * p.scale);
-            store4<TT>(ov + d * T::ES, f32x4_t{dv[db][4 * b], dv[db][4 * b + 1], dv[db][4 * b + 2], dv[db][4 * b + 3]});
+            put4<TT>(ok + d * T::ES, f32x4_t{dk[db][4 * b], dk[db][4 * b + 1], dk[db][4 * b + 2], dk[db][4 * b + 3]} * p.scale);
+            put4<TT>(ov + d * T::ES, f32x4_t{dv[db][4 * b], dv[db][4 * b + 1], dv[db][4 * b + 2], dv[db][4 * b + 3]});
         }
 }
 
@@ -872,10 +1033,10 @@ __global__ __launch_bounds__(256) void k_attn_sum(const Args p) {
         f32x4_t t = {0.f, 0.f, 0.f, 0.f};
         for (int s = 0; s < p.splits; ++s) t += *reinterpret_cast<const f32x4_t*>(part + s * (n * heads * width));
         if constexpr (KEYS) {
-            if (d < p.D) store4<TT>(p.dk + int64_t(row) * p.lddk + (int64_t(head) * p.D + d) * ES, t * p.scale);
-            else store4<TT>(p.dv + int64_t(row) * p.lddv + (int64_t(head) * p.D + d - p.D) * ES, t);
+            if (d < p.D) put4<TT>(p.dk + int64_t(row) * p.lddk + (int64_t(head) * p.D + d) * ES, t * p.scale);
+            else put4<TT>(p.dv + int64_t(row) * p.lddv + (int64_t(head) * p.D + d - p.D) * ES, t);
         } else {
-            store4<TT>(p.dq + int64_t(row) * p.lddq + (int64_t(head) * p.D + d) * ES, t * p.scale);
+            put4<TT>(p.dq + int64_t(row) * p.lddq + (int64_t(head) * p.D + d) * ES, t * p.scale);
         }
     }
 }
@@ -897,11 +1058,16 @@ spc_status launch_bwd_bf16(const Args& p, const Cut& q, const Cut& k, hipStream_
 
 inline int64_t slots_of(int64_t rows, int64_t n_seg, int bm) { return rows / bm + n_seg + 1; }
 
-inline unsigned set_grid(Args& p, int64_t slots, int splits) {
+// Sets the grid of a walk; its workgroups.  A group is 1,024 rows of all heads
+// where there are many (windows of 1,024 on 266,426 x 4 x 32 bf16: forward
+// GROUPED us against ROUND us in groups of one slot), a slot where the work of
+// neighbours differs (causal) or there are few.
+inline unsigned set_grid(Args& p, int64_t slots, int splits, int rows_of_slot, bool even) {
     p.slots = int32_t(slots), p.splits = splits;
     p.total = unsigned(slots * splits * p.hk);
-    p.chunk = unsigned(ceil_div(int64_t(p.total), 8));
-    return p.chunk * 8;
+    const int64_t g = 1024 / rows_of_slot;
+    p.group = unsigned(p.hk) * unsigned(even && slots * splits >= 64 * g ? g : 1);
+    return unsigned(ceil_div(int64_t(p.total), int64_t(p.group) * 8)) * p.group * 8u;
 }
 
 #define ATTN_WIDTH(name, dp, nw, grid, p)                                                                                     \
@@ -912,8 +1078,10 @@ inline unsigned set_grid(Args& p, int64_t slots, int splits) {
 
 #define ATTN_WIDTHS(name, nw, grid, p)                                                                                        \
     do {                                                                                                                      \
-        if (p.D <= 16) ATTN_WIDTH(name, 16, nw, grid, p);                                                                     \
-        else if (p.D <= 32) ATTN_WIDTH(name, 32, nw, grid, p);                                                                \
+        /* c above 1 could take a large fp16 number past the type's range when it is multiplied: no split then */             \
+        const bool split = TT::id != SPC_F16 || p.c <= 1.f;                                                                   \
+        if (p.D <= 16 && split) ATTN_WIDTH(name, 16, nw, grid, p);                                                            \
+        else if (p.D <= 32 && split) ATTN_WIDTH(name, 32, nw, grid, p);                                                       \
         else if (p.D <= 64) ATTN_WIDTH(name, 64, nw, grid, p);                                                                \
         else ATTN_WIDTH(name, 128, nw, grid, p);                                                                              \
         SPC_LAUNCHED(#name);                                                                                                  \
@@ -921,12 +1089,12 @@ inline unsigned set_grid(Args& p, int64_t slots, int splits) {
 
 template <typename TT>
 spc_status launch_fwd(Args p, const Cut& c, hipStream_t stream) {
-    const unsigned grid = set_grid(p, c.slots, c.splits);
+    const unsigned grid = set_grid(p, c.slots, c.splits, 32 * c.nw, !p.causal);
     if (c.nw == 4) ATTN_WIDTHS(k_attn_fwd, 4, grid, p);
     else ATTN_WIDTHS(k_attn_fwd, 1, grid, p);
     if (c.splits > 1) {
         const int splits = p.splits;
-        const unsigned rows = set_grid(p, slots_of(int64_t(p.qs.n) * p.g, p.qs.n_seg, 32), 1);
+        const unsigned rows = set_grid(p, slots_of(int64_t(p.qs.n) * p.g, p.qs.n_seg, 32), 1, 32, false);
         p.splits = splits;
         hipLaunchKernelGGL(k_attn_join<TT>, dim3(rows), dim3(256), 0, stream, p);
         SPC_LAUNCHED("k_attn_join");
@@ -937,22 +1105,22 @@ spc_status launch_fwd(Args p, const Cut& c, hipStream_t stream) {
 template <typename TT>
 spc_status launch_bwd(Args p, const Cut& cq, const Cut& ck, hipStream_t stream) {
     if (p.qs.n) {
-        unsigned grid = set_grid(p, cq.slots, cq.splits);
+        unsigned grid = set_grid(p, cq.slots, cq.splits, 32 * cq.nw, !p.causal);
         if (cq.nw == 4) ATTN_WIDTHS(k_attn_dq, 4, grid, p);
         else ATTN_WIDTHS(k_attn_dq, 1, grid, p);
         if (cq.splits > 1) {
-            grid = set_grid(p, slots_of(int64_t(p.qs.n) * p.g, p.qs.n_seg, 32), 1);
+            grid = set_grid(p, slots_of(int64_t(p.qs.n) * p.g, p.qs.n_seg, 32), 1, 32, false);
             p.splits = cq.splits;
             hipLaunchKernelGGL((k_attn_sum<TT, false>), dim3(grid), dim3(256), 0, stream, p);
             SPC_LAUNCHED("k_attn_sum");
         }
     }
     if (p.ks.n) {
-        unsigned grid = set_grid(p, ck.slots, ck.splits);
+        unsigned grid = set_grid(p, ck.slots, ck.splits, 32 * ck.nw, !p.causal);
         if (ck.nw == 4) ATTN_WIDTHS(k_attn_dkv, 4, grid, p);
         else ATTN_WIDTHS(k_attn_dkv, 1, grid, p);
         if (ck.splits > 1) {
-            grid = set_grid(p, slots_of(p.ks.n, p.ks.n_seg, 32), 1);
+            grid = set_grid(p, slots_of(p.ks.n, p.ks.n_seg, 32), 1, 32, false);
             p.splits = ck.splits;
             hipLaunchKernelGGL((k_attn_sum<TT, true>), dim3(grid), dim3(256), 0, stream, p);
             SPC_LAUNCHED("k_attn_sum");

@@ -20,7 +20,7 @@ Cut cut_of(int64_t rows, int64_t other, int64_t n_seg, int heads) {
     // rows on average, and the parts are joined by a second launch.
     const int64_t want = 2048 / c.nw, have = (rows / (32 * c.nw) + n_seg) * heads, most = other / n_seg / 256;
     c.splits = int32_t(have * 2 > want || most < 2 ? 1 : (want / have < most ? want / have : most));
-    c.blocks = c.slots * c.splits * heads;
+    c.blocks = (c.slots * c.splits + 8 * (32 / c.nw)) * heads;   // with what rounding up to groups of an XCD adds
     return c;
 }
 
@@ -47,7 +47,7 @@ spc_status check_sizes(spc_dtype dtype, const spc_attention* a, Plan& w) {
     w.q = cut_of(rows, a->n_kv, a->n_seg, a->kv_heads);
     w.k = cut_of(a->n_kv, rows, a->n_seg, a->kv_heads);
     // (a call that is split has few workgroups, so its join has too)
-    if (!launchable(w.q.blocks + 8, 64 * w.q.nw) || !launchable(w.k.blocks + 8, 64 * w.k.nw))
+    if (!launchable(w.q.blocks, 64 * w.q.nw) || !launchable(w.k.blocks, 64 * w.k.nw))
         return fail(SPC_ERR_UNSUPPORTED, "%lld samples of %lld and %lld rows exceed one launch", (long long)a->n_seg, (long long)a->n_q,
                     (long long)a->n_kv);
     const size_t hq = size_t(a->n_q) * size_t(a->heads), hk = size_t(a->n_kv) * size_t(a->kv_heads), D = size_t(a->head_dim);
@@ -75,6 +75,7 @@ spc_status check_call(spc_dtype dtype, const spc_attention* a, const void* ws, s
     p.ks = Segs{a->kv_ptr, int32_t(a->n_seg), int32_t(a->n_kv)};
     p.q_order = a->q_order, p.kv_order = a->kv_order;
     p.hk = a->kv_heads, p.g = a->heads / a->kv_heads, p.D = a->head_dim, p.causal = a->causal != 0;
+    p.inv_g = p.g > 1 ? uint32_t(((uint64_t(1) << 32) + uint64_t(p.g) - 1) / uint64_t(p.g)) : 0u;
     p.scale = a->scale, p.c = float(double(a->scale) * 1.4426950408889634);
     return SPC_OK;
 }

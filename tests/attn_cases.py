@@ -15,6 +15,16 @@ from tests.rowops_cases import half_step, ptr_of, within
 FLOOR = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
 
 
+#: Heads of up to 32 elements of a 16-bit type: scale log2(e) q is kept as hi + lo, two numbers of the
+#: type.  hi is off by up to half a step h of the product (2^-9 for bf16, 2^-11 for fp16) and lo, which is
+#: that remainder, by h of itself: h^2 of the product.  fp16's lo is off by 2^-25 at least (half its
+#: smallest number).
+def split_of(dtype, D):
+    if dtype == torch.float32 or D > 32:
+        return 0.0, 0.0
+    return half_step(dtype) ** 2, 2.0 ** -25 if dtype == torch.float16 else 0.0
+
+
 class Case:
     def __init__(self, lq, lk, H, Hk, D, dtype, seed=0, causal=False, ordered=False, gain=1.0, scale=None, outside=0):
         """lk None: the rows attend to themselves.  outside: rows of no sample, before and after."""
@@ -44,7 +54,8 @@ class Case:
         np_ = lambda t: None if t is None else t.numpy()
         return A.attention(self.q, self.k, self.v, self.q_ptr, self.kv_ptr, self.scale, self.causal, np_(self.order),
                            np_(self.kv_order), dout=self.dout if bwd else None,
-                           step=half_step(self.dtype) if self.dtype != torch.float32 else 0.0, floor=FLOOR[self.dtype])
+                           step=half_step(self.dtype) if self.dtype != torch.float32 else 0.0, floor=FLOOR[self.dtype],
+                           split=split_of(self.dtype, self.D))
 
     def kw(self):
         i32 = lambda v: cuda(torch.tensor(v, dtype=torch.int32))
