@@ -653,31 +653,61 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
     if (p.stats && h == 0) p.stats[id] = float2{m, l};
 }
 
-// Joins the splits of the forward: one thread takes four elements of a row.
+// How the joining kernels lay a workgroup of 256 threads out over rows, splits
+// (up to 8 to a thread, all in flight) and quads of elements: powers of two,
+// the quads fastest.
+struct JoinLayout {
+    int quads, splits, rows;
+    __device__ __forceinline__ JoinLayout(int q, int s) {
+        quads = splits = 1;
+        while (quads < q) quads *= 2;
+        while (splits * 8 < s && quads * splits < 256) splits *= 2;
+        rows = 256 / (quads * splits);
+    }
+};
+
+// Joins the splits of the forward: the parts of a row are read side by side
+// and added up in a tree.
 template <typename TT>
 __global__ __launch_bounds__(256) void k_attn_join(const Args p) {
     constexpr int BM = 32, ES = sizeof(typename TT::storage);
+    __shared__ __attribute__((aligned(16))) f32x4_t sum_o[256];
+    __shared__ float2 sum_ml[256];
     Job j;
     if (!job_of<BM>(p, p.qs, p.g, false, j)) return;
-    const int rows = min(j.len * p.g, j.r0 + BM), quads = p.D / 4;
+    const JoinLayout w(p.D / 4, p.splits);
+    const int tid = int(threadIdx.x), d = (tid % w.quads) * 4, s0 = tid / w.quads % w.splits, rl = tid / (w.quads * w.splits);
+    const int rows = min(j.len * p.g, j.r0 + BM);
     const int64_t step = int64_t(p.qs.n) * (int64_t(p.g) * p.hk) * (p.D + 4);
-    for (int e = int(threadIdx.x); e < (rows - j.r0) * quads; e += 256) {
-        const int rq = j.r0 + e / quads, d = (e % quads) * 4;
-        const Query q = query_of(p, j, j.a, rq, rows);
-        if (q.row < 0) continue;
+    for (int r = j.r0; r < rows; r += w.rows) {
+        const Query q = query_of(p, j, j.a, r + rl, rows);
         const int64_t id = int64_t(q.head) * p.qs.n + q.row;
-        const float* part = p.part + id * (p.D + 4);
-        float m = -INFINITY;
-        for (int s = 0; s < p.splits; ++s) m = fmaxf(m, part[s * step + p.D]);
-        const float base = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
+        float m = -INFINITY, l = 0.f;
         f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.splits; ++s) {
-            const float2 ml = *reinterpret_cast<const float2*>(part + s * step + p.D);
-            const float w = exp2_(ml.x - base);
-            l += ml.y * w;
-            if (ml.x != -INFINITY) o += *reinterpret_cast<const f32x4_t*>(part + s * step + d) * w;
+        auto add = [&](float m2, float l2, const f32x4_t& o2) {
+            const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
+            const float a = exp2_(m - base), b = exp2_(m2 - base);
+            l = l * a + l2 * b;                            // a part without keys: m = -inf, l and o are 0
+            o = o * a + o2 * b;
+            m = top;
+        };
+        if (q.row >= 0 && d < p.D)
+#pragma unroll 4
+            for (int s = s0; s < p.splits; s += w.splits) {
+                const float* part = p.part + id * (p.D + 4) + s * step;
+                const float2 ml = *reinterpret_cast<const float2*>(part + p.D);
+                add(ml.x, ml.y, *reinterpret_cast<const f32x4_t*>(part + d));
+            }
+        for (int n = w.splits / 2; n > 0; n /= 2) {
+            __syncthreads();
+            sum_o[tid] = o, sum_ml[tid] = float2{m, l};
+            __syncthreads();
+            if (s0 < n) {
+                const float2 ml = sum_ml[tid + n * w.quads];
+                add(ml.x, ml.y, sum_o[tid + n * w.quads]);
+            }
         }
+        if (s0 > 0 || q.row < 0 || d >= p.D) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         put4<TT>(p.out + int64_t(q.row) * p.ldo + (int64_t(q.head) * p.D + d) * ES, o * inv);
         if (p.stats && d == 0) p.stats[id] = float2{m, l};
@@ -1009,29 +1039,40 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
         }
 }
 
-// Sums the splits of a gradient, in their order: of dq (KEYS false), or of dk
-// and dv.
+// Sums the splits of a gradient, in a tree: of dq (KEYS false), or of dk and dv.
 template <typename TT, bool KEYS>
 __global__ __launch_bounds__(256) void k_attn_sum(const Args p) {
     constexpr int BM = 32, ES = sizeof(typename TT::storage);
+    __shared__ __attribute__((aligned(16))) f32x4_t sum[256];
     Job j;
     const int mult = KEYS ? 1 : p.g;
     if (!job_of<BM>(p, KEYS ? p.ks : p.qs, mult, false, j)) return;
-    const int rows = min(j.len * mult, j.r0 + BM), width = KEYS ? 2 * p.D : p.D, quads = width / 4;
-    for (int e = int(threadIdx.x); e < (rows - j.r0) * quads; e += 256) {
-        const int r = j.r0 + e / quads, d = (e % quads) * 4;
-        int row, head;
+    const int width = KEYS ? 2 * p.D : p.D;
+    const JoinLayout w(width / 4, p.splits);
+    const int tid = int(threadIdx.x), d = (tid % w.quads) * 4, s0 = tid / w.quads % w.splits, rl = tid / (w.quads * w.splits);
+    const int rows = min(j.len * mult, j.r0 + BM);
+    const int64_t n = KEYS ? p.ks.n : p.qs.n, heads = KEYS ? int64_t(p.hk) : int64_t(p.g) * p.hk;
+    for (int r = j.r0; r < rows; r += w.rows) {
+        int row = -1, head = j.head;
         if constexpr (KEYS) {
-            row = row_of(p.kv_order, j.a, r, p.ks.n), head = j.head;
+            if (r + rl < rows) row = row_of(p.kv_order, j.a, r + rl, p.ks.n);
         } else {
-            const Query q = query_of(p, j, j.a, r, rows);
+            const Query q = query_of(p, j, j.a, r + rl, rows);
             row = q.row, head = q.head;
         }
-        if (row < 0) continue;
-        const int64_t n = KEYS ? p.ks.n : p.qs.n, heads = KEYS ? int64_t(p.hk) : int64_t(p.g) * p.hk;
-        const float* part = p.part + (int64_t(head) * n + row) * width + d;
         f32x4_t t = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.splits; ++s) t += *reinterpret_cast<const f32x4_t*>(part + s * (n * heads * width));
+        if (row >= 0 && d < width) {
+            const float* part = p.part + (int64_t(head) * n + row) * width + d;
+#pragma unroll 8
+            for (int s = s0; s < p.splits; s += w.splits) t += *reinterpret_cast<const f32x4_t*>(part + s * (n * heads * width));
+        }
+        for (int k = w.splits / 2; k > 0; k /= 2) {
+            __syncthreads();
+            sum[tid] = t;
+            __syncthreads();
+            if (s0 < k) t += sum[tid + k * w.quads];
+        }
+        if (s0 > 0 || row < 0 || d >= width) continue;
         if constexpr (KEYS) {
             if (d < p.D) put4<TT>(p.dk + int64_t(row) * p.lddk + (int64_t(head) * p.D + d) * ES, t * p.scale);
             else put4<TT>(p.dv + int64_t(row) * p.lddv + (int64_t(head) * p.D + d - p.D) * ES, t);
@@ -1082,6 +1123,7 @@ inline unsigned set_grid(Args& p, int64_t slots, int splits, int rows_of_slot, b
         const bool split = TT::id != SPC_F16 || p.c <= 1.f;                                                                   \
         if (p.D <= 16 && split) ATTN_WIDTH(name, 16, nw, grid, p);                                                            \
         else if (p.D <= 32 && split) ATTN_WIDTH(name, 32, nw, grid, p);                                                       \
+        else if (TT::E == 4 && p.D <= 48) ATTN_WIDTH(name, (TT::E == 4 ? 48 : 64), nw, grid, p);                              \
         else if (p.D <= 64) ATTN_WIDTH(name, 64, nw, grid, p);                                                                \
         else ATTN_WIDTH(name, 128, nw, grid, p);                                                                              \
         SPC_LAUNCHED(#name);                                                                                                  \
