@@ -170,6 +170,15 @@ def _stream(dev: torch.device):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+def _call(dev: torch.device, f, *args) -> int:
+    """f(*args, stream) on the current stream of `dev`, which need not be the
+    current device."""
+    if dev.index == torch.cuda.current_device():
+        return f(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return f(*args, _stream(dev))
+
+
 def _need(t: torch.Tensor, name: str, dtype=None, dev=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
@@ -1036,8 +1045,8 @@ def layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: 
     else:
         _need_like(out, "out", x.dtype, dev, x.shape)
     stats = x.new_empty((n, 2), dtype=torch.float32)
-    st = lib().spc_layer_norm_fwd(_DTYPES[x.dtype], _ptr(x), _ptr(residual), n, C, _ptr(gamma), _ptr(beta), eps, _ptr(out),
-                                  _ptr(total), _ptr(stats), _stream(dev))
+    st = _call(dev, lib().spc_layer_norm_fwd, _DTYPES[x.dtype], _ptr(x), _ptr(residual), n, C, _ptr(gamma), _ptr(beta), eps, _ptr(out),
+                                  _ptr(total), _ptr(stats))
     _check(st, "spc_layer_norm_fwd")
     return out, stats, total
 
@@ -1065,9 +1074,8 @@ def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Te
     if want_affine:
         dgamma, dbeta = x.new_empty((C,), dtype=torch.float32), x.new_empty((C,), dtype=torch.float32)
     workspace = _scratch(workspace, layer_norm_workspace(n, C) if want_affine else 0, x)
-    st = lib().spc_layer_norm_bwd(_DTYPES[x.dtype], _ptr(dout), _ptr(x), n, C, _ptr(gamma), _ptr(stats), _ptr(dtotal), _ptr(dx),
-                                  _ptr(dgamma), _ptr(dbeta), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                  _stream(dev))
+    st = _call(dev, lib().spc_layer_norm_bwd, _DTYPES[x.dtype], _ptr(dout), _ptr(x), n, C, _ptr(gamma), _ptr(stats), _ptr(dtotal), _ptr(dx),
+                                  _ptr(dgamma), _ptr(dbeta), _ptr(workspace), 0 if workspace is None else workspace.numel())
     _check(st, "spc_layer_norm_bwd")
     return dx, dgamma, dbeta
 
@@ -1123,8 +1131,8 @@ def rotary(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, pairs: Sequen
     elif out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
         raise ValueError("out may be x itself, not another view of it")
     ldo = _heads(out, "out", x.dtype, dev, x.shape)
-    st = lib().spc_rotary(_DTYPES[x.dtype], _ptr(x), ldx, n, H, D, _ptr(pos), pos.stride(0) if n > 1 else len(pairs),
-                          len(pairs), _axis_pairs(pairs), _ptr(freq), 1 if inverse else 0, _ptr(out), ldo, _stream(dev))
+    st = _call(dev, lib().spc_rotary, _DTYPES[x.dtype], _ptr(x), ldx, n, H, D, _ptr(pos), pos.stride(0) if n > 1 else len(pairs),
+                          len(pairs), _axis_pairs(pairs), _ptr(freq), 1 if inverse else 0, _ptr(out), ldo)
     _check(st, "spc_rotary")
     return out
 
@@ -1185,8 +1193,8 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg_ptr: Op
     ldo = _heads(out, "out", q.dtype, dev, q.shape)
     stats = q.new_empty((H, n, 2), dtype=torch.float32) if want_stats else None
     workspace = _scratch(workspace, need, q)
-    st = lib().spc_attention_fwd(_DTYPES[q.dtype], ctypes.byref(a), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(out), ldo,
-                                 _ptr(stats), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev))
+    st = _call(dev, lib().spc_attention_fwd, _DTYPES[q.dtype], ctypes.byref(a), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(out), ldo,
+                                 _ptr(stats), _ptr(workspace), 0 if workspace is None else workspace.numel())
     _check(st, "spc_attention_fwd")
     return out, stats
 
@@ -1208,9 +1216,9 @@ def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     dv = v.new_empty(v.shape) if dv is None else dv
     lddq, lddk, lddv = (_heads(t, nm, q.dtype, dev, like.shape) for t, nm, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
     workspace = _scratch(workspace, need, q)
-    st = lib().spc_attention_bwd(_DTYPES[q.dtype], ctypes.byref(a), _ptr(dout), lddo, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
+    st = _call(dev, lib().spc_attention_bwd, _DTYPES[q.dtype], ctypes.byref(a), _ptr(dout), lddo, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
                                  _ptr(out), ldo, _ptr(stats), _ptr(dq), lddq, _ptr(dk), lddk, _ptr(dv), lddv, _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), _stream(dev))
+                                 0 if workspace is None else workspace.numel())
     _check(st, "spc_attention_bwd")
     return dq, dk, dv
 

@@ -10,20 +10,20 @@ constexpr int D_MAX = 128;
 
 // Rows of one side that work is cut over (positions times the heads that share
 // them), and the other side's.
-Cut cut_of(spc_dtype dtype, int64_t rows, int64_t other, int64_t n_seg, int heads) {
+Cut cut_of(int64_t rows, int64_t other, int64_t n_seg, int heads) {
     Cut c;
     // Four waves share the staged tiles where samples have rows for them and
     // the call fills the chip; else single waves, which leave fewer lanes idle.
     c.nw = rows >= 64 * n_seg && slots_of(rows, n_seg, 128) * heads >= 512 ? 4 : 1;
     c.slots = slots_of(rows, n_seg, 32 * c.nw);
     // Few workgroups: the other side is split too, and the parts are joined by
-    // a second launch.  A split is worth at least `unit` rows of the longest
-    // sample, which may be several times the mean (only the device knows); samples of
-    // fewer than 128 rows in the mean are not split.  fp32 tiles take eight
-    // times as long in the matrix unit, so their calls are cut finer.
-    const bool wide = dtype == SPC_F32;
-    const int64_t want = (wide ? 4096 : 2048) / c.nw, unit = wide ? 128 : 256, have = (rows / (32 * c.nw) + n_seg) * heads;
-    const int64_t mean = other / n_seg, longest = mean < 128 ? 0 : 8 * mean < other ? 8 * mean : other, most = longest / unit;
+    // a second launch, to 4 waves a SIMD (5,003 x 6 x 48 fp32 in 23 ragged samples,
+    // trained: 556 us, 1,560 when only the mean length counted).  A split is
+    // worth at least 128 rows of the longest sample, which may be several
+    // times the mean (only the device knows); samples of fewer than 128 rows
+    // in the mean are not split.
+    const int64_t want = 4096 / c.nw, have = (rows / (32 * c.nw) + n_seg) * heads;
+    const int64_t mean = other / n_seg, longest = mean < 128 ? 0 : 8 * mean < other ? 8 * mean : other, most = longest / 128;
     c.splits = int32_t(have * 2 > want || most < 2 ? 1 : (want / have < most ? want / have : most));
     c.blocks = (c.slots * c.splits + 8 * (32 / c.nw)) * heads;   // with what rounding up to groups of an XCD adds
     return c;
@@ -49,8 +49,8 @@ spc_status check_sizes(spc_dtype dtype, const spc_attention* a, Plan& w) {
         return fail(SPC_ERR_UNSUPPORTED, "rows x heads exceed 31 bits");
     if (!(a->scale > 0.f && a->scale <= 3.402823466e38f)) return fail(SPC_ERR_ARG, "scale=%g must be positive and finite", double(a->scale));
     const int64_t rows = a->n_q * (a->heads / a->kv_heads);
-    w.q = cut_of(dtype, rows, a->n_kv, a->n_seg, a->kv_heads);
-    w.k = cut_of(dtype, a->n_kv, rows, a->n_seg, a->kv_heads);
+    w.q = cut_of(rows, a->n_kv, a->n_seg, a->kv_heads);
+    w.k = cut_of(a->n_kv, rows, a->n_seg, a->kv_heads);
     // (a call that is split has few workgroups, so its join has too)
     if (!launchable(w.q.blocks, 64 * w.q.nw) || !launchable(w.k.blocks, 64 * w.k.nw))
         return fail(SPC_ERR_UNSUPPORTED, "%lld samples of %lld and %lld rows exceed one launch", (long long)a->n_seg, (long long)a->n_q,

@@ -17,25 +17,54 @@ namespace {
 constexpr int LT = 256;          // threads per workgroup
 constexpr int LN_C_MAX = 4096;   // channels that one wave holds: 8 steps of 512
 
-// Sums of K values over the lanes of a row (lanes a power of two, aligned).
+// v of the lane that differs from this one by a step of the row's sum: within
+// 16 lanes by lane moves of the vector unit (once the quads' lanes agree, any
+// lane of the other quad serves), above by swaps of 16 and 32 lanes; no LDS.
+template <int M>
+__device__ __forceinline__ float other(float v) {
+    const int i = __float_as_int(v);
+    if constexpr (M == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0xB1, 0xf, 0xf, true));        // 1 0 3 2
+    else if constexpr (M == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x4E, 0xf, 0xf, true));   // 2 3 0 1
+    else if constexpr (M == 4) return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x141, 0xf, 0xf, true));  // mirror of 8
+    else return __int_as_float(__builtin_amdgcn_mov_dpp(i, 0x140, 0xf, 0xf, true));                        // mirror of 16
+}
+__device__ __forceinline__ float sum_rows16(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_rows32(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Sums of K values over the lanes of a row (lanes a power of two from 2 on, aligned).
 template <int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], int lanes) {
-    for (int m = 1; m < lanes; m <<= 1) {
-        float t[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) t[k] = __shfl_xor(v[k], m);
+    for (int k = 0; k < K; ++k) v[k] += other<1>(v[k]);
+    if (lanes < 4) return;
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += t[k];
-    }
+    for (int k = 0; k < K; ++k) v[k] += other<2>(v[k]);
+    if (lanes < 8) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += other<4>(v[k]);
+    if (lanes < 16) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += other<8>(v[k]);
+    if (lanes < 32) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = sum_rows16(v[k]);
+    if (lanes < 64) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = sum_rows32(v[k]);
 }
 
 __device__ __forceinline__ float sum8(const f32x8_t& v) { return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])); }
 
 __device__ __forceinline__ f32x8_t ldf8(const float* p) { return widen<F32>(ld8<F32>(p)); }
 
-// V steps of 512 channels (lanes = 64), or one step of `lanes` lanes; R rows of
-// a thread in flight.
-template <typename TT, int V, int R, bool RES>
+// V steps of 512 channels (lanes = 64), or one step of `lanes` lanes.
+template <typename TT, int V, bool RES>
 __global__ __launch_bounds__(LT) void k_ln_fwd(const void* x_, const void* res_, int64_t n, int C, int lanes, float inv_c,
                                                const float* gamma, const float* beta, float eps, void* y_, void* total_,
                                                float2* stats) {
@@ -43,60 +72,51 @@ __global__ __launch_bounds__(LT) void k_ln_fwd(const void* x_, const void* res_,
     const S *x = static_cast<const S*>(x_), *res = static_cast<const S*>(res_);
     S *y = static_cast<S*>(y_), *total = static_cast<S*>(total_);
     const int rl = int(threadIdx.x) / lanes, c0 = (int(threadIdx.x) % lanes) * 8, per = LT / lanes;
-    const int64_t row0 = int64_t(blockIdx.x) * (per * R) + rl;
-    f32x8_t u[R][V];
+    const int64_t r = int64_t(blockIdx.x) * per + rl;
+    f32x8_t u[V];
+    float s[1] = {0.f};
 #pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t r = row0 + k * per;
-            const int c = c0 + 512 * v;
-            if (r < n && c < C) {
-                u[k][v] = widen<TT>(ld8<TT>(x + r * C + c));
-                if constexpr (RES) {
-                    const Raw8<TT> t = narrow<TT>(u[k][v] + widen<TT>(ld8<TT>(res + r * C + c)));
-                    st8<TT>(total + r * C + c, t);
-                    u[k][v] = widen<TT>(t);      // the sum as it is stored, so that the backward sees the same
-                }
-            } else {
-                u[k][v] = 0.f;
+    for (int v = 0; v < V; ++v) {
+        const int c = c0 + 512 * v;
+        u[v] = 0.f;
+        if (r < n && c < C) {
+            u[v] = widen<TT>(ld8<TT>(x + r * C + c));
+            if constexpr (RES) {
+                const Raw8<TT> t = narrow<TT>(u[v] + widen<TT>(ld8<TT>(res + r * C + c)));
+                st8<TT>(total + r * C + c, t);
+                u[v] = widen<TT>(t);      // the sum as it is stored, so that the backward sees the same
             }
         }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const int64_t r = row0 + k * per;
-        float s[1] = {0.f};
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[0] += sum8(u[k][v]);
-        row_sums(s, lanes);
-        const float mean = s[0] * inv_c;
-        float q[2] = {0.f, 0.f};
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (c0 + 512 * v < C) u[k][v] -= mean;
-            q[0] += sum8(u[k][v]);
-            q[1] += sum8(u[k][v] * u[k][v]);
-        }
-        row_sums(q, lanes);
-        const float md = q[0] * inv_c, rstd = rsqrtf(fmaxf(fmaf(-md, md, q[1] * inv_c), 0.f) + eps);
-        if (r >= n) continue;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = c0 + 512 * v;
-            if (c >= C) continue;
-            f32x8_t h = (u[k][v] - md) * rstd;
-            if (gamma) h *= ldf8(gamma + c);
-            if (beta) h += ldf8(beta + c);
-            st8<TT>(y + r * C + c, narrow<TT>(h));
-        }
-        if (c0 == 0) stats[r] = float2{mean + md, rstd};
+        s[0] += sum8(u[v]);
     }
+    row_sums(s, lanes);
+    const float mean = s[0] * inv_c;
+    float q[2] = {0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (c0 + 512 * v < C) u[v] -= mean;
+        q[0] += sum8(u[v]);
+        q[1] += sum8(u[v] * u[v]);
+    }
+    row_sums(q, lanes);
+    const float md = q[0] * inv_c, rstd = rsqrtf(fmaxf(fmaf(-md, md, q[1] * inv_c), 0.f) + eps);
+    if (r >= n) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = c0 + 512 * v;
+        if (c >= C) continue;
+        f32x8_t h = (u[v] - md) * rstd;
+        if (gamma) h *= ldf8(gamma + c);
+        if (beta) h += ldf8(beta + c);
+        st8<TT>(y + r * C + c, narrow<TT>(h));
+    }
+    if (c0 == 0) stats[r] = float2{mean + md, rstd};
 }
 
 // A workgroup takes `iters` (at most 16) rows of each of its row groups, keeps
 // its channels' two sums in fp32 over them, and adds up the groups in double:
 // part[workgroup][C] (dgamma, dbeta), or the results where there is one.
-template <typename TT, int V, bool AFFINE>
+template <typename TT, int V, bool AFFINE, bool JOIN>
 __global__ __launch_bounds__(LT) void k_ln_bwd(const void* dy_, const void* x_, int64_t n, int C, int lanes, int iters, float inv_c,
                                                const float* gamma, const float2* stats, const void* dtotal_, void* dx_,
                                                float2* part, float* dgamma, float* dbeta) {
@@ -108,22 +128,38 @@ __global__ __launch_bounds__(LT) void k_ln_bwd(const void* dy_, const void* x_, 
     f32x8_t sg[V], sb[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) sg[v] = 0.f, sb[v] = 0.f;
+    // One round's rows as stored; the next round's are in flight while one is
+    // worked on (up to 1,024 channels: above, the registers hold one).
+    constexpr bool TWO = V <= 2;
+    Raw8<TT> xs[V], gs[V], ts[V];
+    float2 st;
+    auto row = [&](int it) { return (int64_t(blockIdx.x) * iters + it) * per + rl; };
+    auto load = [&](int it) {
+        const int64_t r = row(it) < n ? row(it) : n - 1;
+        st = stats[r];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = c0 + 512 * v < C ? c0 + 512 * v : 0;
+            xs[v] = ld8<TT>(x + r * C + c);
+            gs[v] = ld8<TT>(dy + r * C + c);
+            if constexpr (JOIN) ts[v] = ld8<TT>(dtotal + r * C + c);
+        }
+    };
+    if (TWO) load(0);
     for (int it = 0; it < iters; ++it) {
-        const int64_t r = (int64_t(blockIdx.x) * iters + it) * per + rl;
-        const bool in = r < n;
-        const float2 st = in ? stats[r] : float2{0.f, 0.f};
-        f32x8_t d[V], g[V];
+        const int64_t r = row(it);
+        if (!TWO) load(it);
+        f32x8_t d[V], g[V], t[JOIN ? V : 1];
+        const float rstd = st.y;
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = c0 + 512 * v;
-            if (in && c < C) {
-                d[v] = widen<TT>(ld8<TT>(x + r * C + c)) - st.x;
-                g[v] = widen<TT>(ld8<TT>(dy + r * C + c));
-            } else {
-                d[v] = 0.f, g[v] = 0.f;
-            }
+            const bool in = c0 + 512 * v < C;
+            d[v] = in ? widen<TT>(xs[v]) - st.x : f32x8_t(0.f);
+            g[v] = in ? widen<TT>(gs[v]) : f32x8_t(0.f);
+            if constexpr (JOIN) t[v] = widen<TT>(ts[v]);
         }
+        if (TWO && it + 1 < iters) load(it + 1);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             f32x8_t w = g[v];
@@ -133,16 +169,16 @@ __global__ __launch_bounds__(LT) void k_ln_bwd(const void* dy_, const void* x_, 
             s[2] += sum8(w * d[v]);
         }
         row_sums(s, lanes);
-        const float md = s[0] * inv_c, m1 = s[1] * inv_c, m2 = st.y * fmaf(-md, s[1], s[2]) * inv_c;
+        const float md = s[0] * inv_c, m1 = s[1] * inv_c, m2 = rstd * fmaf(-md, s[1], s[2]) * inv_c;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = c0 + 512 * v;
-            if (!in || c >= C) continue;
-            const f32x8_t h = (d[v] - md) * st.y;
+            if (r >= n || c >= C) continue;
+            const f32x8_t h = (d[v] - md) * rstd;
             f32x8_t w = g[v];
             if (gamma) w *= ldf8(gamma + c);
-            w = (w - m1 - h * m2) * st.y;
-            if (dtotal) w += widen<TT>(ld8<TT>(dtotal + r * C + c));
+            w = (w - m1 - h * m2) * rstd;
+            if constexpr (JOIN) w += t[v];
             st8<TT>(dx + r * C + c, narrow<TT>(w));
             if constexpr (AFFINE) sg[v] += g[v] * h, sb[v] += g[v];
         }
@@ -176,6 +212,7 @@ __global__ __launch_bounds__(LT) void k_ln_sums(const float2* part, int64_t part
     __shared__ double2 lds[LT];
     const int e = int(threadIdx.x) & 3, c = int(blockIdx.x) * 4 + e;
     double a = 0.0, b = 0.0;
+#pragma unroll 8
     for (int64_t k = threadIdx.x >> 2; k < parts; k += LT / 4) {
         const float2 t = part[k * C + c];
         a += t.x, b += t.y;
@@ -205,7 +242,8 @@ spc_status check_sizes(int64_t n, int32_t C, LnCut& k) {
     k.lanes = 2;
     while (k.lanes < 64 && k.lanes * 8 < C) k.lanes *= 2;
     k.per = LT / k.lanes;
-    const int64_t want = ceil_div(n, int64_t(k.per) * 512);
+    // rounds for about 1,024 workgroups: fewer rounds cost parts to add up, more leave compute units idle
+    const int64_t want = ceil_div(n, int64_t(k.per) * 1024);
     k.iters = int(want < 1 ? 1 : want > 16 ? 16 : want);
     k.parts = ceil_div(n, int64_t(k.per) * k.iters);
     k.bytes = k.parts > 1 ? size_t(k.parts) * size_t(C) * 8 : 0;
@@ -214,13 +252,13 @@ spc_status check_sizes(int64_t n, int32_t C, LnCut& k) {
     return SPC_OK;
 }
 
-template <typename TT, int V, int R>
+template <typename TT, int V>
 spc_status launch_fwd(const void* x, const void* res, int64_t n, int C, const LnCut& k, const float* gamma, const float* beta,
                       float eps, void* y, void* total, float2* stats, hipStream_t stream) {
-    const dim3 grid(unsigned(ceil_div(n, int64_t(k.per) * R)));
+    const dim3 grid(unsigned(ceil_div(n, k.per)));
     const float inv = 1.f / float(C);
-    if (res) hipLaunchKernelGGL((k_ln_fwd<TT, V, R, true>), grid, dim3(LT), 0, stream, x, res, n, C, k.lanes, inv, gamma, beta, eps, y, total, stats);
-    else hipLaunchKernelGGL((k_ln_fwd<TT, V, R, false>), grid, dim3(LT), 0, stream, x, res, n, C, k.lanes, inv, gamma, beta, eps, y, total, stats);
+    if (res) hipLaunchKernelGGL((k_ln_fwd<TT, V, true>), grid, dim3(LT), 0, stream, x, res, n, C, k.lanes, inv, gamma, beta, eps, y, total, stats);
+    else hipLaunchKernelGGL((k_ln_fwd<TT, V, false>), grid, dim3(LT), 0, stream, x, res, n, C, k.lanes, inv, gamma, beta, eps, y, total, stats);
     SPC_LAUNCHED("k_ln_fwd");
     return SPC_OK;
 }
@@ -228,10 +266,10 @@ spc_status launch_fwd(const void* x, const void* res, int64_t n, int C, const Ln
 template <typename TT>
 spc_status dispatch_fwd(const void* x, const void* res, int64_t n, int C, const LnCut& k, const float* gamma, const float* beta,
                         float eps, void* y, void* total, float2* stats, hipStream_t stream) {
-    if (C <= 512) return launch_fwd<TT, 1, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
-    if (C <= 1024) return launch_fwd<TT, 2, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
-    if (C <= 2048) return launch_fwd<TT, 4, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
-    return launch_fwd<TT, 8, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+    if (C <= 512) return launch_fwd<TT, 1>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+    if (C <= 1024) return launch_fwd<TT, 2>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+    if (C <= 2048) return launch_fwd<TT, 4>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
+    return launch_fwd<TT, 8>(x, res, n, C, k, gamma, beta, eps, y, total, stats, stream);
 }
 
 template <typename TT, int V>
@@ -240,15 +278,19 @@ spc_status launch_bwd(const void* dy, const void* x, int64_t n, int C, const LnC
     const dim3 grid(unsigned(k.parts));
     const float inv = 1.f / float(C);
     if (k.parts <= 1) part = nullptr;
-    if (!dgamma && !dbeta) {
-        hipLaunchKernelGGL((k_ln_bwd<TT, V, false>), grid, dim3(LT), 0, stream, dy, x, n, C, k.lanes, k.iters, inv, gamma, stats, dtotal, dx, part, dgamma, dbeta);
-        SPC_LAUNCHED("k_ln_bwd");
-        return SPC_OK;
-    }
+#define LN_BWD(AFFINE, JOIN)                                                                                              \
+    hipLaunchKernelGGL((k_ln_bwd<TT, V, AFFINE, JOIN>), grid, dim3(LT), 0, stream, dy, x, n, C, k.lanes, k.iters, inv, gamma, \
+                       stats, dtotal, dx, part, dgamma, dbeta)
+    const bool affine = dgamma || dbeta;
     if (k.parts) {
-        hipLaunchKernelGGL((k_ln_bwd<TT, V, true>), grid, dim3(LT), 0, stream, dy, x, n, C, k.lanes, k.iters, inv, gamma, stats, dtotal, dx, part, dgamma, dbeta);
+        if (affine && dtotal) LN_BWD(true, true);
+        else if (affine) LN_BWD(true, false);
+        else if (dtotal) LN_BWD(false, true);
+        else LN_BWD(false, false);
         SPC_LAUNCHED("k_ln_bwd");
     }
+#undef LN_BWD
+    if (!affine) return SPC_OK;
     if (k.parts != 1) {
         hipLaunchKernelGGL(k_ln_sums, dim3(unsigned(C / 4)), dim3(LT), 0, stream, part, k.parts, C, dgamma, dbeta);
         SPC_LAUNCHED("k_ln_sums");

@@ -55,19 +55,34 @@ __global__ __launch_bounds__(RT) void k_rotary(const RotArgs p) {
         table[e] = cs;
     }
     __syncthreads();
-    const int width = p.heads * (p.D / 8), chunks = rows * width;
-    for (int e = int(threadIdx.x); e < chunks; e += RT) {
-        const int r = e / width, c = e - r * width, i = c % (p.D / 8);
-        f32x8_t v = widen<TT>(ld8<TT>(p.x + (row0 + r) * p.ldx + int64_t(c) * 8 * ES));
-        const float2* t = table + r * half + i * 4;
+    // four chunks of a thread in flight
+    const int per = p.D / 8, width = p.heads * per, chunks = rows * width;
+    for (int e0 = int(threadIdx.x); e0 < chunks; e0 += 4 * RT) {
+        Raw8<TT> x[4];
+        int at[4];
+        int64_t to[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float2 cs = t[k];
-            const float a = v[2 * k], b = v[2 * k + 1];
-            v[2 * k] = fmaf(a, cs.x, -(b * cs.y));
-            v[2 * k + 1] = fmaf(a, cs.y, b * cs.x);
+            const int e = e0 + k * RT < chunks ? e0 + k * RT : e0;
+            const int r = e / width, c = e - r * width;
+            at[k] = r * half + (c % per) * 4;
+            to[k] = (row0 + r) * p.ldo + int64_t(c) * 8 * ES;
+            x[k] = ld8<TT>(p.x + (row0 + r) * p.ldx + int64_t(c) * 8 * ES);
         }
-        st8<TT>(p.out + (row0 + r) * p.ldo + int64_t(c) * 8 * ES, narrow<TT>(v));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (e0 + k * RT >= chunks) continue;
+            f32x8_t v = widen<TT>(x[k]);
+            const float2* t = table + at[k];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 cs = t[i];
+                const float a = v[2 * i], b = v[2 * i + 1];
+                v[2 * i] = fmaf(a, cs.x, -(b * cs.y));
+                v[2 * i + 1] = fmaf(a, cs.y, b * cs.x);
+            }
+            st8<TT>(p.out + to[k], narrow<TT>(v));
+        }
     }
 }
 

@@ -128,3 +128,27 @@ def test_binding_refuses_cpu_tensors():
               lambda: spc.attention_fwd(h, h, h), lambda: spc.attention_bwd(h, h, h, h, h, x)):
         with pytest.raises(TypeError):
             f()
+
+
+def test_calls_go_to_their_tensors_device(monkeypatch):
+    """A call on tensors of another device than the current one makes that
+    device current for the launch, and only then."""
+    log = []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            log.append(("in", self.dev.index))
+
+        def __exit__(self, *a):
+            log.append(("out", self.dev.index))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(B, "_stream", lambda dev: ("stream", dev.index))
+    f = lambda *a: log.append(a) or 0
+    assert B._call(torch.device("cuda", 0), f, 1, 2) == 0 and log == [(1, 2, ("stream", 0))]
+    log.clear()
+    assert B._call(torch.device("cuda", 1), f, 3) == 0
+    assert log == [("in", 1), (3, ("stream", 1)), ("out", 1)]
