@@ -480,7 +480,8 @@ template <typename TT, int NW>
 constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
 
 // Waves that a SIMD is to hold at least, which bounds the registers: the most
-// that costs no spills in the loops.
+// that costs no spills in the loops (heads of 128 masked as causal spill a
+// few: 16,411 x 8 x 128 takes 819 us so, 985 with one wave and none).
 template <typename TT, int DP, bool CAUSAL>
 constexpr int FWD_WAVES = TT::E == 4 ? 1 : DP <= 32 ? 4 - CAUSAL : DP <= 64 ? 3 - CAUSAL : 2;
 template <typename TT, int DP>
@@ -885,50 +886,43 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
 
     const bool in_place = p.g == 1 && !p.q_order;
     S stage;
-    int at[S::PT], mark = 0;
-    uint64_t live = 0;
+    int mark = 0, row = -1;        // of this lane's row of the tile: its order entry, its row
+    uint64_t live = 0;             // rows of the fetched tile that are there, as bits
     float2 own_ml = {0.f, 0.f};
     float own_d = 0.f;
-    bool own = false;
     auto find = [&](int t) {
-        if (!p.q_order) return;
-        const int32_t* o = p.q_order + qa;
-        mark = o[min(place_of(p, j, t * BN + lane).pos, lq - 1)];
-#pragma unroll
-        for (int i = 0; i < S::PT; ++i) at[i] = o[min(place_of(p, j, t * BN + S::row(i)).pos, lq - 1)];
+        if (p.q_order) mark = p.q_order[qa + min(place_of(p, j, t * BN + lane).pos, lq - 1)];
     };
     auto fetch = [&](int t) {
         const int cnt = rows - t * BN;
+        const Query q = place_of(p, j, t * BN + lane);
+        const int w = p.q_order ? mark : qa + q.pos;
+        row = lane < BN && lane < cnt && unsigned(w) < unsigned(p.qs.n) ? w : -1;
+        live = __ballot(row >= 0);
         if (in_place) {
-            const int64_t row = qa + t * BN;
-            stage.load(p.q + row * p.ldq + in, p.ldq, p.dout + row * p.lddo + in, p.lddo, cnt, p.D * T::ES);
-        } else {
+            const int64_t at = qa + t * BN;
+            stage.load(p.q + at * p.ldq + in, p.ldq, p.dout + at * p.lddo + in, p.lddo, cnt, p.D * T::ES);
+        } else {                   // every row's place from the lane that has it
             stage.begin_parts();
 #pragma unroll
             for (int i = 0; i < S::PT; ++i) {
-                const Query q = place_of(p, j, t * BN + S::row(i));
-                const int w = p.q_order ? at[i] : qa + q.pos;
-                const bool is = S::row(i) < cnt && unsigned(w) < unsigned(p.qs.n);
-                const int64_t r = is ? w : 0, o = is ? int64_t(q.head) * p.D * T::ES : 0;
-                stage.load_part(i, is, p.q + r * p.ldq + o, p.dout + r * p.lddo + o, p.D * T::ES);
+                const int e = S::mine(i) ? S::row(i) : 0, r = __shfl(row, e), hd = p.g > 1 ? __shfl(q.head, e) : j.head;
+                const int64_t at = r < 0 ? 0 : r, o = int64_t(hd) * p.D * T::ES;
+                stage.load_part(i, r >= 0, p.q + at * p.ldq + o, p.dout + at * p.lddo + o, p.D * T::ES);
             }
         }
-        const Query q = place_of(p, j, t * BN + lane);
-        const int w = p.q_order ? mark : qa + q.pos;
-        own = lane < BN && lane < cnt && unsigned(w) < unsigned(p.qs.n);
-        live = __ballot(own);
         if (wave == 0) {
-            const int64_t id = own ? int64_t(q.head) * p.qs.n + w : 0;
+            const int64_t id = row < 0 ? 0 : int64_t(q.head) * p.qs.n + row;
             own_ml = p.stats[id], own_d = p.delta[id];
         }
     };
     auto put = [&](int buf) {
         stage.put(lds[buf][0], lds[buf][1]);
         if (int(threadIdx.x) < BN) {
-            const float2 mf = from_stats<TT>(own ? own_ml : float2{0.f, 0.f});
+            const float2 mf = from_stats<TT>(row >= 0 ? own_ml : float2{0.f, 0.f});
             row_m[buf][threadIdx.x] = mf.x;
             if constexpr (TT::E == 4) row_f[buf][threadIdx.x] = mf.y;
-            row_d[buf][threadIdx.x] = own ? -own_d : 0.f;
+            row_d[buf][threadIdx.x] = row >= 0 ? -own_d : 0.f;
         }
     };
 

@@ -111,7 +111,9 @@ def test_attention_limits():
     f_, b_ = ctypes.c_size_t(), ctypes.c_size_t()
     f = lambda **kw: B.lib().spc_attention_workspace(2, ctypes.byref(attn(**dict(dict(H=1, Hk=1), **kw))), ctypes.byref(f_),
                                                      ctypes.byref(b_))
-    assert f(n_q=END - 1) == f(n_kv=END - 1) == f(S=(1 << 26) - 64, n_q=0, n_kv=0) == B.SPC_OK
+    few = (1 << 31) - (1 << 14)
+    assert f(n_q=few) == f(n_kv=few) == f(S=(1 << 26) - 512, n_q=0, n_kv=0) == B.SPC_OK
+    assert f(n_q=END - 1) == f(n_kv=END - 1) == B.SPC_ERR_UNSUPPORTED  # 2^24 groups of 128 rows, 256 threads each
     assert f(S=1 << 26, n_q=0, n_kv=0) == B.SPC_ERR_UNSUPPORTED        # a wave for each: 2^32 threads
     assert f(S=1 << 24, n_q=END - 1) == B.SPC_ERR_UNSUPPORTED
     assert f(n_q=1 << 20, H=1 << 11, Hk=1 << 11, D=16) == B.SPC_ERR_UNSUPPORTED   # rows x heads
