@@ -652,25 +652,34 @@ spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size
  * rounded to the dtype for the second product, their sum is not.
  * stats fp32 [heads, n_q, 2] (NULL ok) receives (m, l) for the backward: the
  * log of the row's sum of exp(s) is (m + log2 l) ln 2; l = 0: no key is seen.
- * Rows of no sample are written neither in out nor in stats.
+ * rest (NULL ok; 16-bit dtypes, unused for fp32), dense [n_q, heads, head_dim]
+ * of the dtype, receives what the rounding to out left of the result, for the
+ * backward.
+ * Where head_dim <= 32, 16-bit dtypes multiply scale log2(e) into one factor
+ * of s, kept as two numbers of the type: s is off by up to 2^-18 (bf16) or
+ * 2^-22 (fp16) of scale sum_d |q_id k_jd|.  A NaN or infinity in a row that is
+ * seen may make everything NaN that depends on it.
+ * Rows of no sample are written in none of the outputs.
  */
 spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a, const void* q, int64_t ldq, const void* k,
-                             int64_t ldk, const void* v, int64_t ldv, void* out, int64_t ldo, float* stats, void* ws,
-                             size_t ws_bytes, hipStream_t stream);
+                             int64_t ldk, const void* v, int64_t ldv, void* out, int64_t ldo, float* stats, void* rest,
+                             void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
- * Backward of the forward of the same arguments, from its out and stats; the
- * probabilities are computed again:
+ * Backward of the forward of the same arguments, from its out, stats and rest;
+ * the probabilities are computed again:
  *   dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - dout_i . out_i),
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
  * with the sums of dk and dv over all heads that share a key head.  p and ds
- * are rounded to the dtype for their products.  dq, dk, dv overlap no input.
+ * are rounded to the dtype for their products.  rest NULL: dout . out is that
+ * of the rounded out, and where one key outweighs the others ds loses the
+ * precision that the difference cancels.  dq, dk, dv overlap no input.
  * Rows of no sample are not written.
  */
 spc_status spc_attention_bwd(spc_dtype dtype, const spc_attention* a, const void* dout, int64_t lddo, const void* q,
                              int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, const void* out,
-                             int64_t ldo, const float* stats, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv,
-                             int64_t lddv, void* ws, size_t ws_bytes, hipStream_t stream);
+                             int64_t ldo, const float* stats, const void* rest, void* dq, int64_t lddq, void* dk,
+                             int64_t lddk, void* dv, int64_t lddv, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * Measurement support (not part of the convolution): the dense MFMA rate of

@@ -156,7 +156,7 @@ def attention(q, k, v, q_ptr, kv_ptr, scale, causal=False, q_order=None, kv_orde
             dp = np.where(see, G @ V.T, 0.0)
             delta = (G * o).sum(1, keepdims=True)
             ds = p * (dp - delta)
-            eout = eo + step * (np.abs(o) + eo)                        # the forward's out is rounded to the type
+            eout = eo + step * step * (np.abs(o) + eo) + floor         # out in two numbers of the type
             edelta = (np.abs(G) * eout).sum(1, keepdims=True) + (D + 4) * EPS * (np.abs(G) * np.abs(o)).sum(1, keepdims=True)
             edp = (D + 4) * EPS * (np.abs(G) @ aV.T)
             # p from the saved m and l: the errors of both, and of their sum's rounding

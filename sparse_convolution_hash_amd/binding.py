@@ -133,9 +133,9 @@ def lib() -> ctypes.CDLL:
         "spc_layer_norm_bwd": [_I32, _P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
         "spc_rotary": [_I32, _P, _I64, _I64, _I32, _I32, _P, _I64, _I32, _P, _P, _I32, _P, _I64, _P],
         "spc_attention_workspace": [_I32, AP, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
-        "spc_attention_fwd": [_I32, AP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _SZ, _P],
-        "spc_attention_bwd": [_I32, AP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64,
-                              _P, _SZ, _P],
+        "spc_attention_fwd": [_I32, AP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P],
+        "spc_attention_bwd": [_I32, AP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P,
+                              _I64, _P, _SZ, _P],
         "spc_calibrate_mfma": [_I32, _I32, _I32, _P, ctypes.POINTER(ctypes.c_double), _P],
     }
     for name, args in sig.items():
@@ -1045,8 +1045,8 @@ def layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: 
     else:
         _need_like(out, "out", x.dtype, dev, x.shape)
     stats = x.new_empty((n, 2), dtype=torch.float32)
-    st = _call(dev, lib().spc_layer_norm_fwd, _DTYPES[x.dtype], _ptr(x), _ptr(residual), n, C, _ptr(gamma), _ptr(beta), eps, _ptr(out),
-                                  _ptr(total), _ptr(stats))
+    st = _call(dev, lib().spc_layer_norm_fwd, _DTYPES[x.dtype], _ptr(x), _ptr(residual), n, C, _ptr(gamma), _ptr(beta), eps,
+               _ptr(out), _ptr(total), _ptr(stats))
     _check(st, "spc_layer_norm_fwd")
     return out, stats, total
 
@@ -1074,8 +1074,8 @@ def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Te
     if want_affine:
         dgamma, dbeta = x.new_empty((C,), dtype=torch.float32), x.new_empty((C,), dtype=torch.float32)
     workspace = _scratch(workspace, layer_norm_workspace(n, C) if want_affine else 0, x)
-    st = _call(dev, lib().spc_layer_norm_bwd, _DTYPES[x.dtype], _ptr(dout), _ptr(x), n, C, _ptr(gamma), _ptr(stats), _ptr(dtotal), _ptr(dx),
-                                  _ptr(dgamma), _ptr(dbeta), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    st = _call(dev, lib().spc_layer_norm_bwd, _DTYPES[x.dtype], _ptr(dout), _ptr(x), n, C, _ptr(gamma), _ptr(stats),
+               _ptr(dtotal), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), 0 if workspace is None else workspace.numel())
     _check(st, "spc_layer_norm_bwd")
     return dx, dgamma, dbeta
 
@@ -1131,8 +1131,9 @@ def rotary(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, pairs: Sequen
     elif out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
         raise ValueError("out may be x itself, not another view of it")
     ldo = _heads(out, "out", x.dtype, dev, x.shape)
-    st = _call(dev, lib().spc_rotary, _DTYPES[x.dtype], _ptr(x), ldx, n, H, D, _ptr(pos), pos.stride(0) if n > 1 else len(pairs),
-                          len(pairs), _axis_pairs(pairs), _ptr(freq), 1 if inverse else 0, _ptr(out), ldo)
+    st = _call(dev, lib().spc_rotary, _DTYPES[x.dtype], _ptr(x), ldx, n, H, D, _ptr(pos),
+               pos.stride(0) if n > 1 else len(pairs), len(pairs), _axis_pairs(pairs), _ptr(freq), 1 if inverse else 0,
+               _ptr(out), ldo)
     _check(st, "spc_rotary")
     return out
 
@@ -1184,23 +1185,27 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg_ptr: Op
     [Nq, heads, D], k and v [Nkv, kv_heads, D], each of which may be a column
     slice of one product.  seg_ptr and order lay out the queries and, where
     neither kv_ptr nor kv_order is given, the keys; scale defaults to D^-1/2.
-    Returns ``(out [Nq, heads, D], stats fp32 [heads, Nq, 2] or None)``; stats
-    are for attention_bwd."""
+    Returns ``(out [Nq, heads, D], stats or None)``; stats are for
+    attention_bwd: ``(ml fp32 [heads, Nq, 2], rest)``, the rows' maxima and sums
+    and what rounding left of out ([Nq, heads, D]; None for fp32)."""
     a, (ldq, ldk, ldv), (need, _) = _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale)
     dev, (n, H, D) = q.device, q.shape
     if out is None:
         out = q.new_empty((n, H, D))
     ldo = _heads(out, "out", q.dtype, dev, q.shape)
-    stats = q.new_empty((H, n, 2), dtype=torch.float32) if want_stats else None
+    ml = rest = None
+    if want_stats:
+        ml = q.new_empty((H, n, 2), dtype=torch.float32)
+        rest = q.new_empty((n, H, D)) if q.dtype != torch.float32 else None
     workspace = _scratch(workspace, need, q)
-    st = _call(dev, lib().spc_attention_fwd, _DTYPES[q.dtype], ctypes.byref(a), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(out), ldo,
-                                 _ptr(stats), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    st = _call(dev, lib().spc_attention_fwd, _DTYPES[q.dtype], ctypes.byref(a), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
+               _ptr(out), ldo, _ptr(ml), _ptr(rest), _ptr(workspace), 0 if workspace is None else workspace.numel())
     _check(st, "spc_attention_fwd")
-    return out, stats
+    return out, (ml, rest) if want_stats else None
 
 
 def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
-                  stats: torch.Tensor, seg_ptr: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None,
+                  stats: tuple, seg_ptr: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None,
                   kv_ptr: Optional[torch.Tensor] = None, kv_order: Optional[torch.Tensor] = None, causal: bool = False,
                   scale: Optional[float] = None, dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
                   dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
@@ -1210,15 +1215,18 @@ def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     a, (ldq, ldk, ldv), (_, need) = _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale)
     dev, (n, H, D) = q.device, q.shape
     lddo, ldo = _heads(dout, "dout", q.dtype, dev, q.shape), _heads(out, "out", q.dtype, dev, q.shape)
-    _need_like(stats, "stats", torch.float32, dev, (H, n, 2))
+    ml, rest = stats
+    _need_like(ml, "stats[0]", torch.float32, dev, (H, n, 2))
+    if rest is not None:
+        _need_like(rest, "stats[1]", q.dtype, dev, (n, H, D))
     dq = q.new_empty(q.shape) if dq is None else dq
     dk = k.new_empty(k.shape) if dk is None else dk
     dv = v.new_empty(v.shape) if dv is None else dv
     lddq, lddk, lddv = (_heads(t, nm, q.dtype, dev, like.shape) for t, nm, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
     workspace = _scratch(workspace, need, q)
-    st = _call(dev, lib().spc_attention_bwd, _DTYPES[q.dtype], ctypes.byref(a), _ptr(dout), lddo, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
-                                 _ptr(out), ldo, _ptr(stats), _ptr(dq), lddq, _ptr(dk), lddk, _ptr(dv), lddv, _ptr(workspace),
-                                 0 if workspace is None else workspace.numel())
+    st = _call(dev, lib().spc_attention_bwd, _DTYPES[q.dtype], ctypes.byref(a), _ptr(dout), lddo, _ptr(q), ldq, _ptr(k), ldk,
+               _ptr(v), ldv, _ptr(out), ldo, _ptr(ml), _ptr(rest), _ptr(dq), lddq, _ptr(dk), lddk, _ptr(dv), lddv,
+               _ptr(workspace), 0 if workspace is None else workspace.numel())
     _check(st, "spc_attention_bwd")
     return dq, dk, dv
 

@@ -30,6 +30,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 struct Args {
     const char *q, *k, *v, *o, *dout;       // o: the forward's output, read by the backward
     char *out, *dq, *dk, *dv;
+    char* rest;                             // [n_q, heads, D], what rounding left of the output (NULL: not kept)
     int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;   // bytes between rows
     const int32_t *q_order, *kv_order;
     Segs qs, ks;
@@ -95,6 +96,20 @@ __device__ __forceinline__ void put4(char* p, f32x4_t v) {
         *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, __builtin_convertvector(v, h4));
     } else {
         *reinterpret_cast<f32x4_t*>(p) = v;
+    }
+}
+
+// What that rounding left of v, rounded itself.
+template <typename TT>
+__device__ __forceinline__ f32x4_t left_of(f32x4_t v) {
+    if constexpr (TT::id == SPC_BF16) {
+        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+        return v - __builtin_convertvector(__builtin_convertvector(v, b4), f32x4_t);
+    } else if constexpr (TT::id == SPC_F16) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        return v - __builtin_convertvector(__builtin_convertvector(v, h4), f32x4_t);
+    } else {
+        return f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
 }
 
@@ -169,16 +184,26 @@ struct Second {
         else return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
     }
 
-    static __device__ __forceinline__ void add(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w, int lane) {
+    // The weights as the right operands of all steps, rounded to the type.
+    struct Packed {
+        u32x4 b[STEPS];
+        __device__ __forceinline__ Packed() {}
+        __device__ __forceinline__ explicit Packed(const f32x16_t& w) {
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-            float wt[PER];
+            for (int t = 0; t < STEPS; ++t) {
+                float wt[PER];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) wt[e] = w[t * PER + e];
-            const u32x4 b = pack(wt);
-#pragma unroll
-            for (int db = 0; db < T::NB; ++db) acc[db] = step(left(x, row0, t, db, lane), b, acc[db]);
+                for (int e = 0; e < PER; ++e) wt[e] = w[t * PER + e];
+                b[t] = pack(wt);
+            }
         }
+    };
+
+    static __device__ __forceinline__ void add(f32x16_t (&acc)[T::NB], const char* x, int row0, const Packed& w, int lane) {
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+            for (int db = 0; db < T::NB; ++db) acc[db] = step(left(x, row0, t, db, lane), w.b[t], acc[db]);
     }
 
     // The finite elements of a left operand, the others 0.
@@ -213,20 +238,16 @@ struct Second {
     // infinite or NaN value reaches the columns that see its row: counted
     // apart.  Without, it has made w itself NaN in those columns.
     template <bool OTHERS>
-    static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w,
+    static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const Packed& w,
                                                       uint32_t vis, int lane) {
         bool odd = false;
 #pragma unroll
         for (int t = 0; t < STEPS; ++t) {
-            float wt[PER];
-#pragma unroll
-            for (int e = 0; e < PER; ++e) wt[e] = w[t * PER + e];
-            const u32x4 b = pack(wt);
 #pragma unroll
             for (int db = 0; db < T::NB; ++db) {
                 const u32x4 a = left(x, row0, t, db, lane), f = finite(a);
                 if constexpr (OTHERS) odd |= a.x != f.x || a.y != f.y || a.z != f.z || a.w != f.w;
-                acc[db] = step(f, b, acc[db]);
+                acc[db] = step(f, w.b[t], acc[db]);
             }
         }
         if constexpr (OTHERS) {
@@ -479,9 +500,14 @@ struct KeyStage : Stage<TT, DP, BN, NT> {
 template <typename TT, int NW>
 constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
 
+// The forward's: heads of 128 have the registers for 2 where nothing is masked
+// (16,384 x 8 x 128: 1,226 us with 2, 1,297 with 1; causal 16,411 x 8 x 128
+// spills with 2: 1,150 us, 780 with 1).
+template <typename TT, int DP, int NW, bool CAUSAL>
+constexpr int KT_FWD = DP <= 64 || (!CAUSAL && NW == 4) ? KT_OF<TT, NW> : 1;
+
 // Waves that a SIMD is to hold at least, which bounds the registers: the most
-// that costs no spills in the loops (heads of 128 masked as causal spill a
-// few: 16,411 x 8 x 128 takes 819 us so, 985 with one wave and none).
+// that costs no spills in the loops.
 template <typename TT, int DP, bool CAUSAL>
 constexpr int FWD_WAVES = TT::E == 4 ? 1 : DP <= 32 ? 4 - CAUSAL : DP <= 64 ? 3 - CAUSAL : 2;
 template <typename TT, int DP>
@@ -491,7 +517,7 @@ constexpr float LAZY = 1024.f;   // far below fp16's largest number, which a sin
 
 template <typename TT, int DP, int NW, bool CAUSAL>
 __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_fwd(const Args p) {
-    constexpr int BM = 32 * NW, KT = KT_OF<TT, NW>, BN = 32 * KT, NT = 64 * NW;
+    constexpr int BM = 32 * NW, KT = KT_FWD<TT, DP, NW, CAUSAL>, BN = 32 * KT, NT = 64 * NW;
     constexpr bool SP = SPLIT<TT, DP>;
     using T = Tile<TT, DP>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * T::PITCH];
@@ -553,7 +579,9 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
             // tells whether it still serves: where a column's part of the tile
             // sums to more than LAZY, and at the first tile, the scores are
             // computed once more (the tile is still there) for a new maximum.
+            using X = Second<TT, DP>;
             f32x16_t s[KT];
+            typename X::Packed w[KT];
             float sum = 0.f;
             for (bool fresh = t == t0;;) {
                 int c = col;
@@ -605,12 +633,14 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                 const float base = m == -INFINITY ? 0.f : m;
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int u = 0; u < KT; ++u)
+                for (int u = 0; u < KT; ++u) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         s[u][r] = exp2_(SP ? s[u][r] : fmaf(s[u][r], p.c, -base));
                         part[r & 3] += s[u][r];
                     }
+                    w[u] = typename X::Packed(s[u]);
+                }
                 sum = (part[0] + part[1]) + (part[2] + part[3]);
                 if (fresh || !__any(sum > LAZY)) break;
                 fresh = true;
@@ -618,8 +648,8 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
             l += sum;
 #pragma unroll
             for (int u = 0; u < KT; ++u) {
-                if (CAUSAL && edge) Second<TT, DP>::template add_masked<true>(acc, vt, 32 * u, s[u], vis[u], lane);
-                else Second<TT, DP>::add(acc, vt, 32 * u, s[u], lane);
+                if (CAUSAL && edge) X::template add_masked<true>(acc, vt, 32 * u, w[u], vis[u], lane);
+                else X::add(acc, vt, 32 * u, w[u], lane);
             }
         }
         if (more) stage.put(lds[buf ^ 1][0], lds[buf ^ 1][1]);
@@ -644,12 +674,16 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     char* out = p.out + int64_t(q.row) * p.ldo + int64_t(q.head) * p.D * T::ES;
+    char* rest = p.rest + (int64_t(q.row) * (int64_t(p.g) * p.hk) + q.head) * p.D * T::ES;
 #pragma unroll
     for (int db = 0; db < T::NB; ++db)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int d = 32 * db + 8 * b + 4 * h;
-            if (d < p.D) put4<TT>(out + d * T::ES, f32x4_t{acc[db][4 * b] * inv, acc[db][4 * b + 1] * inv, acc[db][4 * b + 2] * inv, acc[db][4 * b + 3] * inv});
+            if (d >= p.D) continue;
+            const f32x4_t o = f32x4_t{acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]} * inv;
+            put4<TT>(out + d * T::ES, o);
+            if (TT::E == 8 && p.rest) put4<TT>(rest + d * T::ES, left_of<TT>(o));
         }
     if (p.stats && h == 0) p.stats[id] = float2{m, l};
 }
@@ -710,7 +744,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const Args p) {
         }
         if (s0 > 0 || q.row < 0 || d >= p.D) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        put4<TT>(p.out + int64_t(q.row) * p.ldo + (int64_t(q.head) * p.D + d) * ES, o * inv);
+        o *= inv;
+        put4<TT>(p.out + int64_t(q.row) * p.ldo + (int64_t(q.head) * p.D + d) * ES, o);
+        if (TT::E == 8 && p.rest) put4<TT>(p.rest + ((int64_t(q.row) * (int64_t(p.g) * p.hk) + q.head) * p.D + d) * ES, left_of<TT>(o));
         if (p.stats && d == 0) p.stats[id] = float2{m, l};
     }
 }
@@ -747,14 +783,18 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
     load_frags<TT, DP>(gf, p.dout + int64_t(q.row) * p.lddo + in, q.row >= 0, p.D, h);
     float delta = 0.f;
     {
-        u32x4 of[T::NS];
+        u32x4 of[T::NS], ol[T::NS];
         load_frags<TT, DP>(of, p.o + int64_t(q.row) * p.ldo + in, q.row >= 0, p.D, h);
+        // the output as it was before its rounding: where one key outweighs the
+        // others, do . v_j - delta is a small difference of large numbers
+        const bool kept = TT::E == 8 && p.rest;
+        load_frags<TT, DP>(ol, p.rest + (int64_t(q.row) * (int64_t(p.g) * p.hk) + q.head) * p.D * T::ES, kept && q.row >= 0, p.D, h);
 #pragma unroll
         for (int s = 0; s < T::NS; ++s) {
             if constexpr (TT::E == 8) {
-                Raw8<TT> x, y;
-                x.v[0] = of[s], y.v[0] = gf[s];
-                const f32x8_t a = widen<TT>(x), b = widen<TT>(y);
+                Raw8<TT> x, y, z;
+                x.v[0] = of[s], y.v[0] = gf[s], z.v[0] = ol[s];
+                const f32x8_t a = widen<TT>(x) + widen<TT>(z), b = widen<TT>(y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
             } else {
@@ -802,6 +842,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
             const bool edge = p0 + BN > seen_first || live != first_bits(BN);
 #pragma unroll
             for (int u = 0; u < KT; ++u) {
+                using X = Second<TT, DP>;
                 f32x16_t s = from_s, d = from_d;
 #pragma unroll
                 for (int st = 0; st < T::NS; ++st) {
@@ -823,11 +864,11 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = (vis >> bit_of(r)) & 1u ? s[r] : 0.f;
                     if constexpr (CAUSAL) {
-                        Second<TT, DP>::template add_masked<false>(acc, kt, 32 * u, s, vis, lane);
+                        X::template add_masked<false>(acc, kt, 32 * u, typename X::Packed(s), vis, lane);
                         continue;
                     }
                 }
-                Second<TT, DP>::add(acc, kt, 32 * u, s, lane);
+                X::add(acc, kt, 32 * u, typename X::Packed(s), lane);
             }
         }
         if (more) stage.put(lds[buf ^ 1][0], lds[buf ^ 1][1]);
@@ -949,6 +990,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
             const bool edge = here != first_bits(BN) || p0 < first_hi;
 #pragma unroll
             for (int u = 0; u < KT; ++u) {
+                using X = Second<TT, DP>;
                 // the products start from the rows' -m and -delta
                 f32x16_t s = zero16(), d;
 #pragma unroll
@@ -995,13 +1037,13 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
                         s[r] = see ? s[r] : 0.f, d[r] = see ? d[r] : 0.f;
                     }
                     if constexpr (CAUSAL) {
-                        Second<TT, DP>::template add_masked<true>(dv, gt, 32 * u, s, vis, lane);
-                        Second<TT, DP>::template add_masked<false>(dk, qt, 32 * u, d, vis, lane);
+                        X::template add_masked<true>(dv, gt, 32 * u, typename X::Packed(s), vis, lane);
+                        X::template add_masked<false>(dk, qt, 32 * u, typename X::Packed(d), vis, lane);
                         continue;
                     }
                 }
-                Second<TT, DP>::add(dv, gt, 32 * u, s, lane);
-                Second<TT, DP>::add(dk, qt, 32 * u, d, lane);
+                X::add(dv, gt, 32 * u, typename X::Packed(s), lane);
+                X::add(dk, qt, 32 * u, typename X::Packed(d), lane);
             }
         }
         if (more) put(buf ^ 1);
@@ -1094,9 +1136,10 @@ spc_status launch_bwd_bf16(const Args& p, const Cut& q, const Cut& k, hipStream_
 inline int64_t slots_of(int64_t rows, int64_t n_seg, int bm) { return rows / bm + n_seg + 1; }
 
 // Sets the grid of a walk; its workgroups.  A group is 1,024 rows of all heads
-// where there are many (windows of 1,024 on 266,426 x 4 x 32 bf16: forward
-// GROUPED us against ROUND us in groups of one slot), a slot where the work of
-// neighbours differs (causal) or there are few.
+// where there are many (windows of 1,024 on 266,426 x 4 x 32 bf16: forward 322
+// us, backward 784; 338 and 821 in groups of one slot), a slot where the work of
+// neighbours differs (causal: 16,411 x 8 x 128 took 1,872 us in eight
+// contiguous parts, 985 so) or there are few.
 inline unsigned set_grid(Args& p, int64_t slots, int splits, int rows_of_slot, bool even) {
     p.slots = int32_t(slots), p.splits = splits;
     p.total = unsigned(slots * splits * p.hk);
@@ -1111,6 +1154,10 @@ inline unsigned set_grid(Args& p, int64_t slots, int splits, int rows_of_slot, b
         else hipLaunchKernelGGL((name<TT, dp, nw, false>), dim3(grid), dim3(64 * nw), 0, stream, p);                          \
     } while (0)
 
+// Workgroups of four waves, or of the fewest: one, and two where heads are so
+// wide that one wave's share of the staging would not fit its registers.
+constexpr int few_waves(int D) { return D <= 64 ? 1 : 2; }
+
 #define ATTN_WIDTHS(name, nw, grid, p)                                                                                        \
     do {                                                                                                                      \
         /* c above 1 could take a large fp16 number past the type's range when it is multiplied: no split then */             \
@@ -1119,7 +1166,7 @@ inline unsigned set_grid(Args& p, int64_t slots, int splits, int rows_of_slot, b
         else if (p.D <= 32 && split) ATTN_WIDTH(name, 32, nw, grid, p);                                                       \
         else if (TT::E == 4 && p.D <= 48) ATTN_WIDTH(name, (TT::E == 4 ? 48 : 64), nw, grid, p);                              \
         else if (p.D <= 64) ATTN_WIDTH(name, 64, nw, grid, p);                                                                \
-        else ATTN_WIDTH(name, 128, nw, grid, p);                                                                              \
+        else ATTN_WIDTH(name, 128, (nw == 1 ? few_waves(128) : nw), grid, p);                                                 \
         SPC_LAUNCHED(#name);                                                                                                  \
     } while (0)
 

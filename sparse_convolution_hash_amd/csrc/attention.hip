@@ -10,11 +10,11 @@ constexpr int D_MAX = 128;
 
 // Rows of one side that work is cut over (positions times the heads that share
 // them), and the other side's.
-Cut cut_of(int64_t rows, int64_t other, int64_t n_seg, int heads) {
+Cut cut_of(int64_t rows, int64_t other, int64_t n_seg, int heads, int D) {
     Cut c;
     // Four waves share the staged tiles where samples have rows for them and
-    // the call fills the chip; else single waves, which leave fewer lanes idle.
-    c.nw = rows >= 64 * n_seg && slots_of(rows, n_seg, 128) * heads >= 512 ? 4 : 1;
+    // the call fills the chip; else as few as there can be, which leave fewer lanes idle.
+    c.nw = rows >= 64 * n_seg && slots_of(rows, n_seg, 128) * heads >= 512 ? 4 : few_waves(D);
     c.slots = slots_of(rows, n_seg, 32 * c.nw);
     // Few workgroups: the other side is split too, and the parts are joined by
     // a second launch, to 4 waves a SIMD (5,003 x 6 x 48 fp32 in 23 ragged samples,
@@ -49,8 +49,8 @@ spc_status check_sizes(spc_dtype dtype, const spc_attention* a, Plan& w) {
         return fail(SPC_ERR_UNSUPPORTED, "rows x heads exceed 31 bits");
     if (!(a->scale > 0.f && a->scale <= 3.402823466e38f)) return fail(SPC_ERR_ARG, "scale=%g must be positive and finite", double(a->scale));
     const int64_t rows = a->n_q * (a->heads / a->kv_heads);
-    w.q = cut_of(rows, a->n_kv, a->n_seg, a->kv_heads);
-    w.k = cut_of(a->n_kv, rows, a->n_seg, a->kv_heads);
+    w.q = cut_of(rows, a->n_kv, a->n_seg, a->kv_heads, a->head_dim);
+    w.k = cut_of(a->n_kv, rows, a->n_seg, a->kv_heads, a->head_dim);
     // (a call that is split has few workgroups, so its join has too)
     if (!launchable(w.q.blocks, 64 * w.q.nw) || !launchable(w.k.blocks, 64 * w.k.nw))
         return fail(SPC_ERR_UNSUPPORTED, "%lld samples of %lld and %lld rows exceed one launch", (long long)a->n_seg, (long long)a->n_q,
@@ -110,8 +110,8 @@ extern "C" spc_status spc_attention_workspace(spc_dtype dtype, const spc_attenti
 }
 
 extern "C" spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a, const void* q, int64_t ldq, const void* k,
-                                        int64_t ldk, const void* v, int64_t ldv, void* out, int64_t ldo, float* stats, void* ws,
-                                        size_t ws_bytes, hipStream_t stream) {
+                                        int64_t ldk, const void* v, int64_t ldv, void* out, int64_t ldo, float* stats, void* rest,
+                                        void* ws, size_t ws_bytes, hipStream_t stream) {
     clear_error();
     Plan w;
     Args p;
@@ -122,12 +122,12 @@ extern "C" spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a,
         if ((st = check_rows(dtype, a, s, a->n_q)) != SPC_OK) return st;
     for (const Side& s : {Side{k, ldk, a->kv_heads, "k"}, Side{v, ldv, a->kv_heads, "v"}})
         if ((st = check_rows(dtype, a, s, a->n_kv)) != SPC_OK) return st;
-    if (stats && !aligned16(stats)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    if ((stats && !aligned16(stats)) || (rest && !aligned16(rest))) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     if (a->n_q == 0) return SPC_OK;
     const int64_t e = dtype_size(dtype);
     p.q = static_cast<const char*>(q), p.k = static_cast<const char*>(k), p.v = static_cast<const char*>(v), p.out = static_cast<char*>(out);
     p.ldq = ldq * e, p.ldk = ldk * e, p.ldv = ldv * e, p.ldo = ldo * e;
-    p.stats = reinterpret_cast<float2*>(stats);
+    p.stats = reinterpret_cast<float2*>(stats), p.rest = static_cast<char*>(rest);
     p.part = static_cast<float*>(ws);
     switch (dtype) {
         case SPC_F32: return launch_fwd_f32(p, w.q, stream);
@@ -139,8 +139,8 @@ extern "C" spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a,
 
 extern "C" spc_status spc_attention_bwd(spc_dtype dtype, const spc_attention* a, const void* dout, int64_t lddo, const void* q,
                                         int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, const void* out,
-                                        int64_t ldo, const float* stats, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv,
-                                        int64_t lddv, void* ws, size_t ws_bytes, hipStream_t stream) {
+                                        int64_t ldo, const float* stats, const void* rest, void* dq, int64_t lddq, void* dk, int64_t lddk,
+                                        void* dv, int64_t lddv, void* ws, size_t ws_bytes, hipStream_t stream) {
     clear_error();
     Plan w;
     Args p;
@@ -154,14 +154,14 @@ extern "C" spc_status spc_attention_bwd(spc_dtype dtype, const spc_attention* a,
                           Side{dv, lddv, a->kv_heads, "dv"}})
         if ((st = check_rows(dtype, a, s, a->n_kv)) != SPC_OK) return st;
     if (a->n_q > 0 && !stats) return fail(SPC_ERR_ARG, "stats is NULL");
-    if (stats && !aligned16(stats)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    if ((stats && !aligned16(stats)) || (rest && !aligned16(rest))) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     const int64_t e = dtype_size(dtype);
     p.q = static_cast<const char*>(q), p.k = static_cast<const char*>(k), p.v = static_cast<const char*>(v);
     p.o = static_cast<const char*>(out), p.dout = static_cast<const char*>(dout);
     p.dq = static_cast<char*>(dq), p.dk = static_cast<char*>(dk), p.dv = static_cast<char*>(dv);
     p.ldq = ldq * e, p.ldk = ldk * e, p.ldv = ldv * e, p.ldo = ldo * e, p.lddo = lddo * e;
     p.lddq = lddq * e, p.lddk = lddk * e, p.lddv = lddv * e;
-    p.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
+    p.stats = reinterpret_cast<float2*>(const_cast<float*>(stats)), p.rest = static_cast<char*>(const_cast<void*>(rest));
     p.delta = static_cast<float*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(size_t(a->n_q) * size_t(a->heads) * 4, 256));
     switch (dtype) {

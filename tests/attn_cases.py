@@ -87,7 +87,7 @@ def check(c, bwd=True, q=None):
     rows, keys = ref["rows"], ref["keys"]
     within(f64(out)[rows], ref["out"][rows], ref["e_out"][rows], c.dtype, "out")
     assert (out[~torch.from_numpy(rows)] == mark).all()
-    st = f64(stats)[:, rows]
+    st = f64(stats[0])[:, rows]
     with np.errstate(divide="ignore"):
         lse = (st[..., 0] + np.log2(st[..., 1])) * np.log(2.0)
     lse[st[..., 1] == 0] = -np.inf
@@ -97,9 +97,9 @@ def check(c, bwd=True, q=None):
     lse, want, env = lse[some], want[some], env[some]
     assert (np.abs(lse - want) <= env + 4e-7 * (1 + np.abs(want))).all()
     if not bwd:
-        return out, stats
+        return out, stats[0]
     got = spc.attention_bwd(dout, q, k, v, out, stats, dq=fill(q), dk=fill(k), dv=fill(v), **kw)
     for t, name, there in zip(got, ("dq", "dk", "dv"), (rows, keys, keys)):
         within(f64(t)[there], ref[name][there], ref["e_" + name][there], c.dtype, name)
         assert (t[~torch.from_numpy(there)] == mark).all()
-    return (out, stats) + got
+    return (out, stats[0]) + got

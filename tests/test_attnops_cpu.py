@@ -70,13 +70,14 @@ def attn(n_q=1000, n_kv=1000, S=1, H=4, Hk=2, D=32, causal=0, scale=0.5, qp=None
 def test_attention_refusals():
     L, R = B.lib(), ctypes.byref
 
-    def fwd(dt=2, a=None, q=P, ldq=128, k=P, ldk=64, v=P, ldv=64, out=P, ldo=128, st=P, ws=P, wsb=BIG, **kw):
-        return L.spc_attention_fwd(dt, R(attn(**kw) if a is None else a), q, ldq, k, ldk, v, ldv, out, ldo, st, ws, wsb, None)
+    def fwd(dt=2, a=None, q=P, ldq=128, k=P, ldk=64, v=P, ldv=64, out=P, ldo=128, st=P, rest=P, ws=P, wsb=BIG, **kw):
+        return L.spc_attention_fwd(dt, R(attn(**kw) if a is None else a), q, ldq, k, ldk, v, ldv, out, ldo, st, rest, ws, wsb,
+                                   None)
 
-    def bwd(dt=2, a=None, do=P, lddo=128, q=P, ldq=128, k=P, ldk=64, v=P, ldv=64, out=P, ldo=128, st=P, dq=P, lddq=128, dk=P,
+    def bwd(dt=2, a=None, do=P, lddo=128, q=P, ldq=128, k=P, ldk=64, v=P, ldv=64, out=P, ldo=128, st=P, rest=P, dq=P, lddq=128, dk=P,
             lddk=64, dv=P, lddv=64, ws=P, wsb=BIG, **kw):
-        return L.spc_attention_bwd(dt, R(attn(**kw) if a is None else a), do, lddo, q, ldq, k, ldk, v, ldv, out, ldo, st, dq,
-                                   lddq, dk, lddk, dv, lddv, ws, wsb, None)
+        return L.spc_attention_bwd(dt, R(attn(**kw) if a is None else a), do, lddo, q, ldq, k, ldk, v, ldv, out, ldo, st, rest,
+                                   dq, lddq, dk, lddk, dv, lddv, ws, wsb, None)
 
     for f in (fwd, bwd):
         assert f(D=24) == f(D=144, ldq=1 << 10, ldk=1 << 10) == f(D=0) == B.SPC_ERR_UNSUPPORTED
@@ -91,7 +92,7 @@ def test_attention_refusals():
             assert f(**{name: None}) == f(**{name: ODD}) == B.SPC_ERR_ARG, name
         for name in ("ldq", "ldk", "ldv", "ldo"):
             assert f(**{name: 60}) == f(**{name: 132}) == f(**{name: 1 << 31}) == B.SPC_ERR_ARG, name
-        assert f(st=ODD) == f(ws=ODD) == B.SPC_ERR_ARG
+        assert f(st=ODD) == f(rest=ODD) == f(ws=ODD) == B.SPC_ERR_ARG
     for name in ("do", "dq", "dk", "dv"):
         assert bwd(**{name: None}) == bwd(**{name: ODD}) == B.SPC_ERR_ARG, name
     for name in ("lddo", "lddq", "lddk", "lddv"):
@@ -127,7 +128,7 @@ def test_binding_refuses_cpu_tensors():
     x, h = torch.zeros(4, 16), torch.zeros(4, 1, 16)
     for f in (lambda: spc.layer_norm_fwd(x), lambda: spc.layer_norm_bwd(x, x, None, x),
               lambda: spc.rotary(h, torch.zeros(4, 1, dtype=torch.int32), torch.zeros(8), (8,)),
-              lambda: spc.attention_fwd(h, h, h), lambda: spc.attention_bwd(h, h, h, h, h, x)):
+              lambda: spc.attention_fwd(h, h, h), lambda: spc.attention_bwd(h, h, h, h, h, (x, None))):
         with pytest.raises(TypeError):
             f()
 
