@@ -578,7 +578,8 @@ spc_status spc_layer_norm_workspace(int64_t n, int32_t C, size_t* bytes);
  *   rstd = (var + eps)^-1/2
  * x, residual, y, total [n, C], C a positive multiple of 16 up to 4096; gamma,
  * beta fp32 [C] (NULL: 1 and 0).  residual and total come together: total
- * receives u (NULL both: u is x).  y may be x, total may be x or residual.
+ * receives u (NULL both: u is x).  y may be x, total may be x or residual,
+ * but y and total are not the same rows.
  * stats fp32 [n, 2] receives mean and rstd.
  */
 spc_status spc_layer_norm_fwd(spc_dtype dtype, const void* x, const void* residual, int64_t n, int32_t C,
@@ -627,7 +628,7 @@ spc_status spc_rotary(spc_dtype dtype, const void* x, int64_t ldx, int64_t n, in
  * row.  heads a multiple of kv_heads: query head h reads key head
  * h / (heads / kv_heads).  head_dim a multiple of 16 up to 128.  causal != 0:
  * of a sample's lq queries and lk keys, query i sees the keys j <= i + lk - lq
- * (its last query sees all).  scale positive and finite.
+ * (its last query sees all).  scale positive, at most 1e38.
  */
 typedef struct spc_attention {
     int64_t n_q, n_kv, n_seg;
@@ -658,7 +659,8 @@ spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size
  * Where head_dim <= 32, 16-bit dtypes multiply scale log2(e) into one factor
  * of s, kept as two numbers of the type: s is off by up to 2^-18 (bf16) or
  * 2^-22 (fp16) of scale sum_d |q_id k_jd|.  A NaN or infinity in a row that is
- * seen may make everything NaN that depends on it.
+ * seen may make everything NaN that depends on it, and so may scores s above
+ * 10^8 in size, of which fp32 keeps no fractions.  out overlaps no input.
  * Rows of no sample are written in none of the outputs.
  */
 spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a, const void* q, int64_t ldq, const void* k,

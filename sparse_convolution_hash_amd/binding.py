@@ -1215,6 +1215,8 @@ def attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     a, (ldq, ldk, ldv), (_, need) = _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale)
     dev, (n, H, D) = q.device, q.shape
     lddo, ldo = _heads(dout, "dout", q.dtype, dev, q.shape), _heads(out, "out", q.dtype, dev, q.shape)
+    if not isinstance(stats, tuple) or len(stats) != 2:
+        raise TypeError("stats must be what attention_fwd(..., want_stats=True) returned")
     ml, rest = stats
     _need_like(ml, "stats[0]", torch.float32, dev, (H, n, 2))
     if rest is not None:

@@ -25,7 +25,6 @@ namespace attn {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char lds_char;
 
 struct Args {
     const char *q, *k, *v, *o, *dout;       // o: the forward's output, read by the backward
@@ -36,6 +35,7 @@ struct Args {
     Segs qs, ks;
     int32_t g, hk, D, causal;               // query heads to a key head, key heads, head dimension
     uint32_t inv_g;                         // 2^32 / g, rounded up (g > 1)
+    float up, down;                         // a power of two and its inverse: see SPLIT
     float c, scale;                         // c = scale log2(e)
     float2* stats;                          // [heads, n_q] (m, l)
     float* delta;                           // [heads, n_q] do . o
@@ -340,7 +340,7 @@ __device__ __forceinline__ Query place_of(const Args& p, const Job& j, int rq) {
     if (p.g > 1) {
         // rq times the rounded-up 2^32 / g: the quotient, or one more
         q.pos = int(__umulhi(unsigned(rq), p.inv_g));
-        q.pos -= q.pos * p.g > rq;
+        q.pos -= unsigned(q.pos) * unsigned(p.g) > unsigned(rq);
         q.head = j.head * p.g + (rq - q.pos * p.g);
     }
     return q;
@@ -370,8 +370,18 @@ __device__ __forceinline__ void load_frags(u32x4* f, const char* row, bool there
 // the product starts from -m, so that the matrix unit hands over the exponent
 // itself.  Wider heads would pay more in the matrix unit (a second product
 // over DP) than they save: 64 cycles for DP / 16 products of 32 on each tile.
+// An infinite key meets both numbers, and inf - inf is NaN where the plain
+// product gives minus infinity.
+// fp16 numbers end at 65,504: above c = 1 the operand is multiplied by c / up, a
+// factor of at most 1, and the exponent by up, a power of two (1 otherwise).
 template <typename TT, int DP>
 constexpr bool SPLIT = TT::E == 8 && DP <= 32;
+
+template <typename TT, int DP>
+__device__ __forceinline__ void scale_up(f32x16_t& s, const Args& p) {
+    if constexpr (SPLIT<TT, DP> && TT::id == SPC_F16)
+        if (p.up != 1.f) s *= p.up;
+}
 
 // f times c as f + lo (lo has entries where the product is split).
 template <typename TT, int DP>
@@ -495,7 +505,7 @@ struct KeyStage : Stage<TT, DP, BN, NT> {
 
 // ----------------------------------------------------------- forward
 
-// Keys below 32 rows to a tile step: 64 keys for the wide workgroups of 16-bit
+// 32-key blocks of a staged tile: 64 keys for the wide workgroups of 16-bit
 // types, 32 else (LDS and registers of the staging).
 template <typename TT, int NW>
 constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
@@ -530,7 +540,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
     const Query q = query_of(p, j, j.a, rw + col, rows);
     u32x4 qf[T::NS], ql[SP ? T::NS : 1];
     load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + int64_t(q.head) * p.D * T::ES, q.row >= 0, p.D, h);
-    split_frags<TT, DP>(qf, ql, p.c);
+    split_frags<TT, DP>(qf, ql, p.c * p.down);
     // keys that the workgroup's last row, the wave's first and its last see
     auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
     const int nk = limit(j.r0 + BM - 1), seen_first = rw < rows ? limit(rw) : 0, seen_last = rw < rows ? limit(rw + 31) : 0;
@@ -577,13 +587,18 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
             }
             // Scores are exponentiated against the maximum so far.  Their sum
             // tells whether it still serves: where a column's part of the tile
-            // sums to more than LAZY, and at the first tile, the scores are
-            // computed once more (the tile is still there) for a new maximum.
+            // sums to more than LAZY, the scores are computed once more (the
+            // tile is still there) for a new maximum.  A column without one
+            // (the first tile, or hidden keys and scores of minus infinity so
+            // far) takes it before anything is exponentiated.  Columns next to
+            // such a one may still need the second round; without a causal mask
+            // all columns see the same keys.
             using X = Second<TT, DP>;
             f32x16_t s[KT];
             typename X::Packed w[KT];
             float sum = 0.f;
-            for (bool fresh = t == t0;;) {
+            bool fresh = __any(m == -INFINITY && l == 0.f), last = false;    // (l is NaN where a query is)
+            for (;;) {
                 int c = col;
                 asm volatile("" : "+v"(c));    // the second round reads the tile again: nothing is kept for it
 #pragma unroll
@@ -595,6 +610,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                         s[u] = mfma32<TT>(a, qf[st], s[u]);
                         if constexpr (SP) s[u] = mfma32<TT>(a, ql[st], s[u]);
                     }
+                    scale_up<TT, DP>(s[u], p);
                 }
                 if (edge) {
 #pragma unroll
@@ -621,7 +637,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
 #pragma unroll
                         for (int u = 0; u < KT; ++u) s[u] -= d;
                         m = !grew ? m : none ? top : m + top;
-                        from = all16(m == -INFINITY ? 0.f : -m);
+                        from = all16(m == -INFINITY ? 0.f : -m * p.down);
                     } else if (grew) {
                         a = none ? 0.f : exp2_(m - top * p.c);
                         m = top * p.c;
@@ -642,8 +658,8 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                     w[u] = typename X::Packed(s[u]);
                 }
                 sum = (part[0] + part[1]) + (part[2] + part[3]);
-                if (fresh || !__any(sum > LAZY)) break;
-                fresh = true;
+                if ((CAUSAL ? last : fresh) || !__any(sum > LAZY)) break;
+                last = fresh = true;
             }
             l += sum;
 #pragma unroll
@@ -657,7 +673,6 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
     }
     l = sum_halves(l);
     seen |= uint32_t(__shfl_xor(int(seen), 32));
-    if (seen && l == 0.f) l = NAN;     // keys are seen, and every score is minus infinity
     if (q.row < 0) return;
     const int64_t id = int64_t(q.head) * p.qs.n + q.row;
     if (p.splits > 1) {
@@ -669,9 +684,10 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                 const int d = 32 * db + 8 * b + 4 * h;
                 if (d < p.D) *reinterpret_cast<f32x4_t*>(part + d) = f32x4_t{acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]};
             }
-        if (h == 0) *reinterpret_cast<float2*>(part + p.D) = float2{m, l};
+        if (h == 0) *reinterpret_cast<f32x4_t*>(part + p.D) = f32x4_t{m, l, seen ? 1.f : 0.f, 0.f};
         return;
     }
+    if (seen && l == 0.f) l = NAN;     // keys are seen, and every score is minus infinity
     const float inv = l == 0.f ? 0.f : 1.f / l;
     char* out = p.out + int64_t(q.row) * p.ldo + int64_t(q.head) * p.D * T::ES;
     char* rest = p.rest + (int64_t(q.row) * (int64_t(p.g) * p.hk) + q.head) * p.D * T::ES;
@@ -707,7 +723,7 @@ template <typename TT>
 __global__ __launch_bounds__(256) void k_attn_join(const Args p) {
     constexpr int BM = 32, ES = sizeof(typename TT::storage);
     __shared__ __attribute__((aligned(16))) f32x4_t sum_o[256];
-    __shared__ float2 sum_ml[256];
+    __shared__ __attribute__((aligned(16))) f32x4_t sum_ml[256];      // m, l, whether keys are seen
     Job j;
     if (!job_of<BM>(p, p.qs, p.g, false, j)) return;
     const JoinLayout w(p.D / 4, p.splits);
@@ -717,12 +733,13 @@ __global__ __launch_bounds__(256) void k_attn_join(const Args p) {
     for (int r = j.r0; r < rows; r += w.rows) {
         const Query q = query_of(p, j, j.a, r + rl, rows);
         const int64_t id = int64_t(q.head) * p.qs.n + q.row;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, seen = 0.f;
         f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-        auto add = [&](float m2, float l2, const f32x4_t& o2) {
-            const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
+        auto add = [&](const f32x4_t& ml, const f32x4_t& o2) {
+            const float m2 = ml[0], top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
             const float a = exp2_(m - base), b = exp2_(m2 - base);
-            l = l * a + l2 * b;                            // a part without keys: m = -inf, l and o are 0
+            l = l * a + ml[1] * b;                         // a part without keys: m = -inf, l and o are 0
+            seen += ml[2];
             o = o * a + o2 * b;
             m = top;
         };
@@ -730,19 +747,16 @@ __global__ __launch_bounds__(256) void k_attn_join(const Args p) {
 #pragma unroll 4
             for (int s = s0; s < p.splits; s += w.splits) {
                 const float* part = p.part + id * (p.D + 4) + s * step;
-                const float2 ml = *reinterpret_cast<const float2*>(part + p.D);
-                add(ml.x, ml.y, *reinterpret_cast<const f32x4_t*>(part + d));
+                add(*reinterpret_cast<const f32x4_t*>(part + p.D), *reinterpret_cast<const f32x4_t*>(part + d));
             }
         for (int n = w.splits / 2; n > 0; n /= 2) {
             __syncthreads();
-            sum_o[tid] = o, sum_ml[tid] = float2{m, l};
+            sum_o[tid] = o, sum_ml[tid] = f32x4_t{m, l, seen, 0.f};
             __syncthreads();
-            if (s0 < n) {
-                const float2 ml = sum_ml[tid + n * w.quads];
-                add(ml.x, ml.y, sum_o[tid + n * w.quads]);
-            }
+            if (s0 < n) add(sum_ml[tid + n * w.quads], sum_o[tid + n * w.quads]);
         }
         if (s0 > 0 || q.row < 0 || d >= p.D) continue;
+        if (seen > 0.f && l == 0.f) l = NAN;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         o *= inv;
         put4<TT>(p.out + int64_t(q.row) * p.ldo + (int64_t(q.head) * p.D + d) * ES, o);
@@ -807,7 +821,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
         delta = sum_halves(delta);
     }
     load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + in, q.row >= 0, p.D, h);
-    split_frags<TT, DP>(qf, ql, p.c);
+    split_frags<TT, DP>(qf, ql, p.c * p.down);
     if (q.row >= 0 && h == 0 && j.split == 0) p.delta[id] = delta;
     const float2 mf = from_stats<TT>(q.row >= 0 ? p.stats[id] : float2{0.f, 0.f});
     auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
@@ -818,7 +832,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
 
     KeyStage<TT, DP, BN, NT> stage;
     stage.begin(p, j, ka, lk);
-    const f32x16_t from_s = SP ? all16(mf.x) : zero16(), from_d = all16(-delta);   // what the products start from
+    const f32x16_t from_s = SP ? all16(mf.x * p.down) : zero16(), from_d = all16(-delta);   // what the products start from
     f32x16_t acc[T::NB];
 #pragma unroll
     for (int db = 0; db < T::NB; ++db) acc[db] = zero16();
@@ -850,6 +864,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
                     s = mfma32<TT>(a, qf[st], s);
                     if constexpr (SP) s = mfma32<TT>(a, ql[st], s);
                 }
+                scale_up<TT, DP>(s, p);
 #pragma unroll
                 for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(vt, 32 * u + col, 2 * st + h), gf[st], d);
 #pragma unroll
@@ -918,9 +933,9 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
     u32x4 kf[T::NS], kl[SP ? T::NS : 1], vf[T::NS];
     load_frags<TT, DP>(kf, p.k + int64_t(krow) * p.ldk + in, krow >= 0, p.D, h);
     load_frags<TT, DP>(vf, p.v + int64_t(krow) * p.ldv + in, krow >= 0, p.D, h);
-    split_frags<TT, DP>(kf, kl, p.c);
+    split_frags<TT, DP>(kf, kl, p.c * p.down);
     // the first row that sees a key: of the workgroup's first, the wave's first and last, this lane's
-    auto begin = [&](int k) { return !CAUSAL ? 0 : min(rows, max(0, k - off) * p.g); };
+    auto begin = [&](int k) { return !CAUSAL ? 0 : min(lq, max(0, k - off)) * p.g; };
     const int first = begin(j.r0), first_lo = begin(kw), first_hi = begin(kw + 31), mine = begin(key);
     const int tb = first / BN, tiles = (rows + BN - 1) / BN - tb, per = (tiles + p.splits - 1) / p.splits;
     const int t0 = tb + j.split * per, t1 = min(tb + tiles, t0 + per);
@@ -961,7 +976,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
         stage.put(lds[buf][0], lds[buf][1]);
         if (int(threadIdx.x) < BN) {
             const float2 mf = from_stats<TT>(row >= 0 ? own_ml : float2{0.f, 0.f});
-            row_m[buf][threadIdx.x] = mf.x;
+            row_m[buf][threadIdx.x] = SP ? mf.x * p.down : mf.x;
             if constexpr (TT::E == 4) row_f[buf][threadIdx.x] = mf.y;
             row_d[buf][threadIdx.x] = row >= 0 ? -own_d : 0.f;
         }
@@ -1011,6 +1026,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
                     s = mfma32<TT>(a, kf[st], s);
                     if constexpr (SP) s = mfma32<TT>(a, kl[st], s);
                 }
+                scale_up<TT, DP>(s, p);
 #pragma unroll
                 for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(gt, 32 * u + col, 2 * st + h), vf[st], d);
 #pragma unroll

@@ -2,6 +2,8 @@
 // workgroups, workspaces.  The kernels are in attention.h.
 #include "attention.h"
 
+#include <math.h>
+
 namespace spc {
 namespace attn {
 namespace {
@@ -47,7 +49,7 @@ spc_status check_sizes(spc_dtype dtype, const spc_attention* a, Plan& w) {
     if (int64_t(a->heads) * a->head_dim > C_MAX) return fail(SPC_ERR_UNSUPPORTED, "%d heads of %d are too many", a->heads, a->head_dim);
     if (a->n_q * a->heads >= ROWS_END || a->n_kv * a->kv_heads >= ROWS_END)
         return fail(SPC_ERR_UNSUPPORTED, "rows x heads exceed 31 bits");
-    if (!(a->scale > 0.f && a->scale <= 3.402823466e38f)) return fail(SPC_ERR_ARG, "scale=%g must be positive and finite", double(a->scale));
+    if (!(a->scale > 0.f && a->scale <= 1e38f)) return fail(SPC_ERR_ARG, "scale=%g must be positive and at most 1e38", double(a->scale));
     const int64_t rows = a->n_q * (a->heads / a->kv_heads);
     w.q = cut_of(rows, a->n_kv, a->n_seg, a->kv_heads, a->head_dim);
     w.k = cut_of(a->n_kv, rows, a->n_seg, a->kv_heads, a->head_dim);
@@ -82,6 +84,9 @@ spc_status check_call(spc_dtype dtype, const spc_attention* a, const void* ws, s
     p.hk = a->kv_heads, p.g = a->heads / a->kv_heads, p.D = a->head_dim, p.causal = a->causal != 0;
     p.inv_g = p.g > 1 ? uint32_t(((uint64_t(1) << 32) + uint64_t(p.g) - 1) / uint64_t(p.g)) : 0u;
     p.scale = a->scale, p.c = float(double(a->scale) * 1.4426950408889634);
+    int e = 0;
+    if (dtype == SPC_F16) frexpf(p.c, &e);       // c is below 2^e
+    p.up = e > 0 ? ldexpf(1.f, e) : 1.f, p.down = 1.f / p.up;
     return SPC_OK;
 }
 

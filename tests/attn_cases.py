@@ -1,5 +1,7 @@
 """Shared inputs and checks of the attention tests."""
 
+import math
+
 import numpy as np
 import torch
 
@@ -18,11 +20,12 @@ FLOOR = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 
 #: Heads of up to 32 elements of a 16-bit type: scale log2(e) q is kept as hi + lo, two numbers of the
 #: type.  hi is off by up to half a step h of the product (2^-9 for bf16, 2^-11 for fp16) and lo, which is
 #: that remainder, by h of itself: h^2 of the product.  fp16's lo is off by 2^-25 at least (half its
-#: smallest number).
-def split_of(dtype, D):
+#: smallest number), and of scale log2(e) q above 1 a power of two stays outside.
+def split_of(dtype, D, scale=0.0):
     if dtype == torch.float32 or D > 32:
         return 0.0, 0.0
-    return half_step(dtype) ** 2, 2.0 ** -25 if dtype == torch.float16 else 0.0
+    outside = max(0, math.frexp(scale * math.log2(math.e))[1])
+    return half_step(dtype) ** 2, 2.0 ** (outside - 25) if dtype == torch.float16 else 0.0
 
 
 class Case:
@@ -55,7 +58,7 @@ class Case:
         return A.attention(self.q, self.k, self.v, self.q_ptr, self.kv_ptr, self.scale, self.causal, np_(self.order),
                            np_(self.kv_order), dout=self.dout if bwd else None,
                            step=half_step(self.dtype) if self.dtype != torch.float32 else 0.0, floor=FLOOR[self.dtype],
-                           split=split_of(self.dtype, self.D))
+                           split=split_of(self.dtype, self.D, self.scale))
 
     def kw(self):
         i32 = lambda v: cuda(torch.tensor(v, dtype=torch.int32))

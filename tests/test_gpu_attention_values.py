@@ -9,9 +9,9 @@ import sparse_convolution_hash_amd as spc
 from oracle import attnops as A
 from oracle.rowops import f64
 from sparse_convolution_hash_amd import binding as B
-from tests.attn_cases import Case, check
+from tests.attn_cases import FLOOR, Case, check
 from tests.parity import cuda
-from tests.rowops_cases import DTYPES
+from tests.rowops_cases import DTYPES, half_step, within
 
 pytestmark = pytest.mark.gpu
 
@@ -96,6 +96,86 @@ def test_lowest_values_as_a_mask():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lq,lk,H", [([70, 1], [300, 400], 1), ([600] * 16, None, 8), ([2], [3000], 2)])
+def test_first_keys_hidden(lq, lk, H, dtype):
+    """The first tiles of a walk hold no key that is there, and the scores after
+    them are far below 0: what a walk has summed up so far is nothing, not a
+    maximum of 0."""
+    for causal in (False, True):
+        c = Case(lq, lk, H, H, 16, dtype, seed=26, causal=causal, ordered=True, scale=1.0)
+        c.q[:, :, 0], c.k[:, :, 0] = 16.0, -16.0
+        order = (c.order if lk is None else c.kv_order).clone()
+        for a, b in zip(c.kv_ptr, c.kv_ptr[1:]):
+            order[a:min(b, a + 200)] = -1
+        c.kv_order = order
+        if lk is None:
+            c.order = order
+        check(c)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("n,lq,H", [(1, 64, 1), (16, 256, 8)])
+def test_rows_without_keys_next_to_growing_scores(n, lq, H, D, dtype):
+    """Rows that see no key walk the tiles together with rows whose scores grow
+    from one tile to the next by more than an exponent holds."""
+    c = Case([lq] * n, [lq + 246] * n, H, H, D, dtype, seed=29, causal=True, ordered=True, scale=1.0)
+    c.q[:, :, 0], c.k[:, :, 0] = 16.0, -16.0
+    for a, b in zip(c.kv_ptr, c.kv_ptr[1:]):
+        c.k[c.kv_order[a + 256:b].long(), :, 0] = 16.0
+        c.kv_order[a:a + 252] = -1         # rows 0 to 5 see none of the others, row 6 sees key 252
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D", [16, 64, 128])
+def test_rows_next_to_nan(D, causal, dtype):
+    """A query of NaN is NaN; those next to it, whose scores grow along the keys, are not touched."""
+    c = Case([70], [500], 2, 2, D, dtype, seed=30, causal=causal, scale=1.0)
+    c.q[:, :, 0], c.k[:, :, 0], c.k[130:, :, 0] = 16.0, -16.0, 16.0
+    ref = c.ref(False)
+    q, k, v, _ = c.on_gpu()
+    q = q.clone()
+    q[5] = float("nan")
+    out, _ = spc.attention_fwd(q, k, v, **c.kw())
+    rows = np.arange(70) != 5
+    assert out[5].isnan().all()
+    within(f64(out)[rows], ref["out"][rows], ref["e_out"][rows], dtype, "out")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,H", [(300, 1), (3000, 1), (9000, 8)])
+def test_scores_of_minus_infinity(n, H, dtype):
+    """Keys whose scores are minus infinity count for nothing, in the first
+    tiles of a walk and in whole parts of a split one; rows with no other score
+    are NaN."""
+    D = 32 if dtype == torch.float32 else 48       # narrow 16-bit heads give NaN
+    q = torch.ones(3, H, D, dtype=dtype)
+    g = torch.Generator().manual_seed(27)
+    k, v = (torch.randn(n, H, D, generator=g).to(dtype) for _ in range(2))
+    k[:n - 50, :, 0] = float("-inf")
+    out, stats = spc.attention_fwd(cuda(q), cuda(k), cuda(v), scale=0.25, want_stats=True)
+    r = A.attention(q, k[n - 50:], v[n - 50:], [0, 3], [0, 50], 0.25, step=half_step(dtype) if dtype != torch.float32 else 0.0,
+                    floor=FLOOR[dtype])
+    within(f64(out), r["out"], r["e_out"], dtype, "out")
+    assert stats[0].isfinite().all()
+    out, stats = spc.attention_fwd(cuda(q), cuda(k[:n - 50]), cuda(v[:n - 50]), scale=0.25, want_stats=True)
+    assert out.isnan().all() and stats[0][..., 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scale", [1e-3, 0.9, 3.0])
+def test_scales(scale, dtype):
+    # above c = scale log2(e) = 1, 60,000 c is no number of fp16
+    c = Case([70, 9], None, 2, 1, 16, dtype, seed=28, scale=scale)
+    check(c)
+    if dtype == torch.float16 and scale > 1:
+        c.q[3], c.k[3] = 60000.0, 0.0
+        check(c, bwd=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_strides(dtype):
     """Rows of wider tensors for every argument, gradients into one tensor."""
     c = Case([30, 50], None, 4, 2, 32, dtype, seed=23, causal=True)
@@ -171,6 +251,8 @@ def test_refusals_of_the_binding():
         spc.attention_fwd(q, k.half(), k)
     with pytest.raises(TypeError):
         spc.attention_fwd(q, k, k, ptr.long())
+    with pytest.raises(TypeError):
+        spc.attention_bwd(q, q, k, k, q, spc.attention_fwd(q, k, k)[1])             # a forward without stats
     for kw in (dict(scale=0.0), dict(scale=float("inf"))):
         with pytest.raises(spc.SpcError):
             spc.attention_fwd(q, k, k, **kw)
