@@ -332,6 +332,7 @@ extern "C" spc_status spc_layer_norm_fwd(spc_dtype dtype, const void* x, const v
     if (st != SPC_OK) return st;
     if (!(eps > 0.f)) return fail(SPC_ERR_ARG, "eps=%g must be positive", double(eps));
     if (!residual != !total) return fail(SPC_ERR_ARG, "residual and total: give both or neither");
+    if (total && total == y && n > 0) return fail(SPC_ERR_ARG, "y and total are the same rows");
     for (const void* q : {x, residual, (const void*)gamma, (const void*)beta, (const void*)y, (const void*)total, (const void*)stats})
         if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     if (n == 0) return SPC_OK;

@@ -33,6 +33,7 @@ def test_layer_norm_refusals():
     assert fwd(n=0) == fwd(n=0, x=None, y=None, s=None) == B.SPC_OK
     assert fwd(y=None) == fwd(y=ODD) == fwd(b=ODD) == fwd(eps=0.0) == fwd(eps=float("nan")) == B.SPC_ERR_ARG
     assert fwd(r=P) == fwd(t=P) == fwd(r=ODD, t=P) == fwd(r=P, t=ODD) == B.SPC_ERR_ARG     # both or neither
+    assert fwd(r=ctypes.c_void_p(0x200000), t=P) == B.SPC_ERR_ARG                          # total over y
     assert bwd(n=0, dg=None, db=None, dy=None, x=None, dx=None, s=None) == B.SPC_OK
     assert bwd(dy=None) == bwd(dx=None) == bwd(dx=ODD) == bwd(dt_=ODD) == bwd(dg=ODD) == bwd(db=ODD) == B.SPC_ERR_ARG
     assert bwd(ws=None) == bwd(ws=ODD) == B.SPC_ERR_ARG
