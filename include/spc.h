@@ -656,11 +656,12 @@ spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size
  * rest (NULL ok; 16-bit dtypes, unused for fp32), dense [n_q, heads, head_dim]
  * of the dtype, receives what the rounding to out left of the result, for the
  * backward.
- * Where head_dim <= 32, 16-bit dtypes multiply scale log2(e) into one factor
- * of s, kept as two numbers of the type: s is off by up to 2^-18 (bf16) or
- * 2^-22 (fp16) of scale sum_d |q_id k_jd|.  A NaN or infinity in a row that is
- * seen may make everything NaN that depends on it, and so may scores s above
- * 10^8 in size, of which fp32 keeps no fractions.  out overlaps no input.
+ * Where head_dim <= 32, 16-bit dtypes (fp16 up to a scale of 0.69) multiply
+ * scale log2(e) into one factor of s, kept as two numbers of the type: s is off
+ * by up to 2^-18 (bf16) or 2^-22 (fp16) of scale sum_d |q_id k_jd|.  A NaN or
+ * infinity in a row that is seen may make everything NaN that depends on it,
+ * and so may scores s above 10^8 in size, of which fp32 keeps no fractions.
+ * out overlaps no input.
  * Rows of no sample are written in none of the outputs.
  */
 spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a, const void* q, int64_t ldq, const void* k,

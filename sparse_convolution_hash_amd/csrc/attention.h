@@ -16,6 +16,15 @@
 // over the rows in the order in which the registers hold them, as long as the
 // left operand comes in the same one, and the transposing LDS read
 // (ds_read_b64_tr_b16) gives it so from rows as they were stored.
+//
+// Windows of 1,024 on 266,426 x 4 x 32 bf16, where the exponentials and the
+// packing keep the vector unit busy and not memory: forward 331 us (140 GFLOP
+// in the two products, 420 TFLOP/s), k_attn_dq 379 (three products, 210 GFLOP),
+// k_attn_dkv 502 (four, 279 GFLOP).  Causal 16,411 x 8 heads
+// over 2 x 128 bf16: forward 716 us, 552 GFLOP, 770 TFLOP/s (matrix
+// unit busy for 32% of its cycles, vector unit for 45%, two waves a SIMD to cover
+// each other's waits).  fp32, 5,003 x 6 x 48 ragged and causal: 128, 151 and 244
+// us, one wave a SIMD, the matrix unit busy for half of its cycles.
 #pragma once
 
 #include "rows.h"
@@ -35,7 +44,6 @@ struct Args {
     Segs qs, ks;
     int32_t g, hk, D, causal;               // query heads to a key head, key heads, head dimension
     uint32_t inv_g;                         // 2^32 / g, rounded up (g > 1)
-    float up, down;                         // a power of two and its inverse: see SPLIT
     float c, scale;                         // c = scale log2(e)
     float2* stats;                          // [heads, n_q] (m, l)
     float* delta;                           // [heads, n_q] do . o
@@ -372,16 +380,8 @@ __device__ __forceinline__ void load_frags(u32x4* f, const char* row, bool there
 // over DP) than they save: 64 cycles for DP / 16 products of 32 on each tile.
 // An infinite key meets both numbers, and inf - inf is NaN where the plain
 // product gives minus infinity.
-// fp16 numbers end at 65,504: above c = 1 the operand is multiplied by c / up, a
-// factor of at most 1, and the exponent by up, a power of two (1 otherwise).
 template <typename TT, int DP>
 constexpr bool SPLIT = TT::E == 8 && DP <= 32;
-
-template <typename TT, int DP>
-__device__ __forceinline__ void scale_up(f32x16_t& s, const Args& p) {
-    if constexpr (SPLIT<TT, DP> && TT::id == SPC_F16)
-        if (p.up != 1.f) s *= p.up;
-}
 
 // f times c as f + lo (lo has entries where the product is split).
 template <typename TT, int DP>
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
     const Query q = query_of(p, j, j.a, rw + col, rows);
     u32x4 qf[T::NS], ql[SP ? T::NS : 1];
     load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + int64_t(q.head) * p.D * T::ES, q.row >= 0, p.D, h);
-    split_frags<TT, DP>(qf, ql, p.c * p.down);
+    split_frags<TT, DP>(qf, ql, p.c);
     // keys that the workgroup's last row, the wave's first and its last see
     auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
     const int nk = limit(j.r0 + BM - 1), seen_first = rw < rows ? limit(rw) : 0, seen_last = rw < rows ? limit(rw + 31) : 0;
@@ -610,7 +610,6 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                         s[u] = mfma32<TT>(a, qf[st], s[u]);
                         if constexpr (SP) s[u] = mfma32<TT>(a, ql[st], s[u]);
                     }
-                    scale_up<TT, DP>(s[u], p);
                 }
                 if (edge) {
 #pragma unroll
@@ -637,7 +636,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
 #pragma unroll
                         for (int u = 0; u < KT; ++u) s[u] -= d;
                         m = !grew ? m : none ? top : m + top;
-                        from = all16(m == -INFINITY ? 0.f : -m * p.down);
+                        from = all16(m == -INFINITY ? 0.f : -m);
                     } else if (grew) {
                         a = none ? 0.f : exp2_(m - top * p.c);
                         m = top * p.c;
@@ -821,7 +820,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
         delta = sum_halves(delta);
     }
     load_frags<TT, DP>(qf, p.q + int64_t(q.row) * p.ldq + in, q.row >= 0, p.D, h);
-    split_frags<TT, DP>(qf, ql, p.c * p.down);
+    split_frags<TT, DP>(qf, ql, p.c);
     if (q.row >= 0 && h == 0 && j.split == 0) p.delta[id] = delta;
     const float2 mf = from_stats<TT>(q.row >= 0 ? p.stats[id] : float2{0.f, 0.f});
     auto limit = [&](int r) { return !CAUSAL ? lk : max(0, min(lk, (r < rows ? r : rows - 1) / p.g + 1 + off)); };
@@ -832,7 +831,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
 
     KeyStage<TT, DP, BN, NT> stage;
     stage.begin(p, j, ka, lk);
-    const f32x16_t from_s = SP ? all16(mf.x * p.down) : zero16(), from_d = all16(-delta);   // what the products start from
+    const f32x16_t from_s = SP ? all16(mf.x) : zero16(), from_d = all16(-delta);   // what the products start from
     f32x16_t acc[T::NB];
 #pragma unroll
     for (int db = 0; db < T::NB; ++db) acc[db] = zero16();
@@ -864,7 +863,6 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
                     s = mfma32<TT>(a, qf[st], s);
                     if constexpr (SP) s = mfma32<TT>(a, ql[st], s);
                 }
-                scale_up<TT, DP>(s, p);
 #pragma unroll
                 for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(vt, 32 * u + col, 2 * st + h), gf[st], d);
 #pragma unroll
@@ -933,7 +931,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
     u32x4 kf[T::NS], kl[SP ? T::NS : 1], vf[T::NS];
     load_frags<TT, DP>(kf, p.k + int64_t(krow) * p.ldk + in, krow >= 0, p.D, h);
     load_frags<TT, DP>(vf, p.v + int64_t(krow) * p.ldv + in, krow >= 0, p.D, h);
-    split_frags<TT, DP>(kf, kl, p.c * p.down);
+    split_frags<TT, DP>(kf, kl, p.c);
     // the first row that sees a key: of the workgroup's first, the wave's first and last, this lane's
     auto begin = [&](int k) { return !CAUSAL ? 0 : min(lq, max(0, k - off)) * p.g; };
     const int first = begin(j.r0), first_lo = begin(kw), first_hi = begin(kw + 31), mine = begin(key);
@@ -976,7 +974,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
         stage.put(lds[buf][0], lds[buf][1]);
         if (int(threadIdx.x) < BN) {
             const float2 mf = from_stats<TT>(row >= 0 ? own_ml : float2{0.f, 0.f});
-            row_m[buf][threadIdx.x] = SP ? mf.x * p.down : mf.x;
+            row_m[buf][threadIdx.x] = mf.x;
             if constexpr (TT::E == 4) row_f[buf][threadIdx.x] = mf.y;
             row_d[buf][threadIdx.x] = row >= 0 ? -own_d : 0.f;
         }
@@ -1026,7 +1024,6 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
                     s = mfma32<TT>(a, kf[st], s);
                     if constexpr (SP) s = mfma32<TT>(a, kl[st], s);
                 }
-                scale_up<TT, DP>(s, p);
 #pragma unroll
                 for (int st = 0; st < T::NS; ++st) d = mfma32<TT>(T::row16(gt, 32 * u + col, 2 * st + h), vf[st], d);
 #pragma unroll

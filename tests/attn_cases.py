@@ -20,12 +20,11 @@ FLOOR = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 
 #: Heads of up to 32 elements of a 16-bit type: scale log2(e) q is kept as hi + lo, two numbers of the
 #: type.  hi is off by up to half a step h of the product (2^-9 for bf16, 2^-11 for fp16) and lo, which is
 #: that remainder, by h of itself: h^2 of the product.  fp16's lo is off by 2^-25 at least (half its
-#: smallest number), and of scale log2(e) q above 1 a power of two stays outside.
+#: smallest number), and its heads are not split where scale log2(e) is above 1.
 def split_of(dtype, D, scale=0.0):
-    if dtype == torch.float32 or D > 32:
+    if dtype == torch.float32 or D > 32 or dtype == torch.float16 and scale * math.log2(math.e) > 1:
         return 0.0, 0.0
-    outside = max(0, math.frexp(scale * math.log2(math.e))[1])
-    return half_step(dtype) ** 2, 2.0 ** (outside - 25) if dtype == torch.float16 else 0.0
+    return half_step(dtype) ** 2, 2.0 ** -25 if dtype == torch.float16 else 0.0
 
 
 class Case:
