@@ -18,9 +18,9 @@
 // (ds_read_b64_tr_b16) gives it so from rows as they were stored.
 //
 // Windows of 1,024 on 266,426 x 4 x 32 bf16, where the exponentials and the
-// packing keep the vector unit busy and not memory: forward 331 us (140 GFLOP
-// in the two products, 420 TFLOP/s), k_attn_dq 379 (three products, 210 GFLOP),
-// k_attn_dkv 502 (four, 279 GFLOP).  Causal 16,411 x 8 heads
+// packing keep the vector unit busy and not memory: forward 344 us (140 GFLOP
+// in the two products, 410 TFLOP/s), k_attn_dq 490 (three products, 210 GFLOP),
+// k_attn_dkv 515 (four, 279 GFLOP).  Causal 16,411 x 8 heads
 // over 2 x 128 bf16: forward 716 us, 552 GFLOP, 770 TFLOP/s (matrix
 // unit busy for 32% of its cycles, vector unit for 45%, two waves a SIMD to cover
 // each other's waits).  fp32, 5,003 x 6 x 48 ragged and causal: 128, 151 and 244
@@ -212,6 +212,35 @@ struct Second {
         for (int t = 0; t < STEPS; ++t)
 #pragma unroll
             for (int db = 0; db < T::NB; ++db) acc[db] = step(left(x, row0, t, db, lane), w.b[t], acc[db]);
+    }
+
+    // The same with w as the sum of two numbers of the type: for dq of narrow
+    // heads, whose matrix unit has room for it.  ds sums to 0 over a row, so its
+    // rounding counts for more than that of p: windows of 1,024 on 266,426 x 4 x
+    // 32 bf16 trained in 1,170 us with a relative error of dq below 2.4e-3, in
+    // 1,095 us with 2.6e-3 where ds is rounded once.  Tiles at a causal mask's
+    // edge keep one number.
+    static __device__ __forceinline__ void add_split(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w, int lane) {
+        const Packed hi(w);
+        Packed lo;
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t) {
+            Raw8<TT> r;
+            r.v[0] = hi.b[t];
+            const f32x8_t f = widen<TT>(r);
+            f32x8_t v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = w[t * PER + e] - f[e];
+            lo.b[t] = narrow<TT>(v).v[0];
+        }
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+            for (int db = 0; db < T::NB; ++db) {
+                const u32x4 a = left(x, row0, t, db, lane);
+                acc[db] = step(a, hi.b[t], acc[db]);
+                acc[db] = step(a, lo.b[t], acc[db]);
+            }
     }
 
     // The finite elements of a left operand, the others 0.
@@ -881,7 +910,8 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
                         continue;
                     }
                 }
-                X::add(acc, kt, 32 * u, typename X::Packed(s), lane);
+                if constexpr (SP) X::add_split(acc, kt, 32 * u, s, lane);
+                else X::add(acc, kt, 32 * u, typename X::Packed(s), lane);
             }
         }
         if (more) stage.put(lds[buf ^ 1][0], lds[buf ^ 1][1]);
