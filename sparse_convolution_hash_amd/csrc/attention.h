@@ -619,9 +619,9 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
             // sums to more than LAZY, the scores are computed once more (the
             // tile is still there) for a new maximum.  A column without one
             // (the first tile, or hidden keys and scores of minus infinity so
-            // far) takes it before anything is exponentiated.  Columns next to
-            // such a one may still need the second round; without a causal mask
-            // all columns see the same keys.
+            // far, as a query with an infinity may have along the whole walk)
+            // takes it before anything is exponentiated.  Columns next to such a
+            // one may still need the second round.
             using X = Second<TT, DP>;
             f32x16_t s[KT];
             typename X::Packed w[KT];
@@ -686,7 +686,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                     w[u] = typename X::Packed(s[u]);
                 }
                 sum = (part[0] + part[1]) + (part[2] + part[3]);
-                if ((CAUSAL ? last : fresh) || !__any(sum > LAZY)) break;
+                if (last || !__any(sum > LAZY)) break;
                 last = fresh = true;
             }
             l += sum;
