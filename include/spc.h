@@ -656,9 +656,9 @@ spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size
  * rest (NULL ok; 16-bit dtypes, unused for fp32), dense [n_q, heads, head_dim]
  * of the dtype, receives what the rounding to out left of the result, for the
  * backward.
- * Where head_dim <= 32, 16-bit dtypes (fp16 up to a scale of 0.69) multiply
- * scale log2(e) into one factor of s, kept as two numbers of the type: s is off
- * by up to 2^-18 (bf16) or 2^-22 (fp16) of scale sum_d |q_id k_jd|.  A NaN or
+ * Where head_dim <= 32, bf16 multiplies scale log2(e) into one factor of s (q
+ * here, k for dk and dv), kept as two numbers of the type: s is off by up to
+ * 2^-18 of scale sum_d |q_id k_jd|, and that factor must not pass 3.3e38.  A NaN or
  * infinity in a row that is seen may make everything NaN that depends on it,
  * and so may scores s above 10^8 in size, of which fp32 keeps no fractions.
  * out overlaps no input.

@@ -402,15 +402,21 @@ __device__ __forceinline__ void load_frags(u32x4* f, const char* row, bool there
 
 // Narrow heads of 16-bit types spend their time in the vector unit, a score's
 // multiplication by c and subtraction of m among it, and leave the matrix unit
-// idle.  There the column operand is multiplied by c once, kept as the sum of
-// two numbers of the type (off by 2^-18 of itself for bf16, 2^-22 for fp16), and
-// the product starts from -m, so that the matrix unit hands over the exponent
-// itself.  Wider heads would pay more in the matrix unit (a second product
-// over DP) than they save: 64 cycles for DP / 16 products of 32 on each tile.
+// idle.  For bf16 the column operand is multiplied by c once, kept as the sum of
+// two numbers of the type (off by 2^-18 of itself), and the product starts from
+// -m, so that the matrix unit hands over the exponent itself.  Wider heads would
+// pay more in the matrix unit (a second product over DP) than they save: 64
+// cycles for DP / 16 products of 32 on each tile.  fp16 has not the range: the
+// second number is below its smallest, 2^-24, as soon as the factor is below
+// 2^-3, and the product above its largest where c is above 1.
 // An infinite key meets both numbers, and inf - inf is NaN where the plain
 // product gives minus infinity.
 template <typename TT, int DP>
-constexpr bool SPLIT = TT::E == 8 && DP <= 32;
+constexpr bool SPLIT = TT::id == SPC_BF16 && DP <= 32;
+
+// Where dq takes ds as two numbers of the type.
+template <typename TT, int DP>
+constexpr bool TWO = TT::E == 8 && DP <= 32;
 
 // f times c as f + lo (lo has entries where the product is split).
 template <typename TT, int DP>
@@ -910,7 +916,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
                         continue;
                     }
                 }
-                if constexpr (SP) X::add_split(acc, kt, 32 * u, s, lane);
+                if constexpr (TWO<TT, DP>) X::add_split(acc, kt, 32 * u, s, lane);
                 else X::add(acc, kt, 32 * u, typename X::Packed(s), lane);
             }
         }
@@ -1203,10 +1209,8 @@ constexpr int few_waves(int D) { return D <= 64 ? 1 : 2; }
 
 #define ATTN_WIDTHS(name, nw, grid, p)                                                                                        \
     do {                                                                                                                      \
-        /* c above 1 could take a large fp16 number past the type's range when it is multiplied: no split then */             \
-        const bool split = TT::id != SPC_F16 || p.c <= 1.f;                                                                   \
-        if (p.D <= 16 && split) ATTN_WIDTH(name, 16, nw, grid, p);                                                            \
-        else if (p.D <= 32 && split) ATTN_WIDTH(name, 32, nw, grid, p);                                                       \
+        if (p.D <= 16) ATTN_WIDTH(name, 16, nw, grid, p);                                                                     \
+        else if (p.D <= 32) ATTN_WIDTH(name, 32, nw, grid, p);                                                                \
         else if (TT::E == 4 && p.D <= 48) ATTN_WIDTH(name, (TT::E == 4 ? 48 : 64), nw, grid, p);                              \
         else if (p.D <= 64) ATTN_WIDTH(name, 64, nw, grid, p);                                                                \
         else ATTN_WIDTH(name, 128, (nw == 1 ? few_waves(128) : nw), grid, p);                                                 \
