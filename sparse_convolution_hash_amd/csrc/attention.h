@@ -558,7 +558,21 @@ constexpr int FWD_WAVES = TT::E == 4 ? 1 : DP <= 32 ? 4 - CAUSAL : DP <= 64 ? 3 
 template <typename TT, int DP>
 constexpr int BWD_WAVES = TT::E == 4 ? 1 : DP <= 32 ? 3 : DP <= 64 ? 2 : 1;
 
-constexpr float LAZY = 1024.f;   // far below fp16's largest number, which a single p may not pass
+// Probabilities that are rounded to fp16 are held times a power of two, since
+// below 2^-14 the type keeps no more than its smallest number, 2^-24: where a key
+// outweighs many others by 2^20, their sum was off by 1%.  The forward's (relative
+// to a maximum that may be LAZY below the row's own) have 5 binades above it, the
+// backward's, at most 1, have 15; sums (and l) carry the power along.
+template <typename TT>
+constexpr float FWD_UP = TT::id == SPC_F16 ? 5.f : 0.f;
+template <typename TT>
+constexpr float BWD_UP = TT::id == SPC_F16 ? 15.f : 0.f;
+
+// The sum of a tile's probabilities (of half a column) from which a new maximum
+// is taken: 1,024 times the maximum's own, below fp16's largest, 65,504, which a
+// single one may not pass.
+template <typename TT>
+constexpr float LAZY = TT::id == SPC_F16 ? 32768.f : 1024.f;
 
 template <typename TT, int DP, int NW, bool CAUSAL>
 __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_fwd(const Args p) {
@@ -663,7 +677,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                     const float2 both = halves(top), sums = halves(sum);
                     top = fmaxf(both.x, both.y);
                     // the other columns keep their sums to the bit
-                    const bool none = m == -INFINITY, grew = top > -INFINITY && (none || sums.x > LAZY || sums.y > LAZY);
+                    const bool none = m == -INFINITY, grew = top > -INFINITY && (none || sums.x > LAZY<TT> || sums.y > LAZY<TT>);
                     float a = 1.f;
                     if constexpr (SP) {    // s is c s - m already
                         const float d = grew ? top : 0.f;
@@ -673,8 +687,9 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                         m = !grew ? m : none ? top : m + top;
                         from = all16(m == -INFINITY ? 0.f : -m);
                     } else if (grew) {
-                        a = none ? 0.f : exp2_(m - top * p.c);
-                        m = top * p.c;
+                        const float was = m;
+                        m = top * p.c - FWD_UP<TT>;
+                        a = none ? 0.f : exp2_(was - m);
                     }
                     l *= a;
 #pragma unroll
@@ -692,7 +707,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                     w[u] = typename X::Packed(s[u]);
                 }
                 sum = (part[0] + part[1]) + (part[2] + part[3]);
-                if (last || !__any(sum > LAZY)) break;
+                if (last || !__any(sum > LAZY<TT>)) break;
                 last = fresh = true;
             }
             l += sum;
@@ -1049,13 +1064,14 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
         stage.put(lds[buf][0], lds[buf][1]);
         if (int(threadIdx.x) < BN) {
             const float2 mf = from_stats<TT>(row >= 0 ? own_ml : float2{0.f, 0.f});
-            row_m[buf][threadIdx.x] = mf.x;
+            row_m[buf][threadIdx.x] = mf.x + BWD_UP<TT>;
             if constexpr (TT::E == 4) row_f[buf][threadIdx.x] = mf.y;
             row_d[buf][threadIdx.x] = row >= 0 ? -own_d : 0.f;
         }
     };
 
-    float fk = DS_FACTOR;          // what ds is held times (RANGED)
+    constexpr float P_FACTOR = TT::id == SPC_F16 ? 32768.f : 1.f;     // 2^BWD_UP, what p is held times
+    float fk = DS_FACTOR / P_FACTOR;       // what ds is held times beside it (RANGED)
     f32x16_t dk[T::NB], dv[T::NB];
 #pragma unroll
     for (int db = 0; db < T::NB; ++db) dk[db] = zero16(), dv[db] = zero16();
@@ -1146,7 +1162,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dkv(const
     if (krow < 0) return;
     if constexpr (RANGED<TT>) {
 #pragma unroll
-        for (int db = 0; db < T::NB; ++db) dk[db] *= 1.f / fk;
+        for (int db = 0; db < T::NB; ++db) dk[db] *= 1.f / (fk * P_FACTOR), dv[db] *= 1.f / P_FACTOR;
     }
     if (p.splits > 1) {
         float* part = p.part + (int64_t(j.split) * p.ks.n * p.hk + int64_t(j.head) * p.ks.n + krow) * (2 * p.D);
