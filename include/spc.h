@@ -654,8 +654,8 @@ spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size
  * stats fp32 [heads, n_q, 2] (NULL ok) receives (m, l) for the backward: the
  * log of the row's sum of exp(s) is (m + log2 l) ln 2; l = 0: no key is seen.
  * rest (NULL ok; 16-bit dtypes, unused for fp32), dense [n_q, heads, head_dim]
- * of the dtype, receives what the rounding to out left of the result, for the
- * backward.
+ * of the dtype, receives what the rounding to out left of the result (fp16: times
+ * 2^11), for the backward.
  * Where head_dim <= 32, bf16 multiplies scale log2(e) into one factor of s (q
  * here, k for dk and dv), kept as two numbers of the type: s is off by up to
  * 2^-18 of scale sum_d |q_id k_jd|, and that factor must not pass 3.3e38.  A NaN or

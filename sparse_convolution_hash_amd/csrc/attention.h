@@ -107,7 +107,10 @@ __device__ __forceinline__ void put4(char* p, f32x4_t v) {
     }
 }
 
-// What that rounding left of v, rounded itself.
+// What that rounding left of v, to be rounded itself; times 2^11 for fp16, where
+// it comes to at most v and does not end among the type's smallest numbers.
+template <typename TT>
+constexpr float REST_UP = TT::id == SPC_F16 ? 2048.f : 1.f;
 template <typename TT>
 __device__ __forceinline__ f32x4_t left_of(f32x4_t v) {
     if constexpr (TT::id == SPC_BF16) {
@@ -115,7 +118,7 @@ __device__ __forceinline__ f32x4_t left_of(f32x4_t v) {
         return v - __builtin_convertvector(__builtin_convertvector(v, b4), f32x4_t);
     } else if constexpr (TT::id == SPC_F16) {
         typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-        return v - __builtin_convertvector(__builtin_convertvector(v, h4), f32x4_t);
+        return (v - __builtin_convertvector(__builtin_convertvector(v, h4), f32x4_t)) * REST_UP<TT>;
     } else {
         return f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
@@ -886,7 +889,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
             if constexpr (TT::E == 8) {
                 Raw8<TT> x, y, z;
                 x.v[0] = of[s], y.v[0] = gf[s], z.v[0] = ol[s];
-                const f32x8_t a = widen<TT>(x) + widen<TT>(z), b = widen<TT>(y);
+                const f32x8_t a = widen<TT>(x) + widen<TT>(z) * (1.f / REST_UP<TT>), b = widen<TT>(y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
             } else {
