@@ -675,10 +675,10 @@ spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a, const void
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
  * with the sums of dk and dv over all heads that share a key head.  p and ds
  * are rounded to the dtype for their products, fp16's ds times a power of two that
- * keeps its range (16-bit heads up to 32: dq takes
- * ds as two numbers of the type, but for tiles at a causal mask's edge).  rest NULL: dout . out is that
- * of the rounded out, and where one key outweighs the others ds loses the
- * precision that the difference cancels.  dq, dk, dv overlap no input.
+ * keeps its range (16-bit heads up to 32: dq takes ds as two numbers of the type).
+ * rest NULL: dout . out is that of the rounded out, and where one key outweighs
+ * the others ds loses the precision that the difference cancels.  dq, dk, dv
+ * overlap no input.
  * Rows of no sample are not written.
  */
 spc_status spc_attention_bwd(spc_dtype dtype, const spc_attention* a, const void* dout, int64_t lddo, const void* q,

@@ -217,32 +217,35 @@ struct Second {
             for (int db = 0; db < T::NB; ++db) acc[db] = step(left(x, row0, t, db, lane), w.b[t], acc[db]);
     }
 
-    // The same with w as the sum of two numbers of the type: for dq of narrow
-    // heads, whose matrix unit has room for it.  ds sums to 0 over a row, so its
-    // rounding counts for more than that of p: windows of 1,024 on 266,426 x 4 x
-    // 32 bf16 trained in 1,170 us with a relative error of dq below 2.4e-3, in
-    // 1,095 us with 2.6e-3 where ds is rounded once.  Tiles at a causal mask's
-    // edge keep one number.
-    static __device__ __forceinline__ void add_split(f32x16_t (&acc)[T::NB], const char* x, int row0, const f32x16_t& w, int lane) {
-        const Packed hi(w);
-        Packed lo;
+    // w as the sum of two numbers of the type: for dq of narrow heads, whose
+    // matrix unit has room for it.  ds sums to 0 over a row, so its rounding
+    // counts for more than that of p: windows of 1,024 on 266,426 x 4 x 32 bf16
+    // trained in 1,170 us with a relative error of dq below 2.4e-3, in 1,095 us
+    // with 2.6e-3 where ds is rounded once.
+    struct Two {
+        Packed hi, lo;
+        __device__ __forceinline__ explicit Two(const f32x16_t& w) : hi(w) {
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-            Raw8<TT> r;
-            r.v[0] = hi.b[t];
-            const f32x8_t f = widen<TT>(r);
-            f32x8_t v;
+            for (int t = 0; t < STEPS; ++t) {
+                Raw8<TT> r;
+                r.v[0] = hi.b[t];
+                const f32x8_t f = widen<TT>(r);
+                f32x8_t v;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = w[t * PER + e] - f[e];
-            lo.b[t] = narrow<TT>(v).v[0];
+                for (int e = 0; e < 8; ++e) v[e] = w[t * PER + e] - f[e];
+                lo.b[t] = narrow<TT>(v).v[0];
+            }
         }
+    };
+
+    static __device__ __forceinline__ void add(f32x16_t (&acc)[T::NB], const char* x, int row0, const Two& w, int lane) {
 #pragma unroll
         for (int t = 0; t < STEPS; ++t)
 #pragma unroll
             for (int db = 0; db < T::NB; ++db) {
                 const u32x4 a = left(x, row0, t, db, lane);
-                acc[db] = step(a, hi.b[t], acc[db]);
-                acc[db] = step(a, lo.b[t], acc[db]);
+                acc[db] = step(a, w.hi.b[t], acc[db]);
+                acc[db] = step(a, w.lo.b[t], acc[db]);
             }
     }
 
@@ -310,6 +313,17 @@ struct Second {
                     for (int r = 0; r < 16; ++r) acc[db][r] += n[r] > 0.f ? v : 0.f;
                 }
         }
+    }
+    // Without OTHERS, for w as two numbers.
+    static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const Two& w, int lane) {
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+            for (int db = 0; db < T::NB; ++db) {
+                const u32x4 a = finite(left(x, row0, t, db, lane));
+                acc[db] = step(a, w.hi.b[t], acc[db]);
+                acc[db] = step(a, w.lo.b[t], acc[db]);
+            }
     }
 };
 
@@ -963,14 +977,15 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
                     for (int r = 0; r < 16; ++r) s[r] = (vis >> bit_of(r)) & 1u ? s[r] : 0.f;
                 }
                 if constexpr (RANGED<TT>) into_range(s, acc, f);
-                if (edge) {
-                    if constexpr (CAUSAL) {
-                        X::template add_masked<false>(acc, kt, 32 * u, typename X::Packed(s), vis, lane);
-                        continue;
-                    }
+                if constexpr (TWO<TT, DP>) {
+                    const typename X::Two w(s);
+                    if (CAUSAL && edge) X::add_masked(acc, kt, 32 * u, w, lane);
+                    else X::add(acc, kt, 32 * u, w, lane);
+                } else {
+                    const typename X::Packed w(s);
+                    if (CAUSAL && edge) X::template add_masked<false>(acc, kt, 32 * u, w, vis, lane);
+                    else X::add(acc, kt, 32 * u, w, lane);
                 }
-                if constexpr (TWO<TT, DP>) X::add_split(acc, kt, 32 * u, s, lane);
-                else X::add(acc, kt, 32 * u, typename X::Packed(s), lane);
             }
         }
         if (more) stage.put(lds[buf ^ 1][0], lds[buf ^ 1][1]);
