@@ -1,6 +1,7 @@
 // Rotary positions of several axes: pair j of a head, elements 2j and 2j + 1,
 // belongs to one axis of the row's position and is rotated by the angle
-// position * freq[j]; pairs past the axes' stay as they are.
+// position * freq[j]; pairs past the axes' are copied as they are stored (a
+// rotation by 0 would multiply infinities by 0).
 //
 // A workgroup computes the sines and cosines of its rows once into LDS, for
 // all heads, and then walks the rows' chunks of 8 elements in memory order,
@@ -35,6 +36,20 @@ struct RotArgs {
     float sign;                   // -1: the rotation back
 };
 
+constexpr float COPIED = 2.f;     // the cosine of a pair past the axes in the table
+
+// Those pairs of a chunk as they were in x.
+template <typename TT>
+__device__ __forceinline__ void keep_pairs(Raw8<TT>& y, const Raw8<TT>& x, const float2* t) {
+    constexpr int W = 8 / TT::E;      // words of a pair
+    uint32_t a[4 * W], b[4 * W];
+    __builtin_memcpy(a, &y, sizeof(a));
+    __builtin_memcpy(b, &x, sizeof(b));
+#pragma unroll
+    for (int i = 0; i < 4 * W; ++i) a[i] = t[i / W].x == COPIED ? b[i] : a[i];
+    __builtin_memcpy(&y, a, sizeof(a));
+}
+
 template <typename TT>
 __global__ __launch_bounds__(RT) void k_rotary(const RotArgs p) {
     __shared__ __attribute__((aligned(16))) float2 table[TABLE];
@@ -43,7 +58,7 @@ __global__ __launch_bounds__(RT) void k_rotary(const RotArgs p) {
     const int rows = int(p.n - row0 < p.rows ? p.n - row0 : p.rows), half = p.D / 2;
     for (int e = int(threadIdx.x); e < rows * half; e += RT) {
         const int r = e / half, j = e - r * half;
-        float2 cs = {1.f, 0.f};
+        float2 cs = {COPIED, 0.f};
         if (j < p.pairs) {
             int axis = 0;
             while (j >= p.end[axis]) ++axis;
@@ -84,7 +99,9 @@ __global__ __launch_bounds__(RT) void k_rotary(const RotArgs p) {
                 v[2 * i] = fmaf(a, cs.x, -(b * cs.y));
                 v[2 * i + 1] = fmaf(a, cs.y, b * cs.x);
             }
-            st8<TT>(p.out + to[k], narrow<TT>(v));
+            Raw8<TT> y = narrow<TT>(v);
+            if (p.pairs < half) keep_pairs<TT>(y, x[k], t);
+            st8<TT>(p.out + to[k], y);
         }
     }
 }
