@@ -612,8 +612,8 @@ spc_status spc_layer_norm_bwd(spc_dtype dtype, const void* dout, const void* x, 
  * and pairs past these are copied.  pos int32, aligned to 4 bytes (the
  * coordinates' columns 1 to 3 are the axes z, y, x), freq fp32 [sum of pairs]
  * in radians.  inverse != 0 rotates by -t, which is the gradient.  Angles lose
- * nothing at far positions (products in double).  out: rows ldo elements
- * apart; it may be x with ldo = ldx.
+ * nothing at far positions (products as sums of two doubles).  out: rows ldo
+ * elements apart; it may be x with ldo = ldx.
  */
 spc_status spc_rotary(spc_dtype dtype, const void* x, int64_t ldx, int64_t n, int32_t heads, int32_t head_dim,
                       const int32_t* pos, int64_t ldp, int32_t n_axes, const int32_t* pairs, const float* freq,

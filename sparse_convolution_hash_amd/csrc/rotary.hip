@@ -6,9 +6,10 @@
 // A workgroup computes the sines and cosines of its rows once into LDS, for
 // all heads, and then walks the rows' chunks of 8 elements in memory order,
 // reading and writing every line once.  Angles: the product of the int32
-// position and the fp32 frequency is taken in double, in quarter turns, so a
-// position of 2^31 loses nothing; what is left of it, at most an eighth of a
-// turn, goes to fp32.
+// position and the fp32 frequency, and its quarter turns, are taken as sums of
+// two doubles, so that a position of 2^31 loses nothing (one double would leave
+// 10^-6 radians there); what is left of whole quarter turns, at most an eighth of
+// a turn, goes to fp32.
 //
 // Bound by memory: 266,426 x 8 x 32 bf16 53 us (5.2 TB/s; 67 with one chunk of a
 // thread in flight instead of four), 120,000 x 8 x 16 fp16 13 us.
@@ -36,6 +37,17 @@ struct RotArgs {
     float sign;                   // -1: the rotation back
 };
 
+// Whole quarter turns (mod 4) of the angle pos * freq, and what is left of one.
+__device__ __forceinline__ int quarter_turns(int pos, float freq, float& rest) {
+#pragma clang fp contract(off)        // the products below are rounded where they stand
+    constexpr double TURN = 0x1.45f306dc9c883p-1, TURN_LEFT = -0x1.6b01ec5417056p-55;   // 2 / pi, what rounding left of it
+    const double a = pos, b = freq, t = a * b, t2 = fma(a, b, -t);
+    const double q = t * TURN, q2 = fma(t, TURN, -q) + (t * TURN_LEFT + t2 * TURN);
+    const double whole = rint(q), left = (q - whole) + q2, more = rint(left);
+    rest = float(left - more);
+    return (int(whole - 4.0 * floor(whole * 0.25)) + int(more)) & 3;
+}
+
 constexpr float COPIED = 2.f;     // the cosine of a pair past the axes in the table
 
 // Those pairs of a chunk as they were in x.
@@ -62,11 +74,9 @@ __global__ __launch_bounds__(RT) void k_rotary(const RotArgs p) {
         if (j < p.pairs) {
             int axis = 0;
             while (j >= p.end[axis]) ++axis;
-            const double quarters = double(p.pos[(row0 + r) * p.ldp + axis]) * double(p.freq[j]) * 0.63661977236758134308;
-            const double whole = rint(quarters);
-            float s, c;
-            sincospif(float(quarters - whole) * 0.5f, &s, &c);
-            const int k = int(int64_t(whole) & 3);
+            float s, c, rest;
+            const int k = quarter_turns(p.pos[(row0 + r) * p.ldp + axis], p.freq[j], rest);
+            sincospif(rest * 0.5f, &s, &c);
             cs.x = k == 0 ? c : k == 1 ? -s : k == 2 ? -c : s;
             cs.y = (k == 0 ? s : k == 1 ? c : k == 2 ? -s : -c) * p.sign;
         }
