@@ -565,7 +565,10 @@ spc_status spc_linear_recurrence_step(spc_dtype dtype, const void* gate, const v
  * ----------------------------------------------------------------------------
  * Attention block: what a block of attention over voxels puts next to the
  * convolutions, by the row operators' conventions (samples, rounding, results
- * that repeat, asynchronous calls of kernels only).
+ * that repeat, asynchronous calls of kernels only).  An output that shares a
+ * byte with an input or another output, where it is not said to be allowed, is
+ * refused (columns of one wider tensor share none); scratch and fp32 statistics
+ * are not compared.
  */
 
 /* Host only.  Workspace bytes of spc_layer_norm_bwd. */
@@ -578,8 +581,8 @@ spc_status spc_layer_norm_workspace(int64_t n, int32_t C, size_t* bytes);
  *   rstd = (var + eps)^-1/2
  * x, residual, y, total [n, C], C a positive multiple of 16 up to 4096; gamma,
  * beta fp32 [C] (NULL: 1 and 0).  residual and total come together: total
- * receives u (NULL both: u is x).  y may be x, total may be x or residual,
- * but y and total are not the same rows.
+ * receives u (NULL both: u is x).  y and total may each be x or residual, but
+ * not both the same.
  * stats fp32 [n, 2] receives mean and rstd.
  */
 spc_status spc_layer_norm_fwd(spc_dtype dtype, const void* x, const void* residual, int64_t n, int32_t C,

@@ -93,6 +93,11 @@ spc_status check_rows(spc_dtype dtype, const spc_attention* a, const Side& s, in
     return SPC_OK;
 }
 
+Rows rows_of(spc_dtype dtype, const spc_attention* a, const Side& s, int64_t n) {
+    const int64_t e = dtype_size(dtype);
+    return Rows{s.p, n, int64_t(s.heads) * a->head_dim * e, s.ld * e, s.name};
+}
+
 }  // namespace
 }  // namespace attn
 }  // namespace spc
@@ -118,12 +123,19 @@ extern "C" spc_status spc_attention_fwd(spc_dtype dtype, const spc_attention* a,
     spc_status st = check_sizes(dtype, a, w);
     if (st == SPC_OK) st = check_call(dtype, a, ws, w.fwd, ws_bytes, p);
     if (st != SPC_OK) return st;
-    for (const Side& s : {Side{q, ldq, a->heads, "q"}, Side{out, ldo, a->heads, "out"}})
-        if ((st = check_rows(dtype, a, s, a->n_q)) != SPC_OK) return st;
-    for (const Side& s : {Side{k, ldk, a->kv_heads, "k"}, Side{v, ldv, a->kv_heads, "v"}})
-        if ((st = check_rows(dtype, a, s, a->n_kv)) != SPC_OK) return st;
+    const Side sq{q, ldq, a->heads, "q"}, sk{k, ldk, a->kv_heads, "k"}, sv{v, ldv, a->kv_heads, "v"}, so{out, ldo, a->heads, "out"},
+        sr{dtype == SPC_F32 ? nullptr : rest, int64_t(a->heads) * a->head_dim, a->heads, "rest"};
+    for (const Side* s : {&sq, &so})
+        if ((st = check_rows(dtype, a, *s, a->n_q)) != SPC_OK) return st;
+    for (const Side* s : {&sk, &sv})
+        if ((st = check_rows(dtype, a, *s, a->n_kv)) != SPC_OK) return st;
     if ((stats && !aligned16(stats)) || (rest && !aligned16(rest))) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     if (a->n_q == 0) return SPC_OK;
+    const Rows ro = rows_of(dtype, a, so, a->n_q), rr = rows_of(dtype, a, sr, a->n_q);
+    for (const Rows* o : {&ro, &rr})
+        for (const Rows& in : {rows_of(dtype, a, sq, a->n_q), rows_of(dtype, a, sk, a->n_kv), rows_of(dtype, a, sv, a->n_kv)})
+            if ((st = check_overlap(*o, in)) != SPC_OK) return st;
+    if ((st = check_overlap(ro, rr)) != SPC_OK) return st;
     const int64_t e = dtype_size(dtype);
     p.q = static_cast<const char*>(q), p.k = static_cast<const char*>(k), p.v = static_cast<const char*>(v), p.out = static_cast<char*>(out);
     p.ldq = ldq * e, p.ldk = ldk * e, p.ldv = ldv * e, p.ldo = ldo * e;
@@ -147,14 +159,22 @@ extern "C" spc_status spc_attention_bwd(spc_dtype dtype, const spc_attention* a,
     spc_status st = check_sizes(dtype, a, w);
     if (st == SPC_OK) st = check_call(dtype, a, ws, w.bwd, ws_bytes, p);
     if (st != SPC_OK) return st;
-    for (const Side& s : {Side{dout, lddo, a->heads, "dout"}, Side{q, ldq, a->heads, "q"}, Side{out, ldo, a->heads, "out"},
-                          Side{dq, lddq, a->heads, "dq"}})
+    const Side queries[] = {{dout, lddo, a->heads, "dout"}, {q, ldq, a->heads, "q"}, {out, ldo, a->heads, "out"}, {dq, lddq, a->heads, "dq"}};
+    const Side keys[] = {{k, ldk, a->kv_heads, "k"}, {v, ldv, a->kv_heads, "v"}, {dk, lddk, a->kv_heads, "dk"}, {dv, lddv, a->kv_heads, "dv"}};
+    for (const Side& s : queries)
         if ((st = check_rows(dtype, a, s, a->n_q)) != SPC_OK) return st;
-    for (const Side& s : {Side{k, ldk, a->kv_heads, "k"}, Side{v, ldv, a->kv_heads, "v"}, Side{dk, lddk, a->kv_heads, "dk"},
-                          Side{dv, lddv, a->kv_heads, "dv"}})
+    for (const Side& s : keys)
         if ((st = check_rows(dtype, a, s, a->n_kv)) != SPC_OK) return st;
     if (a->n_q > 0 && !stats) return fail(SPC_ERR_ARG, "stats is NULL");
     if ((stats && !aligned16(stats)) || (rest && !aligned16(rest))) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    // the inputs, and the gradients behind them
+    const Side sr{dtype == SPC_F32 ? nullptr : rest, int64_t(a->heads) * a->head_dim, a->heads, "rest"};
+    const Rows all[] = {rows_of(dtype, a, queries[0], a->n_q), rows_of(dtype, a, queries[1], a->n_q), rows_of(dtype, a, queries[2], a->n_q),
+                        rows_of(dtype, a, keys[0], a->n_kv),   rows_of(dtype, a, keys[1], a->n_kv),   rows_of(dtype, a, sr, a->n_q),
+                        rows_of(dtype, a, queries[3], a->n_q), rows_of(dtype, a, keys[2], a->n_kv),   rows_of(dtype, a, keys[3], a->n_kv)};
+    for (int o = 6; o < 9; ++o)
+        for (int i = 0; i < o; ++i)
+            if ((st = check_overlap(all[o], all[i])) != SPC_OK) return st;
     const int64_t e = dtype_size(dtype);
     p.q = static_cast<const char*>(q), p.k = static_cast<const char*>(k), p.v = static_cast<const char*>(v);
     p.o = static_cast<const char*>(out), p.dout = static_cast<const char*>(dout);

@@ -258,6 +258,11 @@ spc_status check_sizes(int64_t n, int32_t C, LnCut& k) {
     return SPC_OK;
 }
 
+Rows dense(spc_dtype dtype, const void* p, int64_t n, int32_t C, const char* name) {
+    const int64_t w = int64_t(C) * dtype_size(dtype);
+    return Rows{p, n, w, w, name};
+}
+
 template <typename TT, int V>
 spc_status launch_fwd(const void* x, const void* res, int64_t n, int C, const LnCut& k, const float* gamma, const float* beta,
                       float eps, void* y, void* total, float2* stats, hipStream_t stream) {
@@ -334,15 +339,20 @@ extern "C" spc_status spc_layer_norm_fwd(spc_dtype dtype, const void* x, const v
     clear_error();
     LnCut k;
     if (dtype != SPC_F32 && dtype != SPC_F16 && dtype != SPC_BF16) return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
-    const spc_status st = check_sizes(n, C, k);
+    spc_status st = check_sizes(n, C, k);
     if (st != SPC_OK) return st;
     if (!(eps > 0.f)) return fail(SPC_ERR_ARG, "eps=%g must be positive", double(eps));
     if (!residual != !total) return fail(SPC_ERR_ARG, "residual and total: give both or neither");
-    if (total && total == y && n > 0) return fail(SPC_ERR_ARG, "y and total are the same rows");
     for (const void* q : {x, residual, (const void*)gamma, (const void*)beta, (const void*)y, (const void*)total, (const void*)stats})
         if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
     if (n == 0) return SPC_OK;
     if (!x || !y || !stats) return fail(SPC_ERR_ARG, "x, y or stats is NULL");
+    const Rows rx = dense(dtype, x, n, C, "x"), rr = dense(dtype, residual, n, C, "residual"), ry = dense(dtype, y, n, C, "y"),
+               rt = dense(dtype, total, n, C, "total");
+    for (const Rows* in : {&rx, &rr})
+        for (const Rows* o : {&ry, &rt})
+            if ((st = check_overlap(*o, *in, true)) != SPC_OK) return st;
+    if ((st = check_overlap(ry, rt)) != SPC_OK) return st;
     float2* so = reinterpret_cast<float2*>(stats);
     switch (dtype) {
         case SPC_F32: return dispatch_fwd<F32>(x, residual, n, C, k, gamma, beta, eps, y, total, so, stream);
@@ -358,7 +368,7 @@ extern "C" spc_status spc_layer_norm_bwd(spc_dtype dtype, const void* dout, cons
     clear_error();
     LnCut k;
     if (dtype != SPC_F32 && dtype != SPC_F16 && dtype != SPC_BF16) return fail(SPC_ERR_ARG, "unknown dtype %d", int(dtype));
-    const spc_status st = check_sizes(n, C, k);
+    spc_status st = check_sizes(n, C, k);
     if (st != SPC_OK) return st;
     for (const void* q : {dout, x, (const void*)gamma, (const void*)stats, dtotal, (const void*)dx, (const void*)dgamma, (const void*)dbeta, (const void*)ws})
         if (q && !aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
@@ -366,6 +376,11 @@ extern "C" spc_status spc_layer_norm_bwd(spc_dtype dtype, const void* dout, cons
     const size_t need = dgamma || dbeta ? k.bytes : 0;
     if (need && !ws) return fail(SPC_ERR_ARG, "ws is NULL");
     if (ws_bytes < need) return fail(SPC_ERR_WORKSPACE, "ws_bytes=%zu, need %zu", ws_bytes, need);
+    const Rows rx = dense(dtype, x, n, C, "x"), rd = dense(dtype, dout, n, C, "dout"), rt = dense(dtype, dtotal, n, C, "dtotal"),
+               ro = dense(dtype, dx, n, C, "dx");
+    for (const Rows* in : {&rd, &rt})
+        if ((st = check_overlap(ro, *in, true)) != SPC_OK) return st;
+    if ((st = check_overlap(ro, rx)) != SPC_OK) return st;
     const float2* si = reinterpret_cast<const float2*>(stats);
     float2* part = static_cast<float2*>(ws);
     switch (dtype) {

@@ -149,6 +149,8 @@ extern "C" spc_status spc_rotary(spc_dtype dtype, const void* x, int64_t ldx, in
     if (!x || !out || !pos || (sum && !freq)) return fail(SPC_ERR_ARG, "x, out, pos or freq is NULL");
     for (const void* q : {x, (const void*)out})
         if (!aligned16(q)) return fail(SPC_ERR_ARG, "device pointers must be 16-byte aligned");
+    const spc_status st = check_overlap(Rows{out, n, width * e, ldo * e, "out"}, Rows{x, n, width * e, ldx * e, "x"}, true);
+    if (st != SPC_OK) return st;
     // positions may be columns of the coordinates: aligned as their type
     for (const void* q : {(const void*)pos, (const void*)freq})
         if (reinterpret_cast<uintptr_t>(q) & 3u) return fail(SPC_ERR_ARG, "pos and freq must be aligned to 4 bytes");

@@ -115,6 +115,47 @@ struct Segs {
     }
 };
 
+// ------------------------------------------------- where tensors overlap
+
+// Rows of `width` bytes, `ld` bytes apart.
+struct Rows {
+    const void* p;
+    int64_t n, width, ld;
+    const char* name;
+};
+
+// Whether two tensors share a byte.  Columns of one wider tensor do not: rows of
+// the same stride are compared by their distance, others row by row (of the one
+// with fewer), where their ranges meet at all.
+inline bool overlap(Rows a, Rows b) {
+    if (!a.p || !b.p || a.n <= 0 || b.n <= 0 || a.width <= 0 || b.width <= 0) return false;
+    int64_t d = int64_t(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p));    // where b begins, from a
+    if (a.n > b.n) {
+        const Rows t = a;
+        a = b, b = t, d = -d;
+    }
+    if (d >= (a.n - 1) * a.ld + a.width || -d >= (b.n - 1) * b.ld + b.width) return false;
+    // One row of width w that begins `at` bytes past b's first: b's row j meets it iff -b.width < j ld - at < w.
+    auto meets = [&](int64_t at, int64_t w, int64_t lo, int64_t hi) {
+        const int64_t x = at - b.width + 1, q = x / b.ld, j = q + (x > q * b.ld ? 1 : 0);       // the first row past the left bound
+        const int64_t first = j > lo ? j : lo;
+        return first <= hi && first * b.ld - at < w;
+    };
+    // rows i of a and j of b lie (j - i) ld + d apart
+    if (a.ld == b.ld || a.n == 1) return meets(-d, a.width, 1 - a.n, b.n - 1);
+    for (int64_t i = 0; i < a.n; ++i)
+        if (meets(i * a.ld - d, a.width, 0, b.n - 1)) return true;
+    return false;
+}
+
+// Refuses an output that overlaps another tensor; with `same`, it may be that
+// tensor.
+inline spc_status check_overlap(const Rows& out, const Rows& other, bool same = false) {
+    if (same && out.p == other.p && (out.n <= 1 || out.ld == other.ld)) return SPC_OK;
+    if (overlap(out, other)) return fail(SPC_ERR_ARG, "%s and %s overlap", out.name, other.name);
+    return SPC_OK;
+}
+
 // ---------------------------------------------------------------- dropout
 
 // Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
