@@ -11,8 +11,9 @@
 // 10^-6 radians there); what is left of whole quarter turns, at most an eighth of
 // a turn, goes to fp32.
 //
-// Bound by memory: 266,426 x 8 x 32 bf16 53 us (5.2 TB/s; 67 with one chunk of a
-// thread in flight instead of four), 120,000 x 8 x 16 fp16 13 us.
+// Bound by memory: 266,426 x 8 x 32 bf16 63 us with inputs from memory (4.4 TB/s; 61
+// without the second doubles of the angles and the copies), 120,000 x 8 x 16 fp16 13 us.
+// Four chunks of a thread are in flight (one: 67 us where four took 53).
 #include "rows.h"
 
 namespace spc {
@@ -42,10 +43,10 @@ __device__ __forceinline__ int quarter_turns(int pos, float freq, float& rest) {
 #pragma clang fp contract(off)        // the products below are rounded where they stand
     constexpr double TURN = 0x1.45f306dc9c883p-1, TURN_LEFT = -0x1.6b01ec5417056p-55;   // 2 / pi, what rounding left of it
     const double a = pos, b = freq, t = a * b, t2 = fma(a, b, -t);
-    const double q = t * TURN, q2 = fma(t, TURN, -q) + (t * TURN_LEFT + t2 * TURN);
-    const double whole = rint(q), left = (q - whole) + q2, more = rint(left);
-    rest = float(left - more);
-    return (int(whole - 4.0 * floor(whole * 0.25)) + int(more)) & 3;
+    const double q = t * TURN, q2 = fma(t2, TURN, fma(t, TURN_LEFT, fma(t, TURN, -q)));
+    const double r = fma(-4.0, rint(q * 0.25), q) + q2, whole = rint(r);      // the fma is exact
+    rest = float(r - whole);
+    return int(whole) & 3;
 }
 
 constexpr float COPIED = 2.f;     // the cosine of a pair past the axes in the table
