@@ -1290,13 +1290,29 @@ inline unsigned set_grid(Args& p, int64_t slots, int splits, int rows_of_slot, b
 // wide that one wave's share of the staging would not fit its registers.
 constexpr int few_waves(int D) { return D <= 64 ? 1 : 2; }
 
+// Heads of every multiple of 16 up to 96 have kernels of their own width, in every
+// type: work, LDS and registers go with it.  Padded to 64 and 128 they took
+// (40,000 x 4 heads in windows of 1,024, training, us; then one causal sample of
+// 8,000 x 4):
+//         48 own, as 64        80 own, as 128       96 own, as 128
+//   fp32  1,729, 1,782         2,854, 3,937         2,858, 3,977
+//         1,590, 1,907         2,308, 4,450         2,518, 4,489
+//   bf16  309, 306             476, 737             672, 756
+//         416, 638             638, 860             651, 870
+// Heads of 112 have as many 32-row blocks as 128 and gain nothing: bf16 839 us in a
+// width of their own, 797 as 128; causal 936 and 885.
 #define ATTN_WIDTHS(name, nw, grid, p)                                                                                        \
     do {                                                                                                                      \
-        if (p.D <= 16) ATTN_WIDTH(name, 16, nw, grid, p);                                                                     \
-        else if (p.D <= 32) ATTN_WIDTH(name, 32, nw, grid, p);                                                                \
-        else if (TT::E == 4 && p.D <= 48) ATTN_WIDTH(name, (TT::E == 4 ? 48 : 64), nw, grid, p);                              \
-        else if (p.D <= 64) ATTN_WIDTH(name, 64, nw, grid, p);                                                                \
-        else ATTN_WIDTH(name, 128, (nw == 1 ? few_waves(128) : nw), grid, p);                                                 \
+        constexpr int NW = nw, NW2 = nw == 1 ? few_waves(128) : nw;                                                           \
+        switch (p.D / 16) {                                                                                                   \
+            case 1: ATTN_WIDTH(name, 16, NW, grid, p); break;                                                                 \
+            case 2: ATTN_WIDTH(name, 32, NW, grid, p); break;                                                                 \
+            case 3: ATTN_WIDTH(name, 48, NW, grid, p); break;                                                                 \
+            case 4: ATTN_WIDTH(name, 64, NW, grid, p); break;                                                                 \
+            case 5: ATTN_WIDTH(name, 80, NW2, grid, p); break;                                                                \
+            case 6: ATTN_WIDTH(name, 96, NW2, grid, p); break;                                                                \
+            default: ATTN_WIDTH(name, 128, NW2, grid, p);                                                                     \
+        }                                                                                                                     \
         SPC_LAUNCHED(#name);                                                                                                  \
     } while (0)
 
