@@ -562,11 +562,14 @@ struct KeyStage : Stage<TT, DP, BN, NT> {
 template <typename TT, int NW>
 constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
 
-// The forward's: heads of 128 have the registers for 2 where nothing is masked
-// (16,384 x 8 x 128: 1,226 us with 2, 1,297 with 1; causal 16,411 x 8 x 128
-// spills with 2: 1,150 us, 780 with 1).
+// The forward's: workgroups of four waves take 2 up to heads of 96, and of 128
+// where nothing is masked (one sample of 16,384 x 8 x 128: 1,270 us with 2, 1,311
+// with 1; windows of 1,024 on 100,000 x 2 x 128: 196 and 222; causal 16,411 x 8
+// over 2 x 128 spills with 2: 1,064 and 737; causal 30,000 x 8 x 96 in 20 ragged
+// samples: 471 and 603, without the mask 829 and 789; windows of 1,024 on 60,000 x
+// 4 x 80: 180 and 185, causal 136 and 173).
 template <typename TT, int DP, int NW, bool CAUSAL>
-constexpr int KT_FWD = DP <= 64 || (!CAUSAL && NW == 4) ? KT_OF<TT, NW> : 1;
+constexpr int KT_FWD = DP <= 64 || (NW == 4 && (DP <= 96 || !CAUSAL)) ? KT_OF<TT, NW> : 1;
 
 // Waves that a SIMD is to hold at least, which bounds the registers: the most
 // that costs no spills in the loops.
@@ -1268,10 +1271,14 @@ spc_status launch_bwd_bf16(const Args& p, const Cut& q, const Cut& k, hipStream_
 inline int64_t slots_of(int64_t rows, int64_t n_seg, int bm) { return rows / bm + n_seg + 1; }
 
 // Sets the grid of a walk; its workgroups.  A group is 1,024 rows of all heads
-// where there are many (windows of 1,024 on 266,426 x 4 x 32 bf16: forward 322
-// us, backward 784; 338 and 821 in groups of one slot), a slot where the work of
-// neighbours differs (causal: 16,411 x 8 x 128 took 1,872 us in eight
-// contiguous parts, 985 so) or there are few.
+// where there are many, a slot where the work of neighbours differs (causal) or
+// there are few.  Forward and backward in us, with groups of one slot, of 1,024
+// rows and of an eighth of the call: windows of 1,024 on 266,426 x 4 x 32 bf16 342 +
+// 900, 323 + 872 and 325 + 867, of 500 on 120,000 x 8 x 16 139 + 352, 138 + 351 and
+// 133 + 347, of 2,048 on 60,000 x 8 over 2 x 64 341 + 1,069, 341 + 1,068 and 339 +
+// 1,066; causal 16,411 x 8 over 2 x 128 forward 736 with one slot and 1,554 with
+// eighths, 8,000 x 4 over 2 x 64 fp32 407 + 1,377 and 583 + 1,467, 20 ragged samples
+// of 30,000 x 8 x 64 in all 378 + 1,000 and 789 + 1,957.
 inline unsigned set_grid(Args& p, int64_t slots, int splits, int rows_of_slot, bool even) {
     p.slots = int32_t(slots), p.splits = splits;
     p.total = unsigned(slots * splits * p.hk);

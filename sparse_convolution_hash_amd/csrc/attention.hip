@@ -17,11 +17,14 @@ Cut cut_of(int64_t rows, int64_t other, int64_t n_seg, int heads, int D) {
     c.nw = rows >= 64 * n_seg && slots_of(rows, n_seg, 128) * heads >= 512 ? 4 : few_waves(D);
     c.slots = slots_of(rows, n_seg, 32 * c.nw);
     // Few workgroups: the other side is split too, and the parts are joined by
-    // a second launch, to 4 waves a SIMD (5,003 x 6 x 48 fp32 in 23 ragged samples,
-    // trained: 538 us, 1,560 when only the mean length counted).  A split is
-    // worth at least 128 rows of the longest sample, which may be several
-    // times the mean (only the device knows); samples of fewer than 128 rows
-    // in the mean are not split.
+    // a second launch, to 4 waves a SIMD.  A split is worth at least 128 rows of the
+    // longest sample, which may be several times the mean (only the device knows):
+    // taken as 8 times.  Forward + backward in us where it is taken as the mean, 3, 8
+    // and 32 times that, ragged causal samples: 5,003 x 6 over 2 x 48 fp32 in 23 of
+    // them 163 + 392, 91 + 275, 91 + 274, 91 + 275; 8,000 x 2 x 32 bf16 in 50 40 +
+    // 123, 24 + 67, 23 + 60, 23 + 60; even ones pay a little for parts that are
+    // empty: 2,000 x 4 x 32 fp32 in 4 36 + 98, 38 + 104, 36 + 104, 36 + 104.  Samples
+    // of fewer than 128 rows in the mean are not split.
     const int64_t want = 4096 / c.nw, have = (rows / (32 * c.nw) + n_seg) * heads;
     const int64_t mean = other / n_seg, longest = mean < 128 ? 0 : 8 * mean < other ? 8 * mean : other, most = longest / 128;
     c.splits = int32_t(have * 2 > want || most < 2 ? 1 : (want / have < most ? want / have : most));
