@@ -27,6 +27,8 @@
 // us, one wave a SIMD, the matrix unit busy for half of its cycles.
 #pragma once
 
+#include <type_traits>
+
 #include "rows.h"
 
 namespace spc {
@@ -210,20 +212,15 @@ struct Second {
         }
     };
 
-    static __device__ __forceinline__ void add(f32x16_t (&acc)[T::NB], const char* x, int row0, const Packed& w, int lane) {
-#pragma unroll
-        for (int t = 0; t < STEPS; ++t)
-#pragma unroll
-            for (int db = 0; db < T::NB; ++db) acc[db] = step(left(x, row0, t, db, lane), w.b[t], acc[db]);
-    }
-
-    // w as the sum of two numbers of the type: for dq of narrow heads, whose
-    // matrix unit has room for it.  ds sums to 0 over a row, so its rounding
-    // counts for more than that of p: windows of 1,024 on 266,426 x 4 x 32 bf16
-    // trained in 1,170 us with a relative error of dq below 2.4e-3, in 1,095 us
-    // with 2.6e-3 where ds is rounded once.
+    // As sums of two numbers of the type, for twice the products: for dq of
+    // narrow heads, whose matrix unit has room for it (ds sums to 0 over a row, so
+    // its rounding counts for more than that of p: windows of 1,024 on 266,426 x 4
+    // x 32 bf16 trained in 1,170 us with a relative error of dq below 2.4e-3, in
+    // 1,095 us with 2.6e-3 where ds is rounded once), and for the forward's p in
+    // workgroups of few waves.
     struct Two {
         Packed hi, lo;
+        __device__ __forceinline__ Two() {}
         __device__ __forceinline__ explicit Two(const f32x16_t& w) : hi(w) {
 #pragma unroll
             for (int t = 0; t < STEPS; ++t) {
@@ -238,15 +235,17 @@ struct Second {
         }
     };
 
-    static __device__ __forceinline__ void add(f32x16_t (&acc)[T::NB], const char* x, int row0, const Two& w, int lane) {
+    static __device__ __forceinline__ f32x16_t step(const u32x4& a, const Packed& w, int t, f32x16_t c) { return step(a, w.b[t], c); }
+    static __device__ __forceinline__ f32x16_t step(const u32x4& a, const Two& w, int t, f32x16_t c) {
+        return step(a, w.lo.b[t], step(a, w.hi.b[t], c));
+    }
+
+    template <typename W>
+    static __device__ __forceinline__ void add(f32x16_t (&acc)[T::NB], const char* x, int row0, const W& w, int lane) {
 #pragma unroll
         for (int t = 0; t < STEPS; ++t)
 #pragma unroll
-            for (int db = 0; db < T::NB; ++db) {
-                const u32x4 a = left(x, row0, t, db, lane);
-                acc[db] = step(a, w.hi.b[t], acc[db]);
-                acc[db] = step(a, w.lo.b[t], acc[db]);
-            }
+            for (int db = 0; db < T::NB; ++db) acc[db] = step(left(x, row0, t, db, lane), w, t, acc[db]);
     }
 
     // The finite elements of a left operand, the others 0.
@@ -280,8 +279,8 @@ struct Second {
     // values are summed.  With OTHERS (w are probabilities, positive), an
     // infinite or NaN value reaches the columns that see its row: counted
     // apart.  Without, it has made w itself NaN in those columns.
-    template <bool OTHERS>
-    static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const Packed& w,
+    template <bool OTHERS, typename W>
+    static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const W& w,
                                                       uint32_t vis, int lane) {
         bool odd = false;
 #pragma unroll
@@ -290,7 +289,7 @@ struct Second {
             for (int db = 0; db < T::NB; ++db) {
                 const u32x4 a = left(x, row0, t, db, lane), f = finite(a);
                 if constexpr (OTHERS) odd |= a.x != f.x || a.y != f.y || a.z != f.z || a.w != f.w;
-                acc[db] = step(f, w.b[t], acc[db]);
+                acc[db] = step(f, w, t, acc[db]);
             }
         }
         if constexpr (OTHERS) {
@@ -313,17 +312,6 @@ struct Second {
                     for (int r = 0; r < 16; ++r) acc[db][r] += n[r] > 0.f ? v : 0.f;
                 }
         }
-    }
-    // Without OTHERS, for w as two numbers.
-    static __device__ __forceinline__ void add_masked(f32x16_t (&acc)[T::NB], const char* x, int row0, const Two& w, int lane) {
-#pragma unroll
-        for (int t = 0; t < STEPS; ++t)
-#pragma unroll
-            for (int db = 0; db < T::NB; ++db) {
-                const u32x4 a = finite(left(x, row0, t, db, lane));
-                acc[db] = step(a, w.hi.b[t], acc[db]);
-                acc[db] = step(a, w.lo.b[t], acc[db]);
-            }
     }
 };
 
@@ -434,6 +422,16 @@ constexpr bool SPLIT = TT::id == SPC_BF16 && DP <= 32;
 // Where dq takes ds as two numbers of the type.
 template <typename TT, int DP>
 constexpr bool TWO = TT::E == 8 && DP <= 32;
+
+// Where the forward takes p as two numbers: in workgroups of few waves, whose
+// calls do not fill the chip, so that the second products cost next to nothing
+// (a query to each of 4 samples of 266,426 x 8 x 16 bf16 in all: 47.4 us with a
+// relative error of out of 1.6e-3, the rounding of out itself, 47.3 with 2.4e-3;
+// one causal sample of 300 x 6 over 2 x 64 18.3 and 17.6).  Full ones would pay:
+// windows of 1,024 on 266,426 x 4 x 32 413 us, 315 with one number; causal 16,411 x
+// 8 over 2 x 128 883 and 729.
+template <typename TT, int NW>
+constexpr bool TWO_P = TT::E == 8 && NW < 4;
 
 // f times c as f + lo (lo has entries where the product is split).
 template <typename TT, int DP>
@@ -664,7 +662,8 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
             // one may still need the second round.
             using X = Second<TT, DP>;
             f32x16_t s[KT];
-            typename X::Packed w[KT];
+            using WP = std::conditional_t<TWO_P<TT, NW>, typename X::Two, typename X::Packed>;
+            WP w[KT];
             float sum = 0.f;
             bool fresh = __any(m == -INFINITY && l == 0.f), last = false;    // (l is NaN where a query is)
             for (;;) {
@@ -724,7 +723,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                         s[u][r] = exp2_(SP ? s[u][r] : fmaf(s[u][r], p.c, -base));
                         part[r & 3] += s[u][r];
                     }
-                    w[u] = typename X::Packed(s[u]);
+                    w[u] = WP(s[u]);
                 }
                 sum = (part[0] + part[1]) + (part[2] + part[3]);
                 if (last || !__any(sum > LAZY<TT>)) break;
@@ -980,15 +979,9 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
                     for (int r = 0; r < 16; ++r) s[r] = (vis >> bit_of(r)) & 1u ? s[r] : 0.f;
                 }
                 if constexpr (RANGED<TT>) into_range(s, acc, f);
-                if constexpr (TWO<TT, DP>) {
-                    const typename X::Two w(s);
-                    if (CAUSAL && edge) X::add_masked(acc, kt, 32 * u, w, lane);
-                    else X::add(acc, kt, 32 * u, w, lane);
-                } else {
-                    const typename X::Packed w(s);
-                    if (CAUSAL && edge) X::template add_masked<false>(acc, kt, 32 * u, w, vis, lane);
-                    else X::add(acc, kt, 32 * u, w, lane);
-                }
+                const std::conditional_t<TWO<TT, DP>, typename X::Two, typename X::Packed> w(s);
+                if (CAUSAL && edge) X::template add_masked<false>(acc, kt, 32 * u, w, vis, lane);
+                else X::add(acc, kt, 32 * u, w, lane);
             }
         }
         if (more) stage.put(lds[buf ^ 1][0], lds[buf ^ 1][1]);
