@@ -653,8 +653,8 @@ spc_status spc_attention_workspace(spc_dtype dtype, const spc_attention* a, size
  * head_dim; each with its row stride in elements, a multiple of 16 bytes (one
  * product may give q, k and v side by side).  Pairs that a mask hides enter no
  * sum, whatever their rows hold.  Products are fp32; the probabilities are
- * rounded to the dtype for the second product (calls that do not fill the chip:
- * to two numbers of the dtype), their sum is not.
+ * rounded to the dtype for the second product (up to 32 rows a sample against
+ * many keys: to two numbers of the dtype), their sum is not.
  * stats fp32 [heads, n_q, 2] (NULL ok) receives (m, l) for the backward: the
  * log of the row's sum of exp(s) is (m + log2 l) ln 2; l = 0: no key is seen.
  * rest (NULL ok; 16-bit dtypes, unused for fp32), dense [n_q, heads, head_dim]

@@ -216,8 +216,8 @@ struct Second {
     // narrow heads, whose matrix unit has room for it (ds sums to 0 over a row, so
     // its rounding counts for more than that of p: windows of 1,024 on 266,426 x 4
     // x 32 bf16 trained in 1,170 us with a relative error of dq below 2.4e-3, in
-    // 1,095 us with 2.6e-3 where ds is rounded once), and for the forward's p in
-    // workgroups of few waves.
+    // 1,095 us with 2.6e-3 where ds is rounded once), and for the forward's p
+    // where few rows meet many keys.
     struct Two {
         Packed hi, lo;
         __device__ __forceinline__ Two() {}
@@ -421,17 +421,7 @@ constexpr bool SPLIT = TT::id == SPC_BF16 && DP <= 32;
 
 // Where dq takes ds as two numbers of the type.
 template <typename TT, int DP>
-constexpr bool TWO = TT::E == 8 && DP <= 32;
-
-// Where the forward takes p as two numbers: in workgroups of few waves, whose
-// calls do not fill the chip, so that the second products cost next to nothing
-// (a query to each of 4 samples of 266,426 x 8 x 16 bf16 in all: 47.4 us with a
-// relative error of out of 1.6e-3, the rounding of out itself, 47.3 with 2.4e-3;
-// one causal sample of 300 x 6 over 2 x 64 18.3 and 17.6).  Full ones would pay:
-// windows of 1,024 on 266,426 x 4 x 32 413 us, 315 with one number; causal 16,411 x
-// 8 over 2 x 128 883 and 729.
-template <typename TT, int NW>
-constexpr bool TWO_P = TT::E == 8 && NW < 4;
+constexpr bool TWO_DS = TT::E == 8 && DP <= 32;
 
 // f times c as f + lo (lo has entries where the product is split).
 template <typename TT, int DP>
@@ -592,8 +582,9 @@ constexpr float BWD_UP = TT::id == SPC_F16 ? 15.f : 0.f;
 template <typename TT>
 constexpr float LAZY = TT::id == SPC_F16 ? 32768.f : 1024.f;
 
-template <typename TT, int DP, int NW, bool CAUSAL>
-__global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_fwd(const Args p) {
+// TWO: p as two numbers of the type.
+template <typename TT, int DP, int NW, bool CAUSAL, bool TWO>
+__device__ __forceinline__ void attn_fwd(const Args& p) {
     constexpr int BM = 32 * NW, KT = KT_FWD<TT, DP, NW, CAUSAL>, BN = 32 * KT, NT = 64 * NW;
     constexpr bool SP = SPLIT<TT, DP>;
     using T = Tile<TT, DP>;
@@ -662,8 +653,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
             // one may still need the second round.
             using X = Second<TT, DP>;
             f32x16_t s[KT];
-            using WP = std::conditional_t<TWO_P<TT, NW>, typename X::Two, typename X::Packed>;
-            WP w[KT];
+            std::conditional_t<TWO, typename X::Two, typename X::Packed> w[KT];
             float sum = 0.f;
             bool fresh = __any(m == -INFINITY && l == 0.f), last = false;    // (l is NaN where a query is)
             for (;;) {
@@ -723,7 +713,7 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
                         s[u][r] = exp2_(SP ? s[u][r] : fmaf(s[u][r], p.c, -base));
                         part[r & 3] += s[u][r];
                     }
-                    w[u] = WP(s[u]);
+                    w[u] = std::remove_reference_t<decltype(w[u])>(s[u]);
                 }
                 sum = (part[0] + part[1]) + (part[2] + part[3]);
                 if (last || !__any(sum > LAZY<TT>)) break;
@@ -770,6 +760,24 @@ __global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_f
             if (TT::E == 8 && p.rest) put4<TT>(rest + d * T::ES, left_of<TT>(o));
         }
     if (p.stats && h == 0) p.stats[id] = float2{m, l};
+}
+
+template <typename TT, int DP, int NW, bool CAUSAL>
+__global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL>)) void k_attn_fwd(const Args p) {
+    attn_fwd<TT, DP, NW, CAUSAL, false>(p);
+}
+
+// For few rows against many keys: where a sample's rows fit one wave and its keys
+// are split, a staged tile meets one tile of products and the walk waits for
+// memory, so that p as two numbers costs nothing (a query to each of 4 samples of
+// 266,426 x 8 x 16 bf16 in all: 47.5 us with a relative error of out of 1.6e-3, the
+// rounding of out itself, and 47.3 with 2.4e-3).  Others would pay: causal 8,000 x
+// 4 over 2 x 48 124 us, 109 with one number; windows of 1,024 on 266,426 x 4 x 32
+// 413 and 315; causal 16,411 x 8 over 2 x 128 883 and 729.
+// One wave less to a SIMD where that leaves the registers for it.
+template <typename TT, int DP, int NW, bool CAUSAL>
+__global__ __launch_bounds__(64 * NW, (FWD_WAVES<TT, DP, CAUSAL> - (DP == (CAUSAL ? 128 : 32)))) void k_attn_fwd_few(const Args p) {
+    attn_fwd<TT, DP, NW, CAUSAL, true>(p);
 }
 
 // How the joining kernels lay a workgroup of 256 threads out over rows, splits
@@ -979,7 +987,7 @@ __global__ __launch_bounds__(64 * NW, (BWD_WAVES<TT, DP>)) void k_attn_dq(const 
                     for (int r = 0; r < 16; ++r) s[r] = (vis >> bit_of(r)) & 1u ? s[r] : 0.f;
                 }
                 if constexpr (RANGED<TT>) into_range(s, acc, f);
-                const std::conditional_t<TWO<TT, DP>, typename X::Two, typename X::Packed> w(s);
+                const std::conditional_t<TWO_DS<TT, DP>, typename X::Two, typename X::Packed> w(s);
                 if (CAUSAL && edge) X::template add_masked<false>(acc, kt, 32 * u, w, vis, lane);
                 else X::add(acc, kt, 32 * u, w, lane);
             }
@@ -1319,8 +1327,10 @@ constexpr int few_waves(int D) { return D <= 64 ? 1 : 2; }
 template <typename TT>
 spc_status launch_fwd(Args p, const Cut& c, hipStream_t stream) {
     const unsigned grid = set_grid(p, c.slots, c.splits, 32 * c.nw, !p.causal);
+    const bool few = TT::E == 8 && c.splits > 1 && int64_t(p.qs.n) * p.g <= int64_t(32) * p.qs.n_seg;
     if (c.nw == 4) ATTN_WIDTHS(k_attn_fwd, 4, grid, p);
-    else ATTN_WIDTHS(k_attn_fwd, 1, grid, p);
+    else if (!few) ATTN_WIDTHS(k_attn_fwd, 1, grid, p);
+    else if constexpr (TT::E == 8) ATTN_WIDTHS(k_attn_fwd_few, 1, grid, p);
     if (c.splits > 1) {
         const int splits = p.splits;
         const unsigned rows = set_grid(p, slots_of(int64_t(p.qs.n) * p.g, p.qs.n_seg, 32), 1, 32, false);

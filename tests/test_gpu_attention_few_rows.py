@@ -1,6 +1,6 @@
-"""Calls of few rows (pooling, single queries, small samples) take their
-probabilities as two numbers of a 16-bit type: what is left of their rounding is
-the square of half a step, and the result is as near as its own rounding."""
+"""Few rows against many keys (pooling, single queries) take their probabilities
+as two numbers of a 16-bit type: what is left of their rounding is the square of
+half a step, and the result is as near as its own rounding."""
 
 import pytest
 import torch
@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("D", [16, 48, 64, 96, 128])
 @pytest.mark.parametrize("causal", [False, True])
-@pytest.mark.parametrize("lq,lk,H,Hk", [([1, 1, 2], [400, 700, 3], 2, 2), ([1], [3000], 4, 1), ([70, 33, 1], None, 2, 1)])
+@pytest.mark.parametrize("lq,lk,H,Hk", [([1, 1, 2], [400, 700, 3], 2, 2), ([1], [3000], 4, 1), ([7] * 5, [900, 0, 1500, 1, 640], 2, 1)])
 def test_probabilities_in_two_numbers(lq, lk, H, Hk, causal, D, dtype):
     c = Case(lq, lk, H, Hk, D, dtype, seed=71, causal=causal, gain=2.0)
     h = half_step(dtype)
