@@ -583,7 +583,8 @@ spc_status spc_layer_norm_workspace(int64_t n, int32_t C, size_t* bytes);
  * beta fp32 [C] (NULL: 1 and 0).  residual and total come together: total
  * receives u (NULL both: u is x).  y and total may each be x or residual, but
  * not both the same.
- * stats fp32 [n, 2] receives mean and rstd.
+ * stats fp32 [n, 2] receives mean and rstd.  Sums are fp32: rows whose squares
+ * pass its range (differences from the mean around 10^19) come out as beta.
  */
 spc_status spc_layer_norm_fwd(spc_dtype dtype, const void* x, const void* residual, int64_t n, int32_t C,
                               const float* gamma, const float* beta, float eps, void* y, void* total, float* stats,

@@ -1186,8 +1186,9 @@ def attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg_ptr: Op
     slice of one product.  seg_ptr and order lay out the queries and, where
     neither kv_ptr nor kv_order is given, the keys; scale defaults to D^-1/2.
     Returns ``(out [Nq, heads, D], stats or None)``; stats are for
-    attention_bwd: ``(ml fp32 [heads, Nq, 2], rest)``, the rows' maxima and sums
-    and what rounding left of out ([Nq, heads, D]; None for fp32)."""
+    attention_bwd: ``(ml fp32 [heads, Nq, 2], rest)``, from which the log of each
+    row's sum follows, and what rounding left of out ([Nq, heads, D], fp16's
+    times 2^11; None for fp32)."""
     a, (ldq, ldk, ldv), (need, _) = _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale)
     dev, (n, H, D) = q.device, q.shape
     if out is None:

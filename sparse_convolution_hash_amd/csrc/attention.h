@@ -18,12 +18,12 @@
 // (ds_read_b64_tr_b16) gives it so from rows as they were stored.
 //
 // Windows of 1,024 on 266,426 x 4 x 32 bf16, where the exponentials and the
-// packing keep the vector unit busy and not memory: forward 344 us (140 GFLOP
-// in the two products, 410 TFLOP/s), k_attn_dq 490 (three products, 210 GFLOP),
-// k_attn_dkv 515 (four, 279 GFLOP).  Causal 16,411 x 8 heads
-// over 2 x 128 bf16: forward 716 us, 552 GFLOP, 770 TFLOP/s (matrix
+// packing keep the vector unit busy and not memory: forward 315 us (140 GFLOP
+// in the two products, 440 TFLOP/s), backward 850 (k_attn_dq three products, 210
+// GFLOP, k_attn_dkv four, 279 GFLOP; 353, 487 and 526 us under the tracer).  Causal
+// 16,411 x 8 heads over 2 x 128 bf16: forward 720 us, 552 GFLOP, 770 TFLOP/s (matrix
 // unit busy for 32% of its cycles, vector unit for 45%, two waves a SIMD to cover
-// each other's waits).  fp32, 5,003 x 6 x 48 ragged and causal: 128, 151 and 244
+// each other's waits).  fp32, 5,003 x 6 x 48 ragged and causal: 129, 154 and 246
 // us, one wave a SIMD, the matrix unit busy for half of its cycles.
 #pragma once
 
@@ -131,10 +131,13 @@ __device__ __forceinline__ f32x4_t left_of(f32x4_t v) {
 constexpr int bit_of(int r) { return 8 * (r / 4) + r % 4; }
 
 // Tile of `rows` rows of DP elements in LDS, in 16-byte chunks.  The chunk
-// number is XORed with bits of the row so that both reads are free of bank
-// conflicts: 8 consecutive rows of one chunk (row reads), and two chunks of 4
-// consecutive rows (transposing reads).  M chunks a row: rows repeat their
-// banks every 1, 2 or 4 rows when M is a multiple of 8, 4 or 2.
+// number is XORed with bits of the row so that what one access takes lies spread
+// over 128 bytes of banks: 8 consecutive rows of one chunk (row reads), and two
+// chunks of 4 consecutive rows (transposing reads).  M chunks a row: rows repeat
+// their banks every 1, 2 or 4 rows when M is a multiple of 8, 4 or 2.  The banks
+// are 256 bytes wide, and the counters still show conflicts, of LDS's busy cycles
+// 40% in the forward of 128 elements, 25, 33 and 17% in the forward, k_attn_dq and
+// k_attn_dkv of 32 (bf16), 11 to 19% for fp32.
 template <typename TT, int DP>
 struct Tile {
     static constexpr int ES = sizeof(typename TT::storage);
@@ -559,8 +562,10 @@ constexpr int KT_OF = TT::E == 8 && NW > 1 ? 2 : 1;
 template <typename TT, int DP, int NW, bool CAUSAL>
 constexpr int KT_FWD = DP <= 64 || (NW == 4 && (DP <= 96 || !CAUSAL)) ? KT_OF<TT, NW> : 1;
 
-// Waves that a SIMD is to hold at least, which bounds the registers: the most
-// that costs no spills in the loops.
+// Waves that a SIMD is to hold at least, which bounds the registers.  Most kernels
+// fit without spills; k_attn_dkv of causal 16-bit heads, and their forward of 128 in
+// two waves, keep up to 40 registers in scratch, fp32's k_attn_dkv of heads from 96
+// on up to 185 at one wave already.
 template <typename TT, int DP, bool CAUSAL>
 constexpr int FWD_WAVES = TT::E == 4 ? 1 : DP <= 32 ? 4 - CAUSAL : DP <= 64 ? 3 - CAUSAL : 2;
 template <typename TT, int DP>
@@ -860,7 +865,7 @@ __device__ __forceinline__ float2 from_stats(float2 ml) {
 // begins where any ds that counts passes TOP, and is cut so that the largest
 // comes to 2^10 whenever one does: what is below half of fp16's smallest number
 // then is below 2^-35 of the column's largest, and nothing passes fp16's largest.
-// 266,426 x 4 x 32 in windows of 1,024: backward 893 us, 835 at ds' own size, which
+// 266,426 x 4 x 32 in windows of 1,024: backward 906 us, 835 at ds' own size, which
 // had an error of 2% in dq at gradients of 10^-4 and infinite rows at 10^4.
 template <typename TT>
 constexpr bool RANGED = TT::id == SPC_F16;
@@ -1305,8 +1310,8 @@ constexpr int few_waves(int D) { return D <= 64 ? 1 : 2; }
 //         48 own, as 64        80 own, as 128       96 own, as 128
 //   fp32  1,729, 1,782         2,854, 3,937         2,858, 3,977
 //         1,590, 1,907         2,308, 4,450         2,518, 4,489
-//   bf16  309, 306             476, 737             672, 756
-//         416, 638             638, 860             651, 870
+//   bf16  309, 306             472, 737             662, 756
+//         421, 638             641, 860             646, 870
 // Heads of 112 have as many 32-row blocks as 128 and gain nothing: bf16 839 us in a
 // width of their own, 797 as 128; causal 936 and 885.
 #define ATTN_WIDTHS(name, nw, grid, p)                                                                                        \

@@ -4,11 +4,11 @@
 //   du = rstd (w - mean(w) - h mean(w h)) (+ dtotal),
 //   dgamma = sum dy h, dbeta = sum dy over the rows.
 // A row lies in the registers of 2 to 64 lanes, eight channels a lane and
-// step, so every tensor is read once; what bounds it is memory.  266,426 x 128
-// bf16: forward with the residual 50 us (5.4 TB/s), backward onto a later
-// gradient 61 us (4.5 TB/s), whose rows wait for three sums each; the sums of
-// the workgroups' parts 4.5 us.  Small calls are their launches: 2,000 x 16
-// fp32 3.0 us.
+// step, so every tensor is read once; what bounds large calls is memory.  266,426 x
+// 128 bf16: forward with the residual 50 us (5.4 TB/s), backward onto a later
+// gradient 62 us (4.4 TB/s), whose rows wait for three sums each; the sums of
+// the workgroups' parts 4.7 us.  Small calls are their launches: 2,000 x 16
+// fp32 3.6 us.
 //
 // Differences are taken from the rounded mean and their own mean, near 0, is
 // taken out again: a row far from 0 next to its spread keeps the precision

@@ -129,22 +129,23 @@ struct Rows {
 // with fewer), where their ranges meet at all.
 inline bool overlap(Rows a, Rows b) {
     if (!a.p || !b.p || a.n <= 0 || b.n <= 0 || a.width <= 0 || b.width <= 0) return false;
-    int64_t d = int64_t(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p));    // where b begins, from a
+    using I = __int128;                // rows times strides may pass 64 bits
+    I d = I(reinterpret_cast<intptr_t>(b.p)) - reinterpret_cast<intptr_t>(a.p);                 // where b begins, from a
     if (a.n > b.n) {
         const Rows t = a;
         a = b, b = t, d = -d;
     }
-    if (d >= (a.n - 1) * a.ld + a.width || -d >= (b.n - 1) * b.ld + b.width) return false;
+    if (d >= I(a.n - 1) * a.ld + a.width || -d >= I(b.n - 1) * b.ld + b.width) return false;
     // One row of width w that begins `at` bytes past b's first: b's row j meets it iff -b.width < j ld - at < w.
-    auto meets = [&](int64_t at, int64_t w, int64_t lo, int64_t hi) {
-        const int64_t x = at - b.width + 1, q = x / b.ld, j = q + (x > q * b.ld ? 1 : 0);       // the first row past the left bound
-        const int64_t first = j > lo ? j : lo;
+    auto meets = [&](I at, int64_t w, int64_t lo, int64_t hi) {
+        const I x = at - b.width + 1, q = x / b.ld, j = q + (x > q * b.ld ? 1 : 0);             // the first row past the left bound
+        const I first = j > lo ? j : I(lo);
         return first <= hi && first * b.ld - at < w;
     };
     // rows i of a and j of b lie (j - i) ld + d apart
     if (a.ld == b.ld || a.n == 1) return meets(-d, a.width, 1 - a.n, b.n - 1);
     for (int64_t i = 0; i < a.n; ++i)
-        if (meets(i * a.ld - d, a.width, 0, b.n - 1)) return true;
+        if (meets(I(i) * a.ld - d, a.width, 0, b.n - 1)) return true;
     return false;
 }
 
