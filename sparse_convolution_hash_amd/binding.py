@@ -1128,9 +1128,9 @@ def rotary(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, pairs: Sequen
         raise ValueError(f"freq must be [{sum(pairs)}], got {tuple(freq.shape)}")
     if out is None:
         out = x.new_empty((n, H, D))
-    elif out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
-        raise ValueError("out may be x itself, not another view of it")
     ldo = _heads(out, "out", x.dtype, dev, x.shape)
+    if out is not x and n and out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+        raise ValueError("out may be x itself, not another view of it")
     st = _call(dev, lib().spc_rotary, _DTYPES[x.dtype], _ptr(x), ldx, n, H, D, _ptr(pos),
                pos.stride(0) if n > 1 else len(pairs), len(pairs), _axis_pairs(pairs), _ptr(freq), 1 if inverse else 0,
                _ptr(out), ldo)
@@ -1172,7 +1172,7 @@ def _attn_checks(q, k, v, seg_ptr, order, kv_ptr, kv_order, causal, scale):
         _need_like(order, "order", torch.int32, dev, (n,))
     if kv_order is not None:
         _need_like(kv_order, "kv_order", torch.int32, dev, (m,))
-    a = _AttnArg(n, m, n_seg, H, Hk, D, 1 if causal else 0, D ** -0.5 if scale is None else scale, _ptr(seg_ptr), _ptr(kv_ptr),
+    a = _AttnArg(n, m, n_seg, H, Hk, D, 1 if causal else 0, max(D, 1) ** -0.5 if scale is None else scale, _ptr(seg_ptr), _ptr(kv_ptr),
                  _ptr(order), _ptr(kv_order))
     return a, (ldq, ldk, ldv), attention_workspace(q.dtype, n, m, n_seg, H, Hk, D)
 
